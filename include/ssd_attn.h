@@ -1,0 +1,85 @@
+/*
+ * ssd_attn.h - C ABI of libssd: the attention layer of a hybrid stack, as HIP kernels for MI355X
+ * (gfx950).  Hybrid stacks put one attention layer after every few SSD layers (llms.blog "State Space
+ * Models and Mamba", on hybrid architectures), over the same tokens; these entry points run on the
+ * token axes, offsets, element types and streams of ssd.h, whose conventions for ownership, errors and
+ * checks hold here too (ssd_strerror describes the codes).
+ *
+ * The operator, for query i and key j of one sequence (a document of a packed batch), head h with
+ * key/value head h / (H / Hk):
+ *
+ *     z_ij = scale q_i . k_j
+ *     s_ij = (softcap > 0 ? softcap tanh(z_ij / softcap) : z_ij) + bias_h(pk_j - pq_i)
+ *     p_ij = exp(s_ij - lse_i),   lse_i = log sum_j exp s_ij over the keys visible to i
+ *     y_i  = sum_j p_ij v_j
+ *
+ * Positions: pk_j = j, pq_i = i + Lk - Lq within the sequence: its Lq queries are the last Lq of its Lk
+ * positions.  Visible: every key of the same sequence, and with `causal` only those with pk_j <= pq_i,
+ * or pk_j < prefix of the sequence when prefixes are given.  A query that sees no key has y = 0,
+ * lse = -infinity, and no part in any gradient.
+ *
+ * Bias, one of: none; slopes [H], bias = -slopes[h] |pk_j - pq_i|; a learned table [num_buckets, H],
+ * bias = table[bucket(pk_j - pq_i), h].  Buckets: bidirectional = 0: n = num_buckets, distance
+ * d = max(pq_i - pk_j, 0).  bidirectional = 1: n = num_buckets / 2, d = |pk_j - pq_i|, and keys behind the
+ * query (pk_j > pq_i) take the table's second half.  With e = n / 2 and f = n - e: d < e has bucket d; d >= e
+ * has bucket e + k for the largest k < f with (max_distance / e)^k <= (d / e)^f, that is distances spaced
+ * evenly in the logarithm up to max_distance and one bucket beyond; the borders are found in whole
+ * numbers, not in rounded logarithms.
+ *
+ * Layouts: q, y [total_q, H, D], k, v [total_k, Hk, D]; one token's heads are dense, and q, k, v may be
+ * views of wider rows (a fused projection's output) with a token stride of their own.  Everything else
+ * is dense.  slopes, table and lse are fp32 whatever the dtype.
+ * Non-finite inputs propagate to the outputs of their own sequence and head, and of a key/value head's
+ * whole group in gradients; inputs outside every sequence reach no output.
+ */
+#ifndef SSD_ATTN_H
+#define SSD_ATTN_H
+
+#include "ssd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    int64_t nseq;          /* sequences, >= 0 */
+    int64_t total_q;       /* tokens of the packed query axis, 0 .. 2^31 - 1025 */
+    int64_t total_k;       /* tokens of the packed key axis, 0 .. 2^31 - 1025 */
+    int64_t nheads;        /* H >= 1 */
+    int64_t nkvheads;      /* Hk >= 1, divides H */
+    int64_t headdim;       /* D: 32, 64 or 128 */
+    int64_t q_stride;      /* elements from one token of q to the next; 0: dense (H D).  A multiple of */
+    int64_t k_stride;      /* 16 bytes, at least the token's own elements.  Likewise k, v (Hk D) */
+    int64_t v_stride;
+    float scale;           /* of q . k: finite */
+    float softcap;         /* 0: none; else positive and finite */
+    int32_t dtype;         /* ssd_dtype of q, k, v, y and their gradients */
+    int32_t causal;        /* 0 or 1 */
+    int32_t num_buckets;   /* with a table: 2 .. 64 (bidirectional: 4 .. 128, even), otherwise ignored */
+    int32_t max_distance;  /* with a table: above half a direction's buckets, at most 1024 */
+    int32_t bidirectional; /* with a table: 0 or 1 */
+} ssd_attn_dims;
+
+/*
+ * Attention forward (for training and prompts).
+ *   cu_seqlens_q  DEVICE memory, nseq + 1 int64 offsets into the query axis, non-decreasing; sequence s is
+ *                 tokens cu[s] .. cu[s+1] - 1.  NULL: nseq sequences of total_q / nseq tokens (total_q
+ *                 must be a multiple).  The host does not read it; the kernels clamp it into the axis, so
+ *                 malformed offsets give wrong outputs but no access outside the tensors.
+ *   cu_seqlens_k  the same for the key axis.  NULL: cu_seqlens_q (total_k must equal total_q), or equal
+ *                 sequences when that is NULL too; given without cu_seqlens_q: SSD_ERR_INVALID.
+ *   prefix        DEVICE memory, nseq int64 prefix lengths in keys, or NULL; needs causal = 1.
+ *   slopes, table at most one is given.
+ *   lse           [total_q, H] output, natural logarithm, or NULL (the backward pass needs it).
+ * Tokens of no sequence are never written.  No workspace; one launch.
+ */
+int ssd_attn_forward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q,
+                     const int64_t* cu_seqlens_k, const int64_t* prefix, const void* q,
+                     const void* k, const void* v, const float* slopes, const float* table,
+                     void* y, float* lse, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSD_ATTN_H */

@@ -23,6 +23,8 @@ The functions carry the names of the C entry points declared in ``include/ssd.h`
   ssd_forward_noalloc(x, log_a, B, C, D=None, chunk=..., init_state=None, y=None,
                       final_state=None, stream=None) -> (y, final_state)
   ssd_strerror(code) -> str
+and, from ``include/ssd_attn.h`` (``attention.py``), the attention layer of a hybrid stack:
+  ssd_attn_forward(q, k, v, cu_seqlens=None, ..., lse=None) -> (y, lse)
 """
 from __future__ import annotations
 
@@ -37,6 +39,7 @@ __all__ = ["SSDError", "Dims", "library_path", "load_library", "dims_for",
            "ssd_step_dt", "ssd_backward_workspace_bytes", "ssd_backward", "ssd_backward_profiled",
            "ssd_backward_dt_workspace_bytes", "ssd_backward_dt",
            "ssd_forward_noalloc", "ssd_noalloc_scratch_bytes", "ssd_strerror",
+           "ssd_attn_forward",
            "SSD_F32", "SSD_BF16", "SSD_DECAY_SCALAR", "SSD_DECAY_DIAG"]
 
 SSD_F32, SSD_BF16 = 0, 1
@@ -133,6 +136,7 @@ def load_library():
         lib.ssd_forward_noalloc.restype = i32
         lib.ssd_strerror.argtypes = [i32]
         lib.ssd_strerror.restype = ctypes.c_char_p
+        attention.declare(lib)
         _LIB = lib
     return _LIB
 
@@ -753,3 +757,7 @@ def ssd_step(state, x_t, log_a_t, B_t, C_t, D=None, y_t=None, stream=None):
     if rc != SSD_OK:
         raise SSDError(rc, "ssd_step")
     return y_t
+
+
+from . import attention  # noqa: E402  (its functions use the helpers above)
+from .attention import ssd_attn_forward  # noqa: E402

@@ -1,0 +1,137 @@
+"""Python binding of the attention layer (``include/ssd_attn.h``): argument marshalling only.
+
+Tensors of a batched call are q [B,Lq,H,D], k, v [B,Lk,Hk,D]; of a packed call (``cu_seqlens`` given)
+q [Tq,H,D], k, v [Tk,Hk,D].  One token's heads are dense; q, k and v may be views of wider rows, such as
+a fused projection's output.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import SSD_OK, SSDError, _DTYPE_CODE, _check, _on_stream, _ptr, _stream_handle, load_library
+
+
+class AttnDims(ctypes.Structure):
+    """Mirror of ``ssd_attn_dims``."""
+    _fields_ = [("nseq", ctypes.c_int64), ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("nkvheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("num_buckets", ctypes.c_int32),
+                ("max_distance", ctypes.c_int32), ("bidirectional", ctypes.c_int32)]
+
+
+def declare(lib):
+    vp, i32 = ctypes.c_void_p, ctypes.c_int
+    dp = ctypes.POINTER(AttnDims)
+    lib.ssd_attn_forward.argtypes = [dp] + [vp] * 11
+    lib.ssd_attn_forward.restype = i32
+
+
+def _token_stride(t, name, dim, dtype, device):
+    """Elements from one token to the next of a tensor [..., tokens, heads, D] whose tokens are dense."""
+    if t.dim() != dim:
+        raise ValueError("%s must have %d dimensions, got shape %s" % (name, dim, tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.numel() == 0:
+        return 0
+    if (t.shape[-1] > 1 and t.stride(-1) != 1) or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
+        raise ValueError("%s must have dense heads (strides %s)" % (name, t.stride()))
+    dense = t.shape[-2] * t.shape[-1]
+    step = t.stride(-3) if t.shape[-3] > 1 else dense
+    if dim == 4 and t.shape[0] > 1:
+        if t.shape[1] == 1:
+            step = t.stride(0)
+        elif t.stride(0) != t.shape[1] * step:
+            raise ValueError("%s must have its sequences one after another (strides %s)" % (name, t.stride()))
+    if step < dense:
+        raise ValueError("%s has overlapping tokens (strides %s)" % (name, t.stride()))
+    return step
+
+
+def _offsets(t, name, device, n=None):
+    if t is None:
+        return
+    if t.dtype != torch.int64 or t.dim() != 1 or t.device != device or not t.is_contiguous() or (n is None and t.numel() < 1):
+        raise ValueError("%s must be a contiguous 1-D int64 tensor on q's device" % name)
+    if n is not None and t.numel() != n:
+        raise ValueError("%s has %d values, expected %d" % (name, t.numel(), n))
+
+
+def _bias_args(slopes, table, H, device):
+    if slopes is not None and table is not None:
+        raise ValueError("slopes and table are two forms of the bias: give at most one")
+    _check(slopes, "slopes", (H,), torch.float32, device)
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must be [num_buckets, H]")
+        _check(table, "table", (table.shape[0], H), torch.float32, device)
+    return 0 if table is None else table.shape[0]
+
+
+def _dims(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, softcap, slopes, table, max_distance, bidirectional, prefix):
+    """ssd_attn_dims of a call, its arguments checked."""
+    dev, dim = q.device, 4 if cu_seqlens is None else 3
+    if q.dtype not in _DTYPE_CODE:
+        raise TypeError("q must be float32 or bfloat16, got %s" % q.dtype)
+    strides = [_token_stride(t, n, dim, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
+    H, D = q.shape[-2:]
+    Hk = k.shape[-2]
+    if tuple(v.shape) != tuple(k.shape) or k.shape[-1] != D or (dim == 4 and k.shape[0] != q.shape[0]):
+        raise ValueError("k and v must be alike and fit q: q %s, k %s, v %s" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    if cu_seqlens is None:
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        nseq, tq, tk = q.shape[0], q.shape[0] * q.shape[1], k.shape[0] * k.shape[1]
+    else:
+        _offsets(cu_seqlens, "cu_seqlens", dev)
+        nseq, tq, tk = cu_seqlens.numel() - 1, q.shape[0], k.shape[0]
+        _offsets(cu_seqlens_k, "cu_seqlens_k", dev, nseq + 1)
+        if cu_seqlens_k is None and tq != tk:
+            raise ValueError("q and k have different token counts: give cu_seqlens_k")
+    _offsets(prefix, "prefix", dev, nseq)
+    if prefix is not None and not causal:
+        raise ValueError("a prefix needs causal=True")
+    buckets = _bias_args(slopes, table, H, dev)
+    return AttnDims(nseq, tq, tk, H, Hk, D, *strides, D ** -0.5 if scale is None else float(scale), float(softcap),
+                    _DTYPE_CODE[q.dtype], int(bool(causal)), buckets, int(max_distance), int(bool(bidirectional)))
+
+
+def ssd_attn_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal: bool = True, scale=None,
+                     softcap: float = 0.0, slopes=None, table=None, max_distance: int = 128,
+                     bidirectional: bool = False, prefix=None, y=None, lse=None, stream=None):
+    """Run ``ssd_attn_forward``: softmax attention of every query over the visible keys of its own
+    sequence, with scores capped to ``softcap`` * tanh and a bias by distance (``slopes`` [H] or a learned
+    ``table`` [num_buckets, H]).
+
+    ``cu_seqlens``: int64 offsets [nseq + 1] on the GPU of a packed batch (``cu_seqlens_k`` where the keys
+    have offsets of their own; a sequence's queries are then its last positions).  ``scale`` defaults to
+    D ** -0.5.  ``prefix``: int64 [nseq], keys before it are visible to their whole sequence.  ``y`` is
+    allocated when not given; ``lse`` may be a tensor [..., H] fp32 to write, True to allocate one, or
+    None/False to skip it.  Tokens of no sequence are not written.  Returns (y, lse)."""
+    dims = _dims(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, softcap, slopes, table, max_distance, bidirectional,
+                 prefix)
+    dev = q.device
+    if y is None:
+        y = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _check(y, "y", q.shape, q.dtype, dev)
+    if lse is True:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    _check(lse, "lse", q.shape[:-1], torch.float32, dev)
+    _on_stream(stream, y, lse)
+    with torch.cuda.device(dev):
+        rc = load_library().ssd_attn_forward(
+            ctypes.byref(dims), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _ptr(prefix), _ptr(q), _ptr(k), _ptr(v),
+            _ptr(slopes), _ptr(table), _ptr(y), _ptr(lse), _stream_handle(stream, dev))
+    if rc != SSD_OK:
+        raise SSDError(rc, "ssd_attn_forward")
+    return y, lse

@@ -20,7 +20,9 @@ DEVICE_FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
                 "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-Wall", "-Wno-unused-result"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall"]
-DEVICE_SOURCES = ["ssd_kernels.hip", "ssd_fast.hip", "ssd_diag.hip", "ssd_bwd.hip", "ssd_noalloc.hip"]
+DEVICE_SOURCES = ["ssd_kernels.hip", "ssd_fast.hip", "ssd_diag.hip", "ssd_bwd.hip", "ssd_noalloc.hip",
+                  "ssd_attn.hip"]
+HOST_SOURCES = ["ssd_api.cpp", "ssd_attn_api.cpp"]
 
 
 def _run(cmd):
@@ -44,13 +46,15 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         cmds.append([HIPCC, *DEVICE_FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
-    a_obj = os.path.join(BUILD_DIR, "ssd_api.o")
-    cmds.append([HIPCC, *HOST_FLAGS, *inc, "-c", os.path.join(CSRC, "ssd_api.cpp"), "-o", a_obj])
+    for src in HOST_SOURCES:
+        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+        cmds.append([HIPCC, *HOST_FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", obj])
+        objs.append(obj)
     jobs = max(1, min(len(cmds), len(os.sched_getaffinity(0))))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
         logs = list(pool.map(_run, cmds))
     tmp = LIBRARY + ".tmp%d" % os.getpid()
-    logs.append(_run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, *objs, a_obj, "-o", tmp]))
+    logs.append(_run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, *objs, "-o", tmp]))
     os.replace(tmp, LIBRARY)
     if verbose:
         for log in logs:

@@ -1,0 +1,168 @@
+// C ABI of the attention operators (declared in include/ssd_attn.h): argument validation, workspace
+// sizing and dispatch to the kernels.  Every check runs before the first HIP call.
+#include "ssd_attn.h"
+
+#include <cmath>
+#include <vector>
+
+#include <hip/hip_runtime.h>
+
+#include "ssd_attn_launch.h"
+
+namespace {
+
+// one token axis: in-sequence positions, and positions one tile past an end, are 32-bit in the kernels
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1025;
+constexpr int64_t kMaxHeads = 1 << 16;
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// A whole number of any size (little-endian 32-bit limbs), so that bucket borders are compared without
+// rounding.
+struct Whole {
+    std::vector<uint32_t> limb{1};
+    void times(uint32_t f) {
+        uint64_t carry = 0;
+        for (uint32_t& x : limb) {
+            carry += (uint64_t)x * f;
+            x = (uint32_t)carry;
+            carry >>= 32;
+        }
+        if (carry) limb.push_back((uint32_t)carry);
+    }
+    void times_power(uint32_t f, int n) {
+        while (n-- > 0) times(f);
+    }
+    bool at_least(const Whole& o) const {
+        if (limb.size() != o.limb.size()) return limb.size() > o.limb.size();
+        for (size_t i = limb.size(); i-- > 0;)
+            if (limb[i] != o.limb[i]) return limb[i] > o.limb[i];
+        return true;
+    }
+};
+
+// Is bucket e + k reached at distance d, (d / e)^f >= (m / e)^k, that is d^f e^k >= m^k e^f?
+bool reached(int d, int e, int f, int m, int k) {
+    Whole a, b;
+    a.times_power((uint32_t)d, f);
+    a.times_power((uint32_t)e, k);
+    b.times_power((uint32_t)m, k);
+    b.times_power((uint32_t)e, f);
+    return a.at_least(b);
+}
+
+// The distances at which a direction's bucket goes up by one: e - 1 of them one apart, then f.
+int make_buckets(ssd::AttnBuckets& out, int num_buckets, int max_distance, int both) {
+    if (both != 0 && both != 1) return SSD_ERR_INVALID;
+    const int n = both ? num_buckets / 2 : num_buckets;
+    if (num_buckets < (both ? 4 : 2) || (both && num_buckets % 2 != 0) || n > ssd::kMaxBorders) return SSD_ERR_INVALID;
+    const int e = n / 2, f = n - e;
+    if (max_distance <= e) return SSD_ERR_INVALID;
+    if (max_distance > ssd::kMaxDistance) return SSD_ERR_UNSUPPORTED;
+    out.total = num_buckets;
+    out.both = both;
+    out.max_distance = max_distance;
+    out.nborders = n - 1;
+    int at = 0;
+    for (int d = 1; d < e; ++d) out.borders[at++] = d;
+    for (int k = 0; k < f; ++k) {
+        // the smallest d with d >= e (m / e)^(k / f): from the power where it is clearly between two
+        // whole numbers, by the exact comparison where it is next to one
+        const double x = e * std::pow((double)max_distance / e, (double)k / f);
+        int d = (int)std::ceil(x);
+        const int near = (int)std::llround(x);
+        if (std::fabs(x - near) < 1e-9 * x) d = reached(near, e, f, max_distance, k) ? near : near + 1;
+        out.borders[at++] = d;
+    }
+    return SSD_OK;
+}
+
+int check_shape(int64_t H, int64_t Hk, int64_t D, int32_t dtype) {
+    if (H < 1 || Hk < 1 || H > kMaxHeads || H % Hk != 0 || D < 1) return SSD_ERR_INVALID;
+    if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_INVALID;
+    if (D != 32 && D != 64 && D != 128) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+int check_stride(int64_t given, int64_t dense, int64_t elem, int64_t& out) {
+    if (given == 0) {
+        out = dense;
+        return SSD_OK;
+    }
+    if (given < dense || given > ((int64_t)1 << 40)) return SSD_ERR_INVALID;
+    if (given * elem % 16 != 0) return SSD_ERR_ALIGN;
+    out = given;
+    return SSD_OK;
+}
+
+// Everything that forward and backward check alike; fills the launch parameters they share.
+int fill(const ssd_attn_dims* d, const int64_t* cu_q, const int64_t* cu_k, const int64_t* prefix, const void* q,
+         const void* k, const void* v, const float* slopes, const float* table, ssd::AttnParams& p, int& bias) {
+    if (!d) return SSD_ERR_INVALID;
+    int rc = check_shape(d->nheads, d->nkvheads, d->headdim, d->dtype);
+    if (rc != SSD_OK) return rc;
+    if (d->nseq < 0 || d->nseq > kMaxTokens || d->total_q < 0 || d->total_q > kMaxTokens || d->total_k < 0 ||
+        d->total_k > kMaxTokens)
+        return SSD_ERR_INVALID;
+    if ((d->causal != 0 && d->causal != 1) || !std::isfinite(d->scale) || !std::isfinite(d->softcap) || d->softcap < 0.f)
+        return SSD_ERR_INVALID;
+    if (d->nseq > 0 && !cu_q && (d->total_q % d->nseq != 0 || cu_k || d->total_k % d->nseq != 0)) return SSD_ERR_INVALID;
+    if (cu_q && !cu_k && d->total_k != d->total_q) return SSD_ERR_INVALID;
+    if ((prefix && !d->causal) || (slopes && table)) return SSD_ERR_INVALID;
+    // workgroups of a launch are counted in 32 bits
+    if ((d->total_q / 128 + d->total_k / 128 + 2 * d->nseq + 2) * d->nheads >= ((int64_t)1 << 31)) return SSD_ERR_UNSUPPORTED;
+    const int64_t elem = d->dtype == SSD_BF16 ? 2 : 4;
+    if ((rc = check_stride(d->q_stride, d->nheads * d->headdim, elem, p.q_stride)) != SSD_OK) return rc;
+    if ((rc = check_stride(d->k_stride, d->nkvheads * d->headdim, elem, p.k_stride)) != SSD_OK) return rc;
+    if ((rc = check_stride(d->v_stride, d->nkvheads * d->headdim, elem, p.v_stride)) != SSD_OK) return rc;
+    bias = table ? ssd::kBiasBuckets : slopes ? ssd::kBiasSlopes : ssd::kBiasNone;
+    if (table && (rc = make_buckets(p.bk, d->num_buckets, d->max_distance, d->bidirectional)) != SSD_OK) return rc;
+    if (d->nseq > 0 && ((d->total_q > 0 && !q) || (d->total_k > 0 && (!k || !v)))) return SSD_ERR_INVALID;
+    const void* wide[] = {q, k, v, slopes, table};
+    for (const void* x : wide)
+        if (x && !aligned(x, 16)) return SSD_ERR_ALIGN;
+    const void* offsets[] = {cu_q, cu_k, prefix};
+    for (const void* x : offsets)
+        if (x && !aligned(x, 8)) return SSD_ERR_ALIGN;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.slopes = slopes;
+    p.table = table;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k ? cu_k : cu_q;
+    p.prefix = prefix;
+    p.nseq = d->nseq;
+    p.total_q = d->total_q;
+    p.total_k = d->total_k;
+    p.H = (int)d->nheads;
+    p.Hk = (int)d->nkvheads;
+    p.causal = d->causal;
+    p.scale = d->scale;
+    p.cap = d->softcap;
+    return SSD_OK;
+}
+
+int code(int rc) { return rc == 0 ? SSD_OK : rc == -2 ? SSD_ERR_UNSUPPORTED : SSD_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+int ssd_attn_forward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, const int64_t* cu_seqlens_k,
+                     const int64_t* prefix, const void* q, const void* k, const void* v, const float* slopes,
+                     const float* table, void* y, float* lse, void* stream) {
+    ssd::AttnParams p{};
+    int bias = 0;
+    const int rc = fill(dims, cu_seqlens_q, cu_seqlens_k, prefix, q, k, v, slopes, table, p, bias);
+    if (rc != SSD_OK) return rc;
+    const bool work = p.nseq > 0 && p.total_q > 0;
+    if (work && !y) return SSD_ERR_INVALID;
+    if ((y && !aligned(y, 16)) || (lse && !aligned(lse, 16))) return SSD_ERR_ALIGN;
+    if (!work) return SSD_OK;
+    p.y = y;
+    p.lse = lse;
+    return code(ssd::launch_attn_forward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

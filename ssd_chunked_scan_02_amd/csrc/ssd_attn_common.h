@@ -1,0 +1,246 @@
+// Device helpers shared by the attention kernels: 32x32 MFMA tiles of either element type, the LDS
+// tile layout they read, sequence lookup on the packed axes, and the bucket table.  gfx950 only.
+//
+// Every product here is arranged so that one operand's second index (a query in the forward and
+// query-gradient kernels, a key in the key-gradient kernel) is the MFMA column, lane % 32: the
+// softmax statistics of that index are then one number per lane, and the accumulator registers of
+// a score tile are, without any exchange between lanes, the operand of the next product that
+// contracts over its rows.  Accumulator register r of lane half h holds row (r % 4) + 8 (r / 4) +
+// 4 h; the LDS reads of the other operand take their rows in the same order.
+#pragma once
+
+#include "ssd_attn_launch.h"
+#include "ssd_common.h"
+
+namespace ssd {
+namespace attn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef short v8i16 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// start of a running maximum (log2 units): below any finite score, and finite, so that a row that
+// has seen nothing but masked scores (minus infinity) takes exp2(-inf) = 0 and not a NaN
+constexpr float kNoMax = -1e30f;
+constexpr int kBM = 128;  // rows of a workgroup's own tile: 4 waves of 32
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// One operand fragment is 16 bytes a lane: kK contraction steps over both lane halves.
+template <typename T> struct Op;
+template <> struct Op<__bf16> {
+    using Frag = bf16x8;
+    static constexpr int kE = 8, kK = 16, kKT = 64;  // kKT: rows of a streamed LDS tile
+    static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // accumulator rows kK * kk ... of a 32-row tile as an operand, rounded once to bf16: the
+    // matrix unit's operand type (products and sums stay fp32)
+    static __device__ __forceinline__ Frag pack(const f32x16& v, int kk) {
+        Frag f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (__bf16)v[8 * kk + j];
+        return f;
+    }
+};
+template <> struct Op<float> {
+    using Frag = f32x4;
+    static constexpr int kE = 4, kK = 8, kKT = 32;
+    static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Frag pack(const f32x16& v, int kk) {
+        return Frag{v[4 * kk], v[4 * kk + 1], v[4 * kk + 2], v[4 * kk + 3]};
+    }
+};
+
+// Row-major tile [rows][D] in LDS, in 16-byte chunks, chunk c of a row stored at c ^ swz(row): the
+// eight rows that one pass of a 16-byte read touches, and the four rows of a transposing read, then
+// lie in different banks without padding.
+template <typename T, int D> struct Tile {
+    static constexpr int kE = Op<T>::kE;
+    static constexpr int CH = D / kE;
+    static constexpr int RB = D * (int)sizeof(T);
+    static constexpr int RPB = RB >= 256 ? 1 : 256 / RB;
+    static constexpr int MASK = CH / 2 - 1 < 7 ? CH / 2 - 1 : 7;
+    static constexpr int kRows = Op<T>::kKT;
+    static constexpr int kElems = kRows * D;
+    static constexpr int kLoads = kRows * CH / kThreads;  // 16-byte chunks a thread stages
+    static_assert(kRows * CH % kThreads == 0, "every thread stages whole chunks");
+    static __device__ __forceinline__ int swz(int row) { return 2 * ((row / RPB) & MASK); }
+    static __device__ __forceinline__ int at(int row, int c) { return (row * CH + (c ^ swz(row))) * kE; }
+
+    // operand whose index is a row (lane % 32 of row0 ..), contracting over columns kK * t ..
+    static __device__ __forceinline__ typename Op<T>::Frag rows(const T* s, int row0, int t, int lane) {
+        const uint4 v = ld16(s + at(row0 + lane % 32, 2 * t + lane / 32));
+        return __builtin_bit_cast(typename Op<T>::Frag, v);
+    }
+    // operand whose index is a column (lane % 32 of col0 ..), contracting over rows row0 + kK * kk ..
+    // in the row order of an accumulator (see the top of this file)
+    static __device__ __forceinline__ typename Op<T>::Frag cols(const T* s, int row0, int kk, int col0, int lane);
+
+    // global -> registers: rows first .. of a [tokens][stride] tensor, rows past `last` read as `last`
+    // (a copy of a real row, whose weight is zero)
+    static __device__ __forceinline__ void load(uint4 (&buf)[kLoads], const T* g, int64_t stride, int first, int last) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int idx = (int)threadIdx.x + kThreads * i;
+            const int row = min(first + idx / CH, last);
+            buf[i] = ld16(g + (int64_t)row * stride + (idx % CH) * kE);
+        }
+    }
+    static __device__ __forceinline__ void store(T* s, const uint4 (&buf)[kLoads]) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int idx = (int)threadIdx.x + kThreads * i;
+            st16(s + at(idx / CH, idx % CH), buf[i]);
+        }
+    }
+};
+
+template <typename T, int D>
+__device__ __forceinline__ typename Op<T>::Frag Tile<T, D>::cols(const T* s, int row0, int kk, int col0, int lane) {
+    const int h = lane / 32;
+    if constexpr (sizeof(T) == 2) {
+        // ds_read_b64_tr_b16: a 16-lane group whose lane 4 r + q points at row r, columns 4 q .. 4 q + 3
+        // returns column i of those four rows in its lane i
+        const int r = (lane % 16) / 4, q = lane % 4;
+        const int col = col0 + 16 * ((lane / 16) % 2) + 4 * q;
+        const int row = row0 + 16 * kk + 4 * h + r;
+        const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(s + at(row, col / 8) + col % 8));
+        const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(s + at(row + 8, col / 8) + col % 8));
+        const v8i16 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8, v);
+    } else {
+        const int col = col0 + lane % 32, row = row0 + 8 * kk + 4 * h;
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = s[at(row + i, col / 4) + col % 4];
+        return v;
+    }
+}
+
+// Row of accumulator register r in the lower lane half (the upper half: + 4).
+__device__ __forceinline__ constexpr int acc_row(int r) { return (r % 4) + 8 * (r / 4); }
+
+// The other lane half's value.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, kWave); }
+
+// A sequence of the packed axes and one tile of its queries or keys.
+struct Span {
+    int64_t q0, k0;  // first query and key row
+    int lq, lk;      // their numbers
+    int tile;        // tile of the axis the slots count; negative: the slot is empty
+    int seq;
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// Offsets as a call gave them, clamped into the axis, so that no offsets lead outside a tensor.
+__device__ __forceinline__ void span_of(const int64_t* cu, int64_t total, int64_t nseq, int64_t s, int64_t& first, int& len) {
+    if (!cu) {
+        const int64_t each = total / nseq;
+        first = s * each;
+        len = (int)each;
+        return;
+    }
+    const int64_t a = clamp64(cu[s], 0, total), b = clamp64(cu[s + 1], a, total);
+    first = a;
+    len = (int)(b - a);
+}
+
+// Sequence and tile of a slot.  Sequence s owns the slots from floor(cu[s] / kBM) + s on, one more than
+// its whole tiles at most, so that a workgroup finds its work from the offsets alone, with no list made
+// on the way: a search 64 sequences wide (one step for 64 sequences, two for 4096).
+__device__ __forceinline__ int slot_sequence(const int64_t* cu, int64_t total, int64_t nseq, int slot) {
+    const int lane = threadIdx.x % kWave;
+    int64_t lo = 0, n = nseq;  // the last s in [lo, lo + n) with start(s) <= slot
+    while (n > 1) {
+        const int64_t step = (n + kWave - 1) / kWave;
+        const int64_t s = lo + step * lane;
+        const bool le = s < lo + n && clamp64(cu[s], 0, total) / kBM + s <= slot;
+        const int cnt = __popcll(__ballot(le));
+        const int64_t at = cnt > 0 ? step * (cnt - 1) : 0;
+        lo += at;
+        n = n - at < step ? n - at : step;
+    }
+    return (int)lo;
+}
+
+// (by_keys: the slots count tiles of the key axis)
+__device__ __forceinline__ Span find_span(const AttnParams& p, int slot, bool by_keys) {
+    const int64_t* cu = by_keys ? p.cu_k : p.cu_q;
+    const int64_t total = by_keys ? p.total_k : p.total_q;
+    Span sp;
+    int s, tile;
+    if (!cu) {
+        const int per = (int)((total / p.nseq + kBM - 1) / kBM);
+        s = slot / per;
+        tile = slot % per;
+    } else {
+        s = __builtin_amdgcn_readfirstlane(slot_sequence(cu, total, p.nseq, slot));
+        tile = slot - (int)(clamp64(cu[s], 0, total) / kBM + s);
+    }
+    sp.seq = s;
+    span_of(p.cu_q, p.total_q, p.nseq, s, sp.q0, sp.lq);
+    span_of(p.cu_k, p.total_k, p.nseq, s, sp.k0, sp.lk);
+    const int len = by_keys ? sp.lk : sp.lq;
+    sp.tile = tile >= 0 && (int64_t)tile * kBM < len ? tile : -1;
+    return sp;
+}
+
+// Slots of an axis: its whole tiles, and one more for each sequence.
+inline int64_t slots_of(const int64_t* cu, int64_t total, int64_t nseq) {
+    return cu ? total / kBM + nseq : nseq * ((total / nseq + kBM - 1) / kBM);
+}
+
+// Workgroup -> (slot, head).  Heads run fastest, the slots from the last (under a causal mask the
+// longest) to the first.  Workgroups reach the 8 XCDs in turn, so with 8 or more heads an XCD keeps a
+// run of neighbouring heads, which share keys and values in its L2.
+__device__ __forceinline__ void work_item(int64_t id, int slots, int H, int& slot, int& head) {
+    const int x = (int)(id % H);
+    slot = slots - 1 - (int)(id / H);
+    head = H % 8 == 0 ? (x % 8) * (H / 8) + x / 8 : x;
+}
+
+// Bucket of a relative position (key - query).
+__device__ __forceinline__ int bucket_of(const AttnBuckets& b, int rel) {
+    const int d = b.both ? abs(rel) : (rel < 0 ? -rel : 0);
+    int lo = 0, hi = b.nborders;  // borders at most d
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (b.borders[mid] <= d) lo = mid + 1; else hi = mid;
+    }
+    return lo + (b.both && rel > 0 ? b.nborders + 1 : 0);
+}
+
+// The head's bias, in log2 units, of relative positions -max_distance .. max_distance.
+__device__ __forceinline__ void fill_bias(float* lut, const AttnParams& p, int head) {
+    const int m = p.bk.max_distance;
+    for (int i = threadIdx.x; i <= 2 * m; i += kThreads) lut[i] = p.table[(int64_t)bucket_of(p.bk, i - m) * p.H + head] * kLog2e;
+}
+
+// What turns a raw product q.k into a score in log2 units, and the derivative of the cap.
+//   no cap: x * scale * log2 e.   cap c: c tanh(x scale / c) log2 e, with tanh(u) = 1 - 2 / (1 + e^2u).
+struct Score {
+    float a;     // no cap: scale log2 e; cap: 2 scale log2 e / c (bf16) or scale / c (fp32)
+    float c2;    // c log2 e
+    __device__ __forceinline__ void init(const AttnParams& p, bool capped, bool fp32) {
+        c2 = p.cap * kLog2e;
+        a = !capped ? p.scale * kLog2e : fp32 ? p.scale / p.cap : 2.f * p.scale * kLog2e / p.cap;
+    }
+    // tanh of the capped score: from the hardware's exp2 and reciprocal for bf16 inputs (an absolute
+    // error of some 1e-7, times c in the score), from the math library for fp32 ones
+    template <typename T> __device__ __forceinline__ float tanh_of(float x) const {
+        if constexpr (sizeof(T) == 2) return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + exp2_hw(x * a));
+        else return tanhf(x * a);
+    }
+};
+
+}  // namespace attn
+}  // namespace ssd

@@ -1,0 +1,147 @@
+"""GPU tests of attention over packed documents against the fp64 model (oracle/attention.py)."""
+import numpy as np
+import pytest
+import torch
+
+import ssd_chunked_scan_02_amd as ssd
+from attn_helpers import f64, lse_bound, make, offsets, reference, within, y_bound
+
+pytestmark = pytest.mark.gpu
+
+# documents of no token, one token, odd sizes around the 32-, 64- and 128-row tiles
+LENS = [1, 130, 0, 64, 257, 31, 128, 1, 33]
+MODES = [dict(causal=True), dict(causal=False, bidirectional=True), dict(causal=True, cap=5.0),
+         dict(causal=True, bias="slopes"), dict(causal=False, bias="slopes", cap=30.0),
+         dict(causal=True, bias="buckets"), dict(causal=False, bias="buckets", bidirectional=True),
+         dict(causal=True, prefix=True), dict(causal=True, prefix=True, bias="buckets", bidirectional=True, cap=2.0)]
+
+
+def _case(mode):
+    mode = dict(mode)
+    bias, cap, pre = mode.pop("bias", "none"), mode.pop("cap", 0.0), mode.pop("prefix", False)
+    return mode, bias, cap, pre
+
+
+def _prefix(lens, pre):
+    return torch.tensor([(7 * i + 3) % (n + 2) if n else 5 for i, n in enumerate(lens)], dtype=torch.int64) if pre else None
+
+
+def _forward(d, cu, cu_k=None, prefix=None, cap=0.0, **how):
+    g = {n: (t.cuda() if t is not None else None) for n, t in d.items()}
+    move = lambda t: None if t is None else t.cuda()  # noqa: E731
+    y, lse = ssd.ssd_attn_forward(g["q"], g["k"], g["v"], move(cu), move(cu_k), softcap=cap, slopes=g["slopes"],
+                                  table=g["table"], prefix=move(prefix), lse=True, **how)
+    torch.cuda.synchronize()
+    return f64(y), f64(lse)
+
+
+def _check_forward(label, d, dtype, cap, y, lse, ref):
+    D, n = d["q"].shape[-1], len(d["k"])
+    within(y, ref["y"], y_bound(ref, dtype, D, n, cap), label + " y")
+    within(lse, ref["lse"], lse_bound(ref, D, n, cap), label + " lse")
+
+
+@pytest.mark.parametrize("mode", MODES, ids=lambda m: "-".join("%s=%s" % x for x in m.items()))
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("fp32", 32), ("fp32", 64), ("fp32", 128)])
+def test_forward_packed(dtype, D, mode):
+    how, bias, cap, pre = _case(mode)
+    H, Hk = (6, 2) if D == 32 else (4, 4) if D == 64 else (3, 1)
+    d = make(D, sum(LENS), sum(LENS), H, Hk, D, dtype, bias=bias)
+    cu, prefix = offsets(LENS), _prefix(LENS, pre)
+    y, lse = _forward(d, cu, prefix=prefix, cap=cap, **how)
+    ref = reference(d, cu=cu.numpy(), prefix=None if prefix is None else prefix.numpy(), cap=cap, **how)
+    _check_forward("%s D%d %s" % (dtype, D, mode), d, dtype, cap, y, lse, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_forward_keys_of_their_own(dtype, causal):
+    """Queries as the last positions of longer, shorter and empty key ranges: rows that see nothing."""
+    lq, lk = [5, 70, 40, 9, 0, 130, 3], [200, 70, 10, 0, 33, 1, 64]
+    d = make(3, sum(lq), sum(lk), 4, 2, 64, dtype, bias="buckets")
+    cu, cu_k = offsets(lq), offsets(lk)
+    how = dict(causal=causal, bidirectional=not causal)
+    y, lse = _forward(d, cu, cu_k, **how)
+    ref = reference(d, cu=cu.numpy(), cu_k=cu_k.numpy(), **how)
+    assert np.isneginf(ref["lse"]).any()
+    _check_forward("own keys %s causal=%s" % (dtype, causal), d, dtype, 0.0, y, lse, ref)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("fp32", 32)])
+@pytest.mark.parametrize("lq,lk", [(1, 1), (1, 500), (65, 65), (300, 300), (129, 1000)])
+def test_forward_batched_and_strided(dtype, D, lq, lk):
+    """Batched layout, q and k, v as views of wider rows; the dense call gives the same bits."""
+    B, H, Hk = 3, 4, 2
+    d = make(lq + lk, B * lq, B * lk, H, Hk, D, dtype, bias="slopes")
+    wide = torch.zeros((B * lk, (H + 2 * Hk) * D), dtype=d["q"].dtype).cuda()
+    wide[:, H * D:(H + Hk) * D] = d["k"].flatten(1).cuda()
+    wide[:, (H + Hk) * D:] = d["v"].flatten(1).cuda()
+    k = wide[:, H * D:(H + Hk) * D].view(B, lk, Hk, D)
+    v = wide[:, (H + Hk) * D:].view(B, lk, Hk, D)
+    q = d["q"].cuda().view(B, lq, H, D)
+    y, lse = ssd.ssd_attn_forward(q, k, v, slopes=d["slopes"].cuda(), lse=True)
+    y2, lse2 = ssd.ssd_attn_forward(q, k.contiguous(), v.contiguous(), slopes=d["slopes"].cuda(), lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(lse, lse2)
+    ref = reference(d, nseq=B)
+    _check_forward("batched %s %d %d" % (dtype, lq, lk), d, dtype, 0.0, f64(y).reshape(-1, H, D), f64(lse).reshape(-1, H), ref)
+
+
+def test_forward_large_scores():
+    """Scores far beyond what exp takes, of both signs, and a maximum that grows along the keys."""
+    d = make(11, 300, 300, 2, 1, 64, "fp32", spread=12.0)
+    d["k"] *= torch.linspace(0.01, 3.0, 300)[:, None, None]
+    cu = offsets([300])
+    y, lse = _forward(d, cu)
+    ref = reference(d, cu=cu.numpy())
+    assert np.abs(ref["lse"]).max() > 200
+    _check_forward("large scores", d, "fp32", 0.0, y, lse, ref)
+
+
+def test_rows_of_no_sequence_stay_as_they_were():
+    """Tokens behind the last sequence, NaN themselves, are neither written nor read into anything."""
+    lens, extra = [70, 33], 45
+    d = make(5, sum(lens) + extra, sum(lens) + extra, 2, 2, 64, "bf16")
+    for n in "qkv":
+        d[n][sum(lens):] = float("nan")
+    g = {n: d[n].cuda() for n in "qkv"}
+    y = torch.full_like(g["q"], 7.0)
+    lse = torch.full(g["q"].shape[:2], 7.0, device="cuda")
+    ssd.ssd_attn_forward(g["q"], g["k"], g["v"], offsets(lens).cuda(), causal=False, y=y, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.all(y[sum(lens):] == 7.0) and torch.all(lse[sum(lens):] == 7.0)
+    cut = {n: (t[:sum(lens)] if n in "qkv" else t) for n, t in d.items()}
+    ref = reference(cut, cu=offsets(lens).numpy(), causal=False)
+    _check_forward("tail", cut, "bf16", 0.0, f64(y)[:sum(lens)], f64(lse)[:sum(lens)], ref)
+
+
+def test_documents_do_not_reach_each_other():
+    """A document of NaN and infinities leaves its neighbours' outputs as they are without it."""
+    lens = [50, 77, 40]
+    d = make(6, sum(lens), sum(lens), 2, 1, 64, "bf16")
+    cu = offsets(lens)
+    clean, _ = _forward(d, cu)
+    d["v"][50:127], d["k"][50:127] = float("inf"), float("nan")
+    y, lse = _forward(d, cu)
+    assert np.isnan(y[50:127]).all() and np.isnan(lse[50:127]).all()
+    for s in (slice(0, 50), slice(127, 167)):
+        assert np.array_equal(y[s], clean[s])
+
+
+def test_many_short_documents():
+    """More documents than one search step takes, most of them a few tokens long."""
+    lens = [(5 * i) % 7 for i in range(4500)] + [200]
+    d = make(8, sum(lens), sum(lens), 1, 1, 32, "bf16")
+    cu = offsets(lens)
+    y, lse = _forward(d, cu)
+    ref = reference(d, cu=cu.numpy())
+    _check_forward("many documents", d, "bf16", 0.0, y, lse, ref)
+
+
+def test_no_tokens():
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    y, lse = ssd.ssd_attn_forward(z(0, 2, 64), z(0, 2, 64), z(0, 2, 64), offsets([0, 0]).cuda(), lse=True)
+    assert y.shape == (0, 2, 64) and lse.shape == (0, 2)
+    y, lse = ssd.ssd_attn_forward(z(2, 3, 2, 64) + 1, z(2, 0, 2, 64), z(2, 0, 2, 64), lse=True)
+    torch.cuda.synchronize()
+    assert torch.all(y == 0) and torch.all(torch.isneginf(lse))
