@@ -78,6 +78,25 @@ int ssd_attn_forward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q,
                      const void* k, const void* v, const float* slopes, const float* table,
                      void* y, float* lse, void* stream);
 
+/*
+ * The backward pass of ssd_attn_forward: the gradients of <dy, y> with respect to q, k, v and the table
+ * (of the learned bias; slopes and scale are constants), for training.
+ *   q .. table    the forward pass's inputs;  y, lse  its outputs;  dy [total_q, H, D] dense.
+ *   dq            [total_q, H, D];  dk, dv [total_k, Hk, D] (summed over the heads of each group).
+ *   dtable        [num_buckets, H] fp32, or NULL to skip it; needs table.
+ *   workspace     device scratch of at least ssd_attn_backward_workspace_bytes(dims, dtable wanted)
+ *                 bytes, 16-byte aligned; its contents are undefined afterwards.
+ * Rows of no sequence are never written; a key that no query sees has zero gradients.  No atomics: equal
+ * calls give equal bits.  Two launches, three with dtable.
+ */
+size_t ssd_attn_backward_workspace_bytes(const ssd_attn_dims* dims, int want_dtable);
+
+int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q,
+                      const int64_t* cu_seqlens_k, const int64_t* prefix, const void* q,
+                      const void* k, const void* v, const float* slopes, const float* table,
+                      const void* y, const float* lse, const void* dy, void* dq, void* dk, void* dv,
+                      float* dtable, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -106,6 +106,7 @@ def attention(q, k, v, nseq=None, cu=None, cu_k=None, causal=True, scale=None, c
                 out[n + "_abs"][rows, hd] += a(np.abs(ds) * w) @ np.abs(x)
                 out[n + "_y"][rows, hd] += a(dsy * w) @ np.abs(x)
                 out.setdefault(n + "_all", np.zeros_like(out[n]))[rows, hd] += a(dsa * w) @ np.abs(x)
+                out.setdefault(n + "_uncapped", np.zeros_like(out[n]))[rows, hd] += a(np.abs(ds) * abs(scale)) @ np.abs(x)
     return out
 
 

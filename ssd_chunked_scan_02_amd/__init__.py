@@ -25,6 +25,8 @@ The functions carry the names of the C entry points declared in ``include/ssd.h`
   ssd_strerror(code) -> str
 and, from ``include/ssd_attn.h`` (``attention.py``), the attention layer of a hybrid stack:
   ssd_attn_forward(q, k, v, cu_seqlens=None, ..., lse=None) -> (y, lse)
+  ssd_attn_backward_workspace_bytes(dims, want_dtable) -> int
+  ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, ...) -> dict of gradients
 """
 from __future__ import annotations
 
@@ -39,7 +41,7 @@ __all__ = ["SSDError", "Dims", "library_path", "load_library", "dims_for",
            "ssd_step_dt", "ssd_backward_workspace_bytes", "ssd_backward", "ssd_backward_profiled",
            "ssd_backward_dt_workspace_bytes", "ssd_backward_dt",
            "ssd_forward_noalloc", "ssd_noalloc_scratch_bytes", "ssd_strerror",
-           "ssd_attn_forward",
+           "ssd_attn_forward", "ssd_attn_backward", "ssd_attn_backward_workspace_bytes",
            "SSD_F32", "SSD_BF16", "SSD_DECAY_SCALAR", "SSD_DECAY_DIAG"]
 
 SSD_F32, SSD_BF16 = 0, 1
@@ -760,4 +762,5 @@ def ssd_step(state, x_t, log_a_t, B_t, C_t, D=None, y_t=None, stream=None):
 
 
 from . import attention  # noqa: E402  (its functions use the helpers above)
-from .attention import ssd_attn_forward  # noqa: E402
+from .attention import (  # noqa: E402
+    ssd_attn_backward, ssd_attn_backward_workspace_bytes, ssd_attn_forward)

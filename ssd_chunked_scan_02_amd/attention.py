@@ -24,10 +24,14 @@ class AttnDims(ctypes.Structure):
 
 
 def declare(lib):
-    vp, i32 = ctypes.c_void_p, ctypes.c_int
+    vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     dp = ctypes.POINTER(AttnDims)
     lib.ssd_attn_forward.argtypes = [dp] + [vp] * 11
     lib.ssd_attn_forward.restype = i32
+    lib.ssd_attn_backward_workspace_bytes.argtypes = [dp, i32]
+    lib.ssd_attn_backward_workspace_bytes.restype = sz
+    lib.ssd_attn_backward.argtypes = [dp] + [vp] * 16 + [sz, vp]
+    lib.ssd_attn_backward.restype = i32
 
 
 def _token_stride(t, name, dim, dtype, device):
@@ -135,3 +139,44 @@ def ssd_attn_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal: bool =
     if rc != SSD_OK:
         raise SSDError(rc, "ssd_attn_forward")
     return y, lse
+
+
+def ssd_attn_backward_workspace_bytes(dims: AttnDims, want_dtable: bool = False) -> int:
+    return int(load_library().ssd_attn_backward_workspace_bytes(ctypes.byref(dims), int(bool(want_dtable))))
+
+
+def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, causal: bool = True, scale=None,
+                      softcap: float = 0.0, slopes=None, table=None, max_distance: int = 128,
+                      bidirectional: bool = False, prefix=None, want_dtable=None, workspace=None, stream=None):
+    """Run ``ssd_attn_backward``: the gradients of <dy, y> for ssd_attn_forward, whose arguments these are
+    with its results ``y`` and ``lse``.  Returns a dict: dq, dk, dv (dtype of q, dense), and dtable
+    [num_buckets, H] fp32 where a table is given (want_dtable=False skips it).  Rows of no sequence are
+    not written."""
+    dims = _dims(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, softcap, slopes, table, max_distance, bidirectional,
+                 prefix)
+    dev = q.device
+    _check(y, "y", q.shape, q.dtype, dev)
+    _check(dy, "dy", q.shape, q.dtype, dev)
+    _check(lse, "lse", q.shape[:-1], torch.float32, dev)
+    if want_dtable is None:
+        want_dtable = table is not None
+    if want_dtable and table is None:
+        raise ValueError("dtable needs a table")
+    out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev), dk=torch.empty(k.shape, dtype=q.dtype, device=dev),
+               dv=torch.empty(v.shape, dtype=q.dtype, device=dev))
+    if want_dtable:
+        # (no sequence: no launch writes it)
+        out["dtable"] = (torch.empty if dims.nseq else torch.zeros)(table.shape, dtype=torch.float32, device=dev)
+    need = ssd_attn_backward_workspace_bytes(dims, want_dtable)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _on_stream(stream, workspace, *out.values())
+    with torch.cuda.device(dev):
+        rc = load_library().ssd_attn_backward(
+            ctypes.byref(dims), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _ptr(prefix), _ptr(q), _ptr(k), _ptr(v),
+            _ptr(slopes), _ptr(table), _ptr(y), _ptr(lse), _ptr(dy), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+            _ptr(out.get("dtable")), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
+    if rc != SSD_OK:
+        raise SSDError(rc, "ssd_attn_backward")
+    return out

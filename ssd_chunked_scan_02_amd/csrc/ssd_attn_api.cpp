@@ -145,6 +145,22 @@ int fill(const ssd_attn_dims* d, const int64_t* cu_q, const int64_t* cu_k, const
 
 int code(int rc) { return rc == 0 ? SSD_OK : rc == -2 ? SSD_ERR_UNSUPPORTED : SSD_ERR_HIP; }
 
+size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// Workspace of the backward pass: D per (query, head), then the table's partial gradients.  The slots
+// are bounded without the offsets, so that the size does not depend on how a call gives its sequences.
+struct BackwardWorkspace {
+    size_t delta, part, total;
+};
+BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
+    BackwardWorkspace w{};
+    const size_t slots = (size_t)(d->total_q / 128 + d->nseq + 1);
+    w.delta = align16((size_t)d->total_q * (size_t)d->nheads * 4);
+    w.part = table ? align16(slots * (size_t)d->nheads * (size_t)d->num_buckets * 4) : 0;
+    w.total = w.delta + w.part;
+    return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -163,6 +179,43 @@ int ssd_attn_forward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, con
     p.y = y;
     p.lse = lse;
     return code(ssd::launch_attn_forward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_attn_backward_workspace_bytes(const ssd_attn_dims* d, int want_dtable) {
+    if (!d || d->nseq <= 0 || d->nseq > kMaxTokens || d->total_q < 0 || d->total_q > kMaxTokens || d->total_k < 0 ||
+        d->total_k > kMaxTokens || check_shape(d->nheads, d->nkvheads, d->headdim, d->dtype) != SSD_OK ||
+        (want_dtable && (d->num_buckets < 2 || d->num_buckets > 2 * ssd::kMaxBorders)))
+        return 0;
+    return backward_workspace(d, want_dtable != 0).total;
+}
+
+int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, const int64_t* cu_seqlens_k,
+                      const int64_t* prefix, const void* q, const void* k, const void* v, const float* slopes,
+                      const float* table, const void* y, const float* lse, const void* dy, void* dq, void* dk, void* dv,
+                      float* dtable, void* workspace, size_t workspace_bytes, void* stream) {
+    ssd::AttnParams p{};
+    int bias = 0;
+    const int rc = fill(dims, cu_seqlens_q, cu_seqlens_k, prefix, q, k, v, slopes, table, p, bias);
+    if (rc != SSD_OK) return rc;
+    if (dtable && !table) return SSD_ERR_INVALID;
+    const bool queries = p.nseq > 0 && p.total_q > 0, keys = p.nseq > 0 && p.total_k > 0;
+    if ((queries && (!y || !lse || !dy || !dq)) || (keys && (!dk || !dv))) return SSD_ERR_INVALID;
+    const void* wide[] = {y, lse, dy, dq, dk, dv, dtable, workspace};
+    for (const void* x : wide)
+        if (x && !aligned(x, 16)) return SSD_ERR_ALIGN;
+    const BackwardWorkspace w = backward_workspace(dims, dtable != nullptr);
+    if (p.nseq > 0 && w.total > 0 && (!workspace || workspace_bytes < w.total)) return SSD_ERR_INVALID;
+    if (!queries && !keys && !dtable) return SSD_OK;
+    p.y = const_cast<void*>(y);
+    p.lse = const_cast<float*>(lse);
+    p.dy = dy;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dtable = dtable;
+    p.delta = static_cast<float*>(workspace);
+    p.table_part = dtable ? reinterpret_cast<float*>(static_cast<char*>(workspace) + w.delta) : nullptr;
+    return code(ssd::launch_attn_backward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

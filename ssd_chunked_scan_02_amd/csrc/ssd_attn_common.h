@@ -196,6 +196,7 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, bool by
 
 // Slots of an axis: its whole tiles, and one more for each sequence.
 inline int64_t slots_of(const int64_t* cu, int64_t total, int64_t nseq) {
+    if (nseq == 0) return 0;
     return cu ? total / kBM + nseq : nseq * ((total / nseq + kBM - 1) / kBM);
 }
 

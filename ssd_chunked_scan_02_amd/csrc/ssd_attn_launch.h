@@ -52,8 +52,6 @@ struct AttnParams {
 };
 
 // 0 on success, -1 when HIP rejects a launch, -2 for an unsupported shape.
-int attn_forward_tile(int dtype, int D);   // queries a workgroup takes
-int attn_backward_tile(int dtype, int D);  // keys a workgroup of the key-gradient kernel takes
 int launch_attn_forward(const AttnParams& p, int dtype, int D, int bias, hipStream_t stream);
 int launch_attn_backward(const AttnParams& p, int dtype, int D, int bias, hipStream_t stream);
 

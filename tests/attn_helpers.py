@@ -75,3 +75,23 @@ def reference(d, cu=None, cu_k=None, nseq=None, dy=None, y_err=None, **how):
 
 def offsets(lens):
     return torch.tensor([0] + list(lens), dtype=torch.int64).cumsum(0)
+
+
+def grad_bounds(ref, dtype, D, n, H, Hk, cap):
+    """Bounds of dq, dk, dv and dtable.  dv: p rounded to bf16 and one output rounding.  dq, dk: dS rounded,
+    the output rounded, and what the inexact y adds to D (``*_y``, from y_err).  fp32 parts: p has the
+    relative error 2 e_s of its score and lse, on every term of dS (``*_all`` takes both terms' magnitude),
+    and a cap's 1 - t^2 loses 4 u of itself in each of the two roundings of t.  Sums: n terms per head."""
+    es = float(score_error(ref, D, cap).max())
+    u, group = 2.0 ** -24, H // Hk
+    rel = 4 * es + (n * group + 2 * D + 32) * u
+    soft = U[dtype] if dtype == "bf16" else 0.0
+    got = {"dv": 1.1 * (soft * ref["dv_abs"] + U[dtype] * np.abs(ref["dv"]) + rel * ref["dv_abs"]) + 1e-30}
+    for x in ("dq", "dk"):
+        flat = rel * ref[x + "_all"]
+        if cap:  # near the cap the derivative is small, and its error is not
+            flat = flat + 16 * u * ref[x + "_uncapped"]
+        got[x] = 1.1 * (soft * ref[x + "_abs"] + U[dtype] * np.abs(ref[x]) + ref[x + "_y"] + flat) + 1e-30
+    if "dtable" in ref:  # (its D is exact: no part of y's error)
+        got["dtable"] = 1.1 * rel * ref["dtable_abs"] + 1e-30
+    return got

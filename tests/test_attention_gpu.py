@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import ssd_chunked_scan_02_amd as ssd
-from attn_helpers import f64, lse_bound, make, offsets, reference, within, y_bound
+from attn_helpers import f64, grad_bounds, lse_bound, make, offsets, reference, within, y_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +145,105 @@ def test_no_tokens():
     y, lse = ssd.ssd_attn_forward(z(2, 3, 2, 64) + 1, z(2, 0, 2, 64), z(2, 0, 2, 64), lse=True)
     torch.cuda.synchronize()
     assert torch.all(y == 0) and torch.all(torch.isneginf(lse))
+
+
+def _backward(d, cu, cu_k=None, prefix=None, cap=0.0, **how):
+    g = {n: (t.cuda() if t is not None else None) for n, t in d.items()}
+    move = lambda t: None if t is None else t.cuda()  # noqa: E731
+    how = dict(how, softcap=cap, slopes=g["slopes"], table=g["table"], prefix=move(prefix))
+    y, lse = ssd.ssd_attn_forward(g["q"], g["k"], g["v"], move(cu), move(cu_k), lse=True, **how)
+    got = ssd.ssd_attn_backward(g["q"], g["k"], g["v"], y, lse, g["dy"], move(cu), move(cu_k), **how)
+    torch.cuda.synchronize()
+    return {n: f64(t) for n, t in got.items()}
+
+
+def _check_backward(label, d, dtype, cap, got, cu, cu_k=None, prefix=None, **how):
+    H, D = d["q"].shape[1:]
+    n = max(len(d["q"]), len(d["k"]))
+    how = dict(how, cap=cap, cu=cu.numpy(), cu_k=None if cu_k is None else cu_k.numpy(),
+               prefix=None if prefix is None else prefix.numpy())
+    first = reference(d, **how)
+    ref = reference(d, dy=d["dy"], y_err=y_bound(first, dtype, D, n, cap), **how)
+    bounds = grad_bounds(ref, dtype, D, n, H, d["k"].shape[1], cap)
+    assert set(got) == set(bounds)
+    for x in sorted(bounds):
+        within(got[x], ref[x], bounds[x], "%s %s" % (label, x))
+
+
+@pytest.mark.parametrize("mode", MODES, ids=lambda m: "-".join("%s=%s" % x for x in m.items()))
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("fp32", 32), ("fp32", 64), ("fp32", 128)])
+def test_backward_packed(dtype, D, mode):
+    how, bias, cap, pre = _case(mode)
+    H, Hk = (6, 2) if D == 32 else (4, 4) if D == 64 else (3, 1)
+    d = make(100 + D, sum(LENS), sum(LENS), H, Hk, D, dtype, bias=bias, grads=True)
+    cu, prefix = offsets(LENS), _prefix(LENS, pre)
+    got = _backward(d, cu, prefix=prefix, cap=cap, **how)
+    _check_backward("%s D%d %s" % (dtype, D, mode), d, dtype, cap, got, cu, prefix=prefix, **how)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_backward_keys_of_their_own(dtype, causal):
+    lq, lk = [5, 70, 40, 9, 0, 130, 3], [200, 70, 10, 0, 33, 1, 64]
+    d = make(30, sum(lq), sum(lk), 4, 2, 64, dtype, bias="buckets", grads=True)
+    cu, cu_k = offsets(lq), offsets(lk)
+    how = dict(causal=causal, bidirectional=not causal)
+    got = _backward(d, cu, cu_k, **how)
+    _check_backward("own keys %s causal=%s" % (dtype, causal), d, dtype, 0.0, got, cu, cu_k, **how)
+
+
+@pytest.mark.parametrize("buckets,reach,both", [(2, 2, False), (4, 3, True), (7, 20, False), (64, 1024, False),
+                                                (128, 1000, True), (32, 17, False)])
+def test_table_shapes(buckets, reach, both):
+    """Few and many buckets, reaches shorter and longer than a document."""
+    lens = [600, 45]
+    d = make(buckets, sum(lens), sum(lens), 2, 1, 32, "fp32", bias="buckets", buckets=buckets, grads=True)
+    cu = offsets(lens)
+    how = dict(causal=False, bidirectional=both, max_distance=reach)
+    got = _backward(d, cu, **how)
+    _check_backward("table %d %d %s" % (buckets, reach, both), d, "fp32", 0.0, got, cu, **how)
+
+
+def test_backward_same_bits_and_batched():
+    """Equal calls give equal bits; the batched layout is the packed one with equal documents."""
+    B, T, H, Hk, D = 2, 200, 4, 2, 64
+    d = make(40, B * T, B * T, H, Hk, D, "bf16", bias="buckets", grads=True)
+    cu = offsets([T] * B)
+    a, b = _backward(d, cu), _backward(d, cu)
+    g = {n: d[n].cuda().view(B, T, *d[n].shape[1:]) for n in ("q", "k", "v", "dy")}
+    table = d["table"].cuda()
+    y, lse = ssd.ssd_attn_forward(g["q"], g["k"], g["v"], table=table, lse=True)
+    c = ssd.ssd_attn_backward(g["q"], g["k"], g["v"], y, lse, g["dy"], table=table)
+    torch.cuda.synchronize()
+    for n in a:
+        assert np.array_equal(a[n], b[n]), n
+        assert np.array_equal(a[n], f64(c[n]).reshape(a[n].shape)), n
+
+
+def test_gradients_against_differences():
+    """The fp32 gradients against central differences of the fp64 model's loss."""
+    d = make(50, 90, 90, 2, 1, 32, "fp32", bias="buckets", grads=True)
+    cu = offsets([90])
+    got = _backward(d, cu, cap=3.0)
+    rng = np.random.RandomState(0)
+    for n in ("q", "k", "v", "table"):
+        way = torch.from_numpy(rng.randn(*d[n].shape))
+        loss = lambda e: (reference(dict(d, **{n: d[n].double() + e * way}), cu=cu.numpy(), cap=3.0)["y"] * f64(d["dy"])).sum()  # noqa: E731
+        want = (loss(1e-4) - loss(-1e-4)) / 2e-4
+        have = float((got["d" + n] * way.numpy()).sum())
+        size = float(np.linalg.norm(got["d" + n]) * np.linalg.norm(way))
+        # differences: h^2 and 1e-16 / h of the loss; gradients: fp32 sums of some hundred terms
+        assert abs(have - want) <= 1e-5 * size, (n, have, want)
+
+
+def test_gradients_of_no_sequence_stay_as_they_were():
+    lens, extra = [70, 33], 45
+    total = sum(lens) + extra
+    d = make(60, total, total, 2, 1, 64, "bf16", grads=True)
+    for n in ("q", "k", "v", "dy"):
+        d[n][sum(lens):] = float("nan")
+    got = _backward(d, offsets(lens))
+    cut = {n: (t[:sum(lens)] if t is not None else None) for n, t in d.items()}
+    want = _backward(cut, offsets(lens))
+    for n in want:
+        assert np.array_equal(got[n][:sum(lens)], want[n]), n
