@@ -97,6 +97,67 @@ int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q,
                       const void* y, const float* lse, const void* dy, void* dq, void* dk, void* dv,
                       float* dtable, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * A paged cache of keys and values: k_cache, v_cache [num_pages, page_size, Hk, D].  Position t of sequence s
+ * is row t % page_size of page block_table[s, t / page_size] (block_table: DEVICE memory, int32
+ * [nseq, max_pages]).  An entry that is no page (negative, or num_pages and more) is never followed: its
+ * keys are not visible, and nothing is written to it.
+ */
+typedef struct {
+    int64_t nseq;          /* sequences, >= 0 */
+    int64_t nheads;        /* H, Hk, D as in ssd_attn_dims */
+    int64_t nkvheads;
+    int64_t headdim;
+    int64_t num_pages;     /* 0 .. 2^31 - 1 */
+    int64_t page_size;     /* a multiple of 16, at most 65536 */
+    int64_t max_pages;     /* entries of a block table row, >= 0; max_pages page_size at most 2^31 - 1025 */
+    int64_t q_stride;      /* elements from one token to the next, as in ssd_attn_dims (0: dense) */
+    int64_t k_stride;      /* of the tokens that ssd_kv_append is given */
+    int64_t v_stride;
+    float scale;
+    float softcap;
+    int32_t dtype;         /* ssd_dtype of q, k, v, y and the cache */
+    int32_t num_buckets;   /* with a table: as in ssd_attn_dims */
+    int32_t max_distance;
+    int32_t bidirectional;
+} ssd_attn_cache;
+
+/*
+ * Attention of one query per sequence over the cache (a decode step): the operator above with Lq = 1 and
+ * Lk = seq_lens[s], every cached position visible, the query at the last one.
+ *   q [nseq, H, D], y [nseq, H, D] dense; block_table, seq_lens (int64 [nseq], clamped into
+ *   [0, max_pages page_size]) DEVICE memory, read by the kernels only.  A sequence of no visible key has y = 0.
+ *   Rows of a page past a sequence's length are not read.
+ *   workspace     ssd_attn_decode_workspace_bytes(dims) bytes, 16-byte aligned, private to calls that
+ *                 may overlap; its contents are undefined afterwards.
+ * One launch, or two where sequences are split along their keys.
+ */
+size_t ssd_attn_decode_workspace_bytes(const ssd_attn_cache* dims);
+
+int ssd_attn_decode(const ssd_attn_cache* dims, const void* q, const void* k_cache,
+                    const void* v_cache, const int32_t* block_table, const int64_t* seq_lens,
+                    const float* slopes, const float* table, void* y, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Appends new tokens' keys and values to the cache, the keys rotated by their positions, and rotates the
+ * queries beside them.  Tokens are packed: token i of sequence s (cu_seqlens, int64 [nseq + 1], DEVICE
+ * memory; NULL: one token per sequence, tokens must equal nseq) has position
+ * seq_lens[s] - (cu_seqlens[s + 1] - i): seq_lens counts the sequence with its new tokens.
+ *   inv_freq      fp32 [rot_pairs] or NULL (no rotation, rot_pairs 0): pair r of a head is turned by
+ *                 position * inv_freq[r] radians, (a, b) -> (a cos - b sin, b cos + a sin).
+ *   rot_pairs     a multiple of 8, at most D / 2.  Pairs are elements (r, r + rot_pairs), or with
+ *                 `interleaved` (2 r, 2 r + 1); elements from 2 rot_pairs on are copied.
+ *   q, q_out      queries [tokens, H, D] and their rotated copy (dense), or both NULL.
+ * A token whose position is outside the block table or on no page is not appended (its query is rotated
+ * all the same); tokens of no sequence are left alone.  Two tokens for one place leave either's values,
+ * element by element.
+ */
+int ssd_kv_append(const ssd_attn_cache* dims, int64_t tokens, const int64_t* cu_seqlens,
+                  const int64_t* seq_lens, const int32_t* block_table, const void* k, const void* v,
+                  const void* q, const float* inv_freq, int rot_pairs, int interleaved,
+                  void* k_cache, void* v_cache, void* q_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,9 @@ and, from ``include/ssd_attn.h`` (``attention.py``), the attention layer of a hy
   ssd_attn_forward(q, k, v, cu_seqlens=None, ..., lse=None) -> (y, lse)
   ssd_attn_backward_workspace_bytes(dims, want_dtable) -> int
   ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, ...) -> dict of gradients
+  ssd_attn_decode_workspace_bytes(dims) -> int
+  ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, ...) -> y
+  ssd_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, ...) -> rotated q or None
 """
 from __future__ import annotations
 
@@ -42,6 +45,7 @@ __all__ = ["SSDError", "Dims", "library_path", "load_library", "dims_for",
            "ssd_backward_dt_workspace_bytes", "ssd_backward_dt",
            "ssd_forward_noalloc", "ssd_noalloc_scratch_bytes", "ssd_strerror",
            "ssd_attn_forward", "ssd_attn_backward", "ssd_attn_backward_workspace_bytes",
+           "ssd_attn_decode", "ssd_attn_decode_workspace_bytes", "ssd_kv_append",
            "SSD_F32", "SSD_BF16", "SSD_DECAY_SCALAR", "SSD_DECAY_DIAG"]
 
 SSD_F32, SSD_BF16 = 0, 1
@@ -763,4 +767,5 @@ def ssd_step(state, x_t, log_a_t, B_t, C_t, D=None, y_t=None, stream=None):
 
 from . import attention  # noqa: E402  (its functions use the helpers above)
 from .attention import (  # noqa: E402
-    ssd_attn_backward, ssd_attn_backward_workspace_bytes, ssd_attn_forward)
+    ssd_attn_backward, ssd_attn_backward_workspace_bytes, ssd_attn_decode,
+    ssd_attn_decode_workspace_bytes, ssd_attn_forward, ssd_kv_append)

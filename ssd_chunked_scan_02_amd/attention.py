@@ -23,6 +23,16 @@ class AttnDims(ctypes.Structure):
                 ("max_distance", ctypes.c_int32), ("bidirectional", ctypes.c_int32)]
 
 
+class AttnCache(ctypes.Structure):
+    """Mirror of ``ssd_attn_cache``."""
+    _fields_ = [("nseq", ctypes.c_int64), ("nheads", ctypes.c_int64), ("nkvheads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("num_buckets", ctypes.c_int32), ("max_distance", ctypes.c_int32),
+                ("bidirectional", ctypes.c_int32)]
+
+
 def declare(lib):
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     dp = ctypes.POINTER(AttnDims)
@@ -32,6 +42,13 @@ def declare(lib):
     lib.ssd_attn_backward_workspace_bytes.restype = sz
     lib.ssd_attn_backward.argtypes = [dp] + [vp] * 16 + [sz, vp]
     lib.ssd_attn_backward.restype = i32
+    cp = ctypes.POINTER(AttnCache)
+    lib.ssd_attn_decode_workspace_bytes.argtypes = [cp]
+    lib.ssd_attn_decode_workspace_bytes.restype = sz
+    lib.ssd_attn_decode.argtypes = [cp] + [vp] * 9 + [sz, vp]
+    lib.ssd_attn_decode.restype = i32
+    lib.ssd_kv_append.argtypes = [cp, ctypes.c_int64] + [vp] * 7 + [i32, i32] + [vp] * 4
+    lib.ssd_kv_append.restype = i32
 
 
 def _token_stride(t, name, dim, dtype, device):
@@ -180,3 +197,101 @@ def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, c
     if rc != SSD_OK:
         raise SSDError(rc, "ssd_attn_backward")
     return out
+
+
+def _cache_dims(q, heads, k_cache, v_cache, block_table, seq_lens, strides, scale, softcap, buckets, max_distance,
+                bidirectional):
+    """ssd_attn_cache of a call, the cache's arguments checked; q: any tensor of its dtype and device."""
+    dev = q.device
+    if q.dtype not in _DTYPE_CODE:
+        raise TypeError("the cache's tensors must be float32 or bfloat16, got %s" % q.dtype)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, page_size, Hk, D], got shape %s" % (tuple(k_cache.shape),))
+    _check(k_cache, "k_cache", k_cache.shape, q.dtype, dev)
+    _check(v_cache, "v_cache", k_cache.shape, q.dtype, dev)
+    pages, size, Hk, D = k_cache.shape
+    _offsets(seq_lens, "seq_lens", dev)
+    nseq = seq_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [nseq, max_pages]")
+    _check(block_table, "block_table", (nseq, block_table.shape[1]), torch.int32, dev)
+    return AttnCache(nseq, heads, Hk, D, pages, size, block_table.shape[1], *strides,
+                     D ** -0.5 if scale is None else float(scale), float(softcap), _DTYPE_CODE[q.dtype], buckets,
+                     int(max_distance), int(bool(bidirectional)))
+
+
+def ssd_attn_decode_workspace_bytes(dims: AttnCache) -> int:
+    return int(load_library().ssd_attn_decode_workspace_bytes(ctypes.byref(dims)))
+
+
+def ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0, slopes=None, table=None,
+                    max_distance: int = 128, bidirectional: bool = False, y=None, workspace=None, stream=None):
+    """Run ``ssd_attn_decode``: one query per sequence, q [nseq,H,D], over a paged cache.
+
+    k_cache, v_cache [num_pages, page_size, Hk, D] (page_size a multiple of 16), block_table int32
+    [nseq, max_pages], seq_lens int64 [nseq] with the present token, all on the GPU.  Bias and cap as in
+    ssd_attn_forward.  Returns y [nseq,H,D]."""
+    dev = q.device
+    stride = _token_stride(q, "q", 3, q.dtype, dev)
+    nseq, H, D = q.shape
+    buckets = _bias_args(slopes, table, H, dev)
+    dims = _cache_dims(q, H, k_cache, v_cache, block_table, seq_lens, (stride, 0, 0), scale, softcap, buckets,
+                       max_distance, bidirectional)
+    if dims.nseq != nseq or dims.headdim != D:
+        raise ValueError("q %s does not fit %d sequences of head dim %d" % (tuple(q.shape), dims.nseq, dims.headdim))
+    if y is None:
+        y = torch.empty((nseq, H, D), dtype=q.dtype, device=dev)
+    _check(y, "y", (nseq, H, D), q.dtype, dev)
+    need = ssd_attn_decode_workspace_bytes(dims)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _on_stream(stream, y, workspace)
+    with torch.cuda.device(dev):
+        rc = load_library().ssd_attn_decode(
+            ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(slopes),
+            _ptr(table), _ptr(y), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
+    if rc != SSD_OK:
+        raise SSDError(rc, "ssd_attn_decode")
+    return y
+
+
+def ssd_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, inv_freq=None,
+                  interleaved: bool = False, q=None, q_out=None, stream=None):
+    """Run ``ssd_kv_append``: the keys and values of new tokens, k, v [tokens,Hk,D], into the cache's pages in
+    place, the keys (and q [tokens,H,D], if given) rotated by their positions with ``inv_freq`` [pairs].
+
+    ``cu_seqlens``: int64 offsets of each sequence's new tokens (None: one token per sequence);
+    ``seq_lens`` counts the sequences with them.  Returns the rotated q, or None without q."""
+    dev = k.device
+    strides = [0 if t is None else _token_stride(t, n, 3, k.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
+    tokens, Hk, D = k.shape
+    H = Hk if q is None else q.shape[1]
+    dims = _cache_dims(k, H, k_cache, v_cache, block_table, seq_lens, strides, None, 0.0, 0, 0, False)
+    if (dims.nkvheads, dims.headdim) != (Hk, D) or tuple(v.shape) != tuple(k.shape):
+        raise ValueError("k %s and v %s do not fit the cache %s" % (tuple(k.shape), tuple(v.shape), tuple(k_cache.shape)))
+    if q is not None and (q.shape[0], q.shape[2]) != (tokens, D):
+        raise ValueError("q %s does not fit k %s" % (tuple(q.shape), tuple(k.shape)))
+    if q is not None and H % Hk != 0:
+        raise ValueError("q's %d heads are not a multiple of k's %d" % (H, Hk))
+    _offsets(cu_seqlens, "cu_seqlens", dev, dims.nseq + 1)
+    if cu_seqlens is None and tokens != dims.nseq:
+        raise ValueError("%d tokens for %d sequences: give cu_seqlens" % (tokens, dims.nseq))
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, dev)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out needs q")
+    else:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _check(q_out, "q_out", q.shape, q.dtype, dev)
+    _on_stream(stream, q_out)
+    with torch.cuda.device(dev):
+        rc = load_library().ssd_kv_append(
+            ctypes.byref(dims), tokens, _ptr(cu_seqlens), _ptr(seq_lens), _ptr(block_table), _ptr(k), _ptr(v), _ptr(q),
+            _ptr(inv_freq), 0 if inv_freq is None else inv_freq.numel(), int(bool(interleaved)), _ptr(k_cache),
+            _ptr(v_cache), _ptr(q_out), _stream_handle(stream, dev))
+    if rc != SSD_OK:
+        raise SSDError(rc, "ssd_kv_append")
+    return q_out

@@ -21,7 +21,7 @@ DEVICE_FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
                 "-Wall", "-Wno-unused-result"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall"]
 DEVICE_SOURCES = ["ssd_kernels.hip", "ssd_fast.hip", "ssd_diag.hip", "ssd_bwd.hip", "ssd_noalloc.hip",
-                  "ssd_attn.hip", "ssd_attn_bwd.hip"]
+                  "ssd_attn.hip", "ssd_attn_bwd.hip", "ssd_attn_decode.hip"]
 HOST_SOURCES = ["ssd_api.cpp", "ssd_attn_api.cpp"]
 
 

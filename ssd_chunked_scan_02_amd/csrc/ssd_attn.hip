@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
         L::load(vb, vg, p.v_stride, 0, sp.lk - 1);
     }
     Score sc;
-    sc.init(p, CAP, sizeof(T) == 4);
+    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     if constexpr (BIAS == kBiasBuckets) fill_bias(lut, p, head);

@@ -161,6 +161,43 @@ BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
     return w;
 }
 
+int check_cache(const ssd_attn_cache* d) {
+    if (!d) return SSD_ERR_INVALID;
+    const int rc = check_shape(d->nheads, d->nkvheads, d->headdim, d->dtype);
+    if (rc != SSD_OK) return rc;
+    if (d->nseq < 0 || d->nseq > kMaxTokens || d->num_pages < 0 || d->num_pages >= ((int64_t)1 << 31) || d->page_size < 1 ||
+        d->max_pages < 0 || d->max_pages > kMaxTokens)
+        return SSD_ERR_INVALID;
+    if (d->page_size % 16 != 0 || d->page_size > 65536 || d->max_pages * d->page_size > kMaxTokens) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Splits of a sequence's keys: enough workgroups for four on each of the 256 CUs, so that short and long
+// sequences even out, of at least 128 keys (a block for each wave) at the longest length, and few
+// enough that joining them stays small.
+int decode_splits(const ssd_attn_cache* d) {
+    const int64_t group = d->nheads / d->nkvheads, units = d->nseq * d->nkvheads * ((group + 15) / 16);
+    int64_t n = units > 0 ? (1024 + units - 1) / units : 1;
+    const int64_t most = (d->max_pages * d->page_size + 127) / 128;
+    if (n > most) n = most;
+    if (n > 64) n = 64;
+    return n < 1 ? 1 : (int)n;
+}
+
+struct DecodeWorkspace {
+    size_t o, ml, total;
+};
+DecodeWorkspace decode_workspace(const ssd_attn_cache* d) {
+    DecodeWorkspace w{};
+    const size_t n = (size_t)decode_splits(d), units = (size_t)d->nseq * (size_t)d->nheads;
+    if (n > 1) {
+        w.o = units * n * (size_t)d->headdim * 4;
+        w.ml = align16(units * n * 2 * 4);
+    }
+    w.total = w.o + w.ml;
+    return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +253,101 @@ int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, co
     p.delta = static_cast<float*>(workspace);
     p.table_part = dtable ? reinterpret_cast<float*>(static_cast<char*>(workspace) + w.delta) : nullptr;
     return code(ssd::launch_attn_backward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_attn_decode_workspace_bytes(const ssd_attn_cache* d) {
+    return check_cache(d) == SSD_OK ? decode_workspace(d).total : 0;
+}
+
+int ssd_attn_decode(const ssd_attn_cache* d, const void* q, const void* k_cache, const void* v_cache,
+                    const int32_t* block_table, const int64_t* seq_lens, const float* slopes, const float* table, void* y,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_cache(d);
+    if (rc != SSD_OK) return rc;
+    if (!std::isfinite(d->scale) || !std::isfinite(d->softcap) || d->softcap < 0.f || (slopes && table)) return SSD_ERR_INVALID;
+    ssd::DecodeParams p{};
+    if ((rc = check_stride(d->q_stride, d->nheads * d->headdim, d->dtype == SSD_BF16 ? 2 : 4, p.q_stride)) != SSD_OK) return rc;
+    if (table && (rc = make_buckets(p.bk, d->num_buckets, d->max_distance, d->bidirectional)) != SSD_OK) return rc;
+    const bool cached = d->num_pages > 0 && d->max_pages > 0;
+    if (d->nseq > 0 && (!q || !y || !seq_lens || (cached && (!k_cache || !v_cache)) || (d->max_pages > 0 && !block_table)))
+        return SSD_ERR_INVALID;
+    const void* wide[] = {q, k_cache, v_cache, slopes, table, y, workspace};
+    for (const void* x : wide)
+        if (x && !aligned(x, 16)) return SSD_ERR_ALIGN;
+    if ((block_table && !aligned(block_table, 4)) || (seq_lens && !aligned(seq_lens, 8))) return SSD_ERR_ALIGN;
+    p.splits = decode_splits(d);
+    if (d->nseq * d->nheads * p.splits >= ((int64_t)1 << 31)) return SSD_ERR_UNSUPPORTED;
+    const DecodeWorkspace w = decode_workspace(d);
+    if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return SSD_ERR_INVALID;
+    if (d->nseq == 0) return SSD_OK;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.slopes = slopes;
+    p.table = table;
+    p.y = y;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = w.total > 0 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o) : nullptr;
+    p.nseq = d->nseq;
+    p.H = (int)d->nheads;
+    p.Hk = (int)d->nkvheads;
+    p.num_pages = (int)d->num_pages;
+    p.page_size = (int)d->page_size;
+    p.max_pages = (int)d->max_pages;
+    p.scale = d->scale;
+    p.cap = d->softcap;
+    const int bias = table ? ssd::kBiasBuckets : slopes ? ssd::kBiasSlopes : ssd::kBiasNone;
+    return code(ssd::launch_attn_decode(p, d->dtype, (int)d->headdim, bias, static_cast<hipStream_t>(stream)));
+}
+
+int ssd_kv_append(const ssd_attn_cache* d, int64_t tokens, const int64_t* cu_seqlens, const int64_t* seq_lens,
+                  const int32_t* block_table, const void* k, const void* v, const void* q, const float* inv_freq,
+                  int rot_pairs, int interleaved, void* k_cache, void* v_cache, void* q_out, void* stream) {
+    int rc = check_cache(d);
+    if (rc != SSD_OK) return rc;
+    if (tokens < 0 || tokens > kMaxTokens || (!cu_seqlens && tokens != d->nseq)) return SSD_ERR_INVALID;
+    if ((interleaved != 0 && interleaved != 1) || rot_pairs < 0 || 2 * (int64_t)rot_pairs > d->headdim || (rot_pairs > 0 && !inv_freq))
+        return SSD_ERR_INVALID;
+    if (rot_pairs % 8 != 0) return SSD_ERR_UNSUPPORTED;
+    ssd::AppendParams p{};
+    const int64_t elem = d->dtype == SSD_BF16 ? 2 : 4;
+    if ((rc = check_stride(d->q_stride, d->nheads * d->headdim, elem, p.q_stride)) != SSD_OK) return rc;
+    if ((rc = check_stride(d->k_stride, d->nkvheads * d->headdim, elem, p.k_stride)) != SSD_OK) return rc;
+    if ((rc = check_stride(d->v_stride, d->nkvheads * d->headdim, elem, p.v_stride)) != SSD_OK) return rc;
+    if (!q != !q_out) return SSD_ERR_INVALID;
+    const bool cached = d->num_pages > 0 && d->max_pages > 0;
+    if (tokens > 0 && d->nseq > 0 &&
+        (!k || !v || !seq_lens || (cached && (!k_cache || !v_cache)) || (d->max_pages > 0 && !block_table)))
+        return SSD_ERR_INVALID;
+    const void* wide[] = {q, k, v, q_out, k_cache, v_cache, inv_freq};
+    for (const void* x : wide)
+        if (x && !aligned(x, 16)) return SSD_ERR_ALIGN;
+    if ((block_table && !aligned(block_table, 4)) || (seq_lens && !aligned(seq_lens, 8)) || (cu_seqlens && !aligned(cu_seqlens, 8)))
+        return SSD_ERR_ALIGN;
+    if (tokens == 0 || d->nseq == 0) return SSD_OK;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.cu = cu_seqlens;
+    p.inv_freq = inv_freq;
+    p.nseq = d->nseq;
+    p.tokens = tokens;
+    p.H = (int)d->nheads;
+    p.Hk = (int)d->nkvheads;
+    p.D = (int)d->headdim;
+    p.num_pages = (int)d->num_pages;
+    p.page_size = (int)d->page_size;
+    p.max_pages = (int)d->max_pages;
+    p.rot = inv_freq ? rot_pairs : 0;
+    p.interleaved = interleaved;
+    return code(ssd::launch_kv_append(p, d->dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
     if (lse2 == -INFINITY || row >= sp.lq) lse2 = INFINITY;
 
     Score sc;
-    sc.init(p, CAP, sizeof(T) == 4);
+    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     const int md = p.bk.max_distance, reach = 2 * md + 1;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) * D >= 256 ? 1 : 2) attn_d
         }
     }
     Score sc;
-    sc.init(p, CAP, sizeof(T) == 4);
+    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
     const int md = p.bk.max_distance;
 
     f32x16 dk[DT], dv[DT];

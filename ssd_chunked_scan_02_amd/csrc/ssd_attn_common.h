@@ -157,19 +157,27 @@ __device__ __forceinline__ void span_of(const int64_t* cu, int64_t total, int64_
 // Sequence and tile of a slot.  Sequence s owns the slots from floor(cu[s] / kBM) + s on, one more than
 // its whole tiles at most, so that a workgroup finds its work from the offsets alone, with no list made
 // on the way: a search 64 sequences wide (one step for 64 sequences, two for 4096).
-__device__ __forceinline__ int slot_sequence(const int64_t* cu, int64_t total, int64_t nseq, int slot) {
+template <typename F>
+__device__ __forceinline__ int64_t last_at_most(int64_t nseq, int64_t x, F start) {
     const int lane = threadIdx.x % kWave;
-    int64_t lo = 0, n = nseq;  // the last s in [lo, lo + n) with start(s) <= slot
+    int64_t lo = 0, n = nseq;  // the last s in [lo, lo + n) with start(s) <= x
     while (n > 1) {
         const int64_t step = (n + kWave - 1) / kWave;
         const int64_t s = lo + step * lane;
-        const bool le = s < lo + n && clamp64(cu[s], 0, total) / kBM + s <= slot;
+        const bool le = s < lo + n && start(s) <= x;
         const int cnt = __popcll(__ballot(le));
         const int64_t at = cnt > 0 ? step * (cnt - 1) : 0;
         lo += at;
         n = n - at < step ? n - at : step;
     }
-    return (int)lo;
+    return __builtin_amdgcn_readfirstlane((int)lo);
+}
+__device__ __forceinline__ int slot_sequence(const int64_t* cu, int64_t total, int64_t nseq, int slot) {
+    return (int)last_at_most(nseq, slot, [&](int64_t s) { return clamp64(cu[s], 0, total) / kBM + s; });
+}
+// The sequence whose tokens token t of a packed axis is among, if it is among any.
+__device__ __forceinline__ int64_t last_start(const int64_t* cu, int64_t nseq, int64_t t) {
+    return last_at_most(nseq, t, [&](int64_t s) { return cu[s]; });
 }
 
 // (by_keys: the slots count tiles of the key axis)
@@ -183,7 +191,7 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, bool by
         s = slot / per;
         tile = slot % per;
     } else {
-        s = __builtin_amdgcn_readfirstlane(slot_sequence(cu, total, p.nseq, slot));
+        s = slot_sequence(cu, total, p.nseq, slot);
         tile = slot - (int)(clamp64(cu[s], 0, total) / kBM + s);
     }
     sp.seq = s;
@@ -231,9 +239,9 @@ __device__ __forceinline__ void fill_bias(float* lut, const AttnParams& p, int h
 struct Score {
     float a;     // no cap: scale log2 e; cap: 2 scale log2 e / c (bf16) or scale / c (fp32)
     float c2;    // c log2 e
-    __device__ __forceinline__ void init(const AttnParams& p, bool capped, bool fp32) {
-        c2 = p.cap * kLog2e;
-        a = !capped ? p.scale * kLog2e : fp32 ? p.scale / p.cap : 2.f * p.scale * kLog2e / p.cap;
+    __device__ __forceinline__ void init(float scale, float cap, bool capped, bool fp32) {
+        c2 = cap * kLog2e;
+        a = !capped ? scale * kLog2e : fp32 ? scale / cap : 2.f * scale * kLog2e / cap;
     }
     // tanh of the capped score: from the hardware's exp2 and reciprocal for bf16 inputs (an absolute
     // error of some 1e-7, times c in the score), from the math library for fp32 ones

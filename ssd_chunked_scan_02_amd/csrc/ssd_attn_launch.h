@@ -51,8 +51,47 @@ struct AttnParams {
     AttnBuckets bk;
 };
 
+// One query per sequence over a paged cache.
+struct DecodeParams {
+    const void* q;            // [nseq, H, D]
+    const void* k_cache;      // [num_pages, page_size, Hk, D]
+    const void* v_cache;
+    const int* block_table;   // [nseq, max_pages]
+    const int64_t* seq_lens;  // [nseq]
+    const float* slopes;
+    const float* table;
+    void* y;                  // [nseq, H, D]
+    float* part_o;            // workspace [nseq, H, splits, D]
+    float* part_ml;           // workspace [nseq, H, splits, 2]
+    int64_t nseq, q_stride;
+    int H, Hk, num_pages, page_size, max_pages, splits;
+    float scale, cap;
+    AttnBuckets bk;
+};
+
+// Tokens appended to a paged cache, rotated by their positions.
+constexpr int kMaxRot = 64;
+struct AppendParams {
+    const void* q;  // null: no queries
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    const int* block_table;
+    const int64_t* seq_lens;  // lengths with the new tokens
+    const int64_t* cu;        // null: one token per sequence
+    const float* inv_freq;    // [rot]
+    int64_t nseq, tokens, q_stride, k_stride, v_stride;
+    int H, Hk, D, num_pages, page_size, max_pages;
+    int rot;                  // pairs that are rotated
+    int interleaved;
+};
+
 // 0 on success, -1 when HIP rejects a launch, -2 for an unsupported shape.
 int launch_attn_forward(const AttnParams& p, int dtype, int D, int bias, hipStream_t stream);
 int launch_attn_backward(const AttnParams& p, int dtype, int D, int bias, hipStream_t stream);
+int launch_attn_decode(const DecodeParams& p, int dtype, int D, int bias, hipStream_t stream);
+int launch_kv_append(const AppendParams& p, int dtype, hipStream_t stream);
 
 }  // namespace ssd
