@@ -49,8 +49,8 @@ typedef struct {
     int64_t nkvheads;      /* Hk >= 1, divides H */
     int64_t headdim;       /* D: 32, 64 or 128 */
     int64_t q_stride;      /* elements from one token of q to the next; 0: dense (H D).  A multiple of */
-    int64_t k_stride;      /* 16 bytes, at least the token's own elements.  Likewise k, v (Hk D) */
-    int64_t v_stride;
+    int64_t k_stride;      /* 16 bytes, at least the token's own elements, under 2^24.  Likewise k, v */
+    int64_t v_stride;      /* (dense: Hk D).  H D itself is under 2^24 */
     float scale;           /* of q . k: finite */
     float softcap;         /* 0: none; else positive and finite */
     int32_t dtype;         /* ssd_dtype of q, k, v, y and their gradients */

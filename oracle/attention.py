@@ -57,7 +57,6 @@ def attention(q, k, v, nseq=None, cu=None, cu_k=None, causal=True, scale=None, c
             out[n], out[n + "_abs"], out[n + "_y"] = np.zeros_like(x), np.zeros_like(x), np.zeros_like(x)
         if table is not None:
             out["dtable"], out["dtable_abs"] = np.zeros_like(table), np.zeros_like(table)
-            out["dtable_y"] = np.zeros_like(table)
     for s, ((q0, lq), (k0, lk)) in enumerate(zip(_spans(cu, Tq, nseq), _spans(cu if cu_k is None else cu_k, len(k), nseq))):
         out["seen"][q0:q0 + lq] = True
         if lq == 0 or lk == 0:
@@ -96,10 +95,8 @@ def attention(q, k, v, nseq=None, cu=None, cu_k=None, causal=True, scale=None, c
             out["dv"][k0:k0 + lk, g] += p.T @ gs
             out["dv_abs"][k0:k0 + lk, g] += p.T @ np.abs(gs)
             if cells is not None:
-                for i in range(table.shape[0]):
-                    out["dtable"][i, h] += ds[cells == i].sum()
-                    out["dtable_abs"][i, h] += dsa[cells == i].sum()
-                    out["dtable_y"][i, h] += dsy[cells == i].sum()
+                for n, x in (("dtable", ds), ("dtable_abs", dsa)):
+                    out[n][:, h] += np.bincount(cells.ravel(), x.ravel(), table.shape[0])
             w = c1 * abs(scale)
             for n, a, x, rows, hd in (("dq", lambda m: m, ks, slice(q0, q0 + lq), h), ("dk", np.transpose, qs, slice(k0, k0 + lk), g)):
                 out[n][rows, hd] += a(ds * c1 * scale) @ x

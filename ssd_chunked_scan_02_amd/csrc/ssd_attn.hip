@@ -4,10 +4,11 @@
 //
 // One pass over the keys with a running maximum m and sum l (in log2 units): a workgroup of four waves
 // owns 128 queries of one head and document, 32 a wave, and streams 64-key tiles (32 in fp32) through
-// LDS, double buffered, the next tile's global loads in flight while the present one is used.  A wave
-// forms S^T = K Q^T (queries in lanes), so m and l are one number a lane, and P^T in its accumulator
-// layout is the operand of O^T += V^T P^T (ssd_attn_common.h).  O is rescaled only when a row's maximum
-// has grown by more than 2^8: weights are relative to m, so a late m costs no accuracy.
+// LDS, double buffered, the next tile on its way to LDS while the present one is used.  A wave forms
+// S^T = K Q^T (queries in lanes), so m and l are one number a lane, and P^T in its accumulator layout is
+// the operand of O^T += V^T P^T (ssd_attn_common.h).  O is rescaled only when a row's maximum has grown by
+// more than 2^8: weights are relative to m, so a late m costs no accuracy.  With too few rows to fill
+// the chip the waves split the keys instead (SPLIT).
 #include "ssd_attn_common.h"
 
 namespace ssd {
@@ -15,31 +16,41 @@ namespace attn {
 namespace {
 
 constexpr float kLazy = 8.f;  // log2 growth of a maximum that is let pass without a rescale
+// Scores capped to at most 2^80 need no maximum at all: weights in [2^-80, 2^80] times 2^24 keys and any
+// sensible value stay inside fp32 (and bf16, which has its range).
+constexpr float kNoMaxNeeded = 80.f;
 
-template <typename T, int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
+template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_fwd_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
-    constexpr int KT = O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
-    __shared__ __attribute__((aligned(16))) T ks[2][L::kElems];
-    __shared__ __attribute__((aligned(16))) T vs[2][L::kElems];
+    constexpr int OWN = kOwn<SPLIT>, KT = SPLIT ? 32 : O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
+    constexpr int ELEMS = (SPLIT ? kWaves : 1) * KT * D;
+    constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;  // (two buffers of split fp32 tiles of 128 would not fit)
+    constexpr bool RAW = !CAP && BIAS == kBiasNone;  // scores stay raw products until the exponential
+    __shared__ __attribute__((aligned(16))) T k_a[ELEMS];
+    __shared__ __attribute__((aligned(16))) T v_a[ELEMS];
+    __shared__ __attribute__((aligned(16))) T k_b[DOUBLE ? ELEMS : 8];
+    __shared__ __attribute__((aligned(16))) T v_b[DOUBLE ? ELEMS : 8];
     __shared__ float lut[BIAS == kBiasBuckets ? 2 * kMaxDistance + 1 : 1];
+    __shared__ float stat[SPLIT ? 3 : 1][SPLIT ? kWaves * 32 : 1];  // m, l, weight of a wave's share by row
 
     int slot, head;
     work_item(blockIdx.x, p.q_slots, p.H, slot, head);
-    const Span sp = find_span(p, slot, false);
+    const Span sp = find_span(p, slot, OWN, false);
     if (sp.tile < 0) return;
     const int kvh = head / (p.H / p.Hk);
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, half = lane / 32;
+    const int lane = threadIdx.x % kWave, half = lane / 32;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int shift = sp.lk - sp.lq;  // position of query 0 on the key axis
     int prefix = 0;
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
 
     // keys [0, limit(i)) are visible to query i
     auto limit = [&](int i) { return p.causal ? max(min(max(i + shift + 1, prefix), sp.lk), 0) : sp.lk; };
-    const int row0 = sp.tile * kBM + wave * 32, row = row0 + lane % 32;
-    const int wg_limit = limit(min(sp.tile * kBM + kBM, sp.lq) - 1);
+    const int row0 = sp.tile * OWN + (SPLIT ? 0 : wave * 32), row = row0 + lane % 32;
+    const int wg_limit = limit(min(sp.tile * OWN + OWN, sp.lq) - 1);
     const int ntiles = (wg_limit + KT - 1) / KT;
     const int my_limit = row < sp.lq ? limit(row) : 0;
     const int wave_most = row0 < sp.lq ? limit(min(row0 + 32, sp.lq) - 1) : 0;  // any query of the wave
@@ -47,43 +58,44 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
 
     const T* kg = static_cast<const T*>(p.k) + sp.k0 * p.k_stride + (int64_t)kvh * D;
     const T* vg = static_cast<const T*>(p.v) + sp.k0 * p.v_stride + (int64_t)kvh * D;
+    Feed<T, D, KT, SPLIT ? kWave : kThreads> kf, vf;
+    kf.init(p.k_stride);
+    vf.init(p.v_stride);
+    const int at = SPLIT ? wave * KT * D : 0;
+    T *ka = k_a + at, *va = v_a + at, *kb = k_b + (DOUBLE ? at : 0), *vb = v_b + (DOUBLE ? at : 0);
+    auto fetch = [&](T* ks, T* vs, int t) {
+        kf.load(ks, kg, t * KT, sp.lk - t * KT);
+        vf.load(vs, vg, t * KT, sp.lk - t * KT);
+    };
+    const int t0 = SPLIT ? wave : 0, dt = SPLIT ? kWaves : 1;
+    if (t0 < ntiles) fetch(ka, va, t0);
 
     Frag qf[NT];
     {
         const T* qg = static_cast<const T*>(p.q) + (sp.q0 + min(row, sp.lq - 1)) * p.q_stride + (int64_t)head * D;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) qf[t] = __builtin_bit_cast(Frag, ld16(qg + (2 * t + half) * O::kE));
-    }
-    uint4 kb[L::kLoads], vb[L::kLoads];
-    if (ntiles > 0) {
-        L::load(kb, kg, p.k_stride, 0, sp.lk - 1);
-        L::load(vb, vg, p.v_stride, 0, sp.lk - 1);
+        for (int t = 0; t < NT; ++t) qf[t] = signed_frag<T>(qg + (2 * t + half) * O::kE, p.scale);
     }
     Score sc;
-    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
+    sc.init<T>(p.scale, p.cap, CAP);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     if constexpr (BIAS == kBiasBuckets) fill_bias(lut, p, head);
-    if (ntiles > 0) {
-        L::store(ks[0], kb);
-        L::store(vs[0], vb);
-    }
-    __syncthreads();
 
     f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
-    float m = kNoMax, l = 0.f;  // l: this lane half's share
+    const bool no_max = CAP && BIAS == kBiasNone && sc.c2 <= kNoMaxNeeded;
+    float m = no_max ? 0.f : kNoMax, l = 0.f;  // l: this lane half's share
     const int qpos = row + shift;
 
-    for (int t = 0; t < ntiles; ++t) {
+    auto settle = [&]() {  // what was on its way to LDS is there, and (SPLIT: this wave's) reads are over
+        __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
+        if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
+    };
+    auto step = [&](const T* kt, const T* vt, T* kn, T* vn, int t) {
         const int k0 = t * KT;
-        if (t + 1 < ntiles) {
-            L::load(kb, kg, p.k_stride, k0 + KT, sp.lk - 1);
-            L::load(vb, vg, p.v_stride, k0 + KT, sp.lk - 1);
-        }
-        const T* kt = ks[t & 1];
-        const T* vt = vs[t & 1];
+        if (DOUBLE && t + dt < ntiles) fetch(kn, vn, t + dt);
         if (k0 < wave_most) {
             f32x16 s[NS];
 #pragma unroll
@@ -92,43 +104,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) s[n] = O::mma(L::rows(kt, 32 * n, i, lane), qf[i], s[n]);
             }
-            // scores in log2 units
-            const int rel0 = k0 + 4 * half - qpos;  // relative position of register 0 of sub-tile 0
-            if constexpr (CAP) {
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[n][r] = sc.c2 * sc.template tanh_of<T>(s[n][r]);
-            }
-            const float a = CAP ? 1.f : sc.a;
-            if constexpr (BIAS == kBiasNone) {
-                if constexpr (!CAP) {
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) s[n] *= a;
-                }
-            } else if constexpr (BIAS == kBiasSlopes) {
-                const float rel = (float)rel0;
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[n][r] = s[n][r] * a - slope2 * fabsf(rel + (float)(32 * n + acc_row(r)));
-            } else {
-                const int md = p.bk.max_distance;
-                const int lowest = k0 - (row0 + 31 + shift), highest = k0 + KT - 1 - (row0 + shift);
-                if (highest <= -md || lowest >= md) {
-                    const float b = lut[highest <= -md ? 0 : 2 * md];
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[n][r] = s[n][r] * a + b;
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            s[n][r] = s[n][r] * a + lut[min(max(rel0 + 32 * n + acc_row(r), -md), md) + md];
-                }
-            }
+            if constexpr (CAP) sc.template capped<T>(s);
+            add_bias<BIAS, 1>(s, CAP ? 1.f : sc.a, slope2, lut, p.bk.max_distance, k0 + 4 * half - qpos,
+                              k0 - (row0 + 31 + shift), k0 + KT - 1 - (row0 + shift));
             if (k0 + KT > wave_least) {
                 const int left = my_limit - k0 - 4 * half;
 #pragma unroll
@@ -136,25 +114,28 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[n][r] = 32 * n + acc_row(r) < left ? s[n][r] : -INFINITY;
             }
-            float mx = s[0][0];
+            if (!no_max) {
+                float mx = s[0][0];
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
+                for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
-            mx = fmaxf(mx, other_half(mx));
-            if (__any(mx > m + kLazy)) {
-                const float next = fmaxf(m, mx), keep = exp2_hw(m - next);
-                m = next;
-                l *= keep;
+                    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
+                mx = fmaxf(mx, other_half(mx));
+                if constexpr (RAW) mx *= sc.a;
+                if (__any(mx > m + kLazy)) {
+                    const float next = fmaxf(m, mx), keep = exp2_hw(m - next);
+                    m = next;
+                    l *= keep;
 #pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= keep;
+                    for (int d = 0; d < DT; ++d) o[d] *= keep;
+                }
             }
             float add = 0.f;
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[n][r] = exp2_hw(s[n][r] - m);
+                    s[n][r] = exp2_hw(RAW ? __builtin_fmaf(s[n][r], sc.a, -m) : no_max ? s[n][r] : s[n][r] - m);
                     add += s[n][r];
                 }
             l += add;
@@ -167,14 +148,52 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
                     for (int d = 0; d < DT; ++d) o[d] = O::mma(L::cols(vt, 32 * n, kk, 32 * d, lane), pf, o[d]);
                 }
         }
-        if (t + 1 < ntiles) {
-            L::store(ks[(t + 1) & 1], kb);
-            L::store(vs[(t + 1) & 1], vb);
+        settle();
+        if (!DOUBLE && t + dt < ntiles) {
+            fetch(kn, vn, t + dt);
+            settle();
         }
-        lds_barrier();
+    };
+    settle();
+    if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();  // (the bias is everybody's)
+    for (int t = t0; t < ntiles; t += 2 * dt) {
+        step(ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
+        if (t + dt < ntiles) step(DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);
     }
 
     l += other_half(l);
+    if constexpr (SPLIT) {
+        if (half == 0) {
+            stat[0][32 * wave + lane] = m;
+            stat[1][32 * wave + lane] = l;
+        }
+        __syncthreads();  // (nobody reads a tile any more)
+        Join<T, D>::keep(k_a, v_a, o, lane, wave);
+        if (threadIdx.x < 32) {
+            float top = kNoMax, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[0][32 * w + lane]);
+            float f[kWaves];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                f[w] = exp2_hw(stat[0][32 * w + lane] - top);
+                sum += f[w] * stat[1][32 * w + lane];
+            }
+            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) stat[2][32 * w + lane] = f[w] * inv;
+            if (row < sp.lq && p.lse)
+                p.lse[(sp.q0 + row) * p.H + head] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), d4 = i % (D / 4);
+            if (row0 + r >= sp.lq) break;
+            const f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, stat[2]);
+            store4(static_cast<T*>(p.y) + ((sp.q0 + row0 + r) * p.H + head) * D + 4 * d4, v[0], v[1], v[2], v[3]);
+        }
+        return;
+    }
     if (row >= sp.lq) return;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (an empty row is zero; a NaN stays one)
     T* yg = static_cast<T*>(p.y) + ((sp.q0 + row) * p.H + head) * D;
@@ -187,10 +206,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_kernel(AttnParams p) {
 }
 
 template <typename T, int D, bool CAP, int BIAS>
-int launch_fwd(const AttnParams& p, hipStream_t stream) {
+int launch_fwd(AttnParams p, hipStream_t stream) {
+    const int64_t whole = slots_of(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H;
+    const bool split = whole < kSplitBelow;
+    p.q_slots = (int)slots_of(p.cu_q, p.total_q, p.nseq, split ? kOwn<true> : kOwn<false>);
     const int64_t grid = (int64_t)p.q_slots * p.H;
     if (grid == 0) return 0;
-    hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAP, BIAS>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+    if (split) hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAP, BIAS, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAP, BIAS, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 template <typename T, int D, bool CAP>
@@ -215,9 +238,7 @@ int launch_fwd(const AttnParams& p, int D, int bias, hipStream_t stream) {
 }  // namespace
 }  // namespace attn
 
-int launch_attn_forward(const AttnParams& in, int dtype, int D, int bias, hipStream_t stream) {
-    AttnParams p = in;
-    p.q_slots = (int)attn::slots_of(p.cu_q, p.total_q, p.nseq);
+int launch_attn_forward(const AttnParams& p, int dtype, int D, int bias, hipStream_t stream) {
     return dtype == 1 ? attn::launch_fwd<__bf16>(p, D, bias, stream) : attn::launch_fwd<float>(p, D, bias, stream);
 }
 

@@ -81,6 +81,7 @@ int check_shape(int64_t H, int64_t Hk, int64_t D, int32_t dtype) {
     if (H < 1 || Hk < 1 || H > kMaxHeads || H % Hk != 0 || D < 1) return SSD_ERR_INVALID;
     if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_INVALID;
     if (D != 32 && D != 64 && D != 128) return SSD_ERR_UNSUPPORTED;
+    if (H * D >= ((int64_t)1 << 24)) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
@@ -89,7 +90,8 @@ int check_stride(int64_t given, int64_t dense, int64_t elem, int64_t& out) {
         out = dense;
         return SSD_OK;
     }
-    if (given < dense || given > ((int64_t)1 << 40)) return SSD_ERR_INVALID;
+    // (a tile's byte offsets are 32-bit: 64 rows of up to 2^24 four-byte elements)
+    if (given < dense || given >= ((int64_t)1 << 24)) return SSD_ERR_INVALID;
     if (given * elem % 16 != 0) return SSD_ERR_ALIGN;
     out = given;
     return SSD_OK;

@@ -11,9 +11,11 @@
 // gradients through memory.  Both keep their rows' operands and gradients in registers; the tile layout
 // and operand order are the forward kernel's (ssd_attn_common.h).
 //
-// D is sum_d dy_id y_id, which is as exact as the given y.  The gradient of the table sums dS over whole
-// diagonals, where the error of a bf16 y would be most of the result's, so with a table gradient the
-// query kernel takes D from its definition in a first pass over the keys.
+// D is sum_d dy_id y_id, which is as exact as the given y, and a bf16 y is exact enough for dq and dk.  The
+// gradient of the table sums dS over whole diagonals, where that error would be most of the result's.  But
+// the sum of a row's dS is what the D that it was formed with is off by, so after the pass over all
+// keys D is exact; far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of
+// their p, and the tiles near the diagonal are visited once more with the exact D, for the table alone.
 #include "ssd_attn_common.h"
 
 namespace ssd {
@@ -45,19 +47,24 @@ __device__ __forceinline__ float fold_bucket(const AttnBuckets& b, const float* 
     return v;
 }
 
-template <typename T, int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
+template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_dq_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
-    constexpr int KT = O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
-    __shared__ __attribute__((aligned(16))) T ks[2][L::kElems];
-    __shared__ __attribute__((aligned(16))) T vs[2][L::kElems];
+    constexpr int OWN = kOwn<SPLIT>, KT = SPLIT ? 32 : O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
+    constexpr int ELEMS = (SPLIT ? kWaves : 1) * KT * D;
+    constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;
+    __shared__ __attribute__((aligned(16))) T k_a[ELEMS];
+    __shared__ __attribute__((aligned(16))) T v_a[ELEMS];
+    __shared__ __attribute__((aligned(16))) T k_b[DOUBLE ? ELEMS : 8];
+    __shared__ __attribute__((aligned(16))) T v_b[DOUBLE ? ELEMS : 8];
+    __shared__ float off_by[SPLIT ? kWaves * 32 : 1];
     extern __shared__ float extra[];
 
     int slot, head;
     work_item(blockIdx.x, p.q_slots, p.H, slot, head);
-    const Span sp = find_span(p, slot, false);
+    const Span sp = find_span(p, slot, OWN, false);
     const bool grad = BIAS == kBiasBuckets && p.dtable != nullptr;
     float* part = grad ? p.table_part + ((int64_t)slot * p.H + head) * p.bk.total : nullptr;
     if (sp.tile < 0) {
@@ -66,13 +73,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
         return;
     }
     const int kvh = head / (p.H / p.Hk);
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, half = lane / 32;
+    const int lane = threadIdx.x % kWave, half = lane / 32;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int shift = sp.lk - sp.lq;
     int prefix = 0;
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
     auto limit = [&](int i) { return p.causal ? max(min(max(i + shift + 1, prefix), sp.lk), 0) : sp.lk; };
-    const int row0 = sp.tile * kBM + wave * 32, row = row0 + lane % 32;
-    const int wg_limit = limit(min(sp.tile * kBM + kBM, sp.lq) - 1);
+    const int row0 = sp.tile * OWN + (SPLIT ? 0 : wave * 32), row = row0 + lane % 32;
+    const int wg_limit = limit(min(sp.tile * OWN + OWN, sp.lq) - 1);
     const int ntiles = (wg_limit + KT - 1) / KT;
     const int my_limit = row < sp.lq ? limit(row) : 0;
     const int wave_most = row0 < sp.lq ? limit(min(row0 + 32, sp.lq) - 1) : 0;
@@ -80,8 +88,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
 
     const T* kg = static_cast<const T*>(p.k) + sp.k0 * p.k_stride + (int64_t)kvh * D;
     const T* vg = static_cast<const T*>(p.v) + sp.k0 * p.v_stride + (int64_t)kvh * D;
-    const int64_t mine = (sp.q0 + min(row, sp.lq - 1)) * p.H + head;  // this lane's (query, head)
+    Feed<T, D, KT, SPLIT ? kWave : kThreads> kf, vf;
+    kf.init(p.k_stride);
+    vf.init(p.v_stride);
+    const int at = SPLIT ? wave * KT * D : 0;
+    T *ka = k_a + at, *va = v_a + at, *kb = k_b + (DOUBLE ? at : 0), *vb = v_b + (DOUBLE ? at : 0);
+    auto fetch = [&](T* ks, T* vs, int t) {
+        kf.load(ks, kg, t * KT, sp.lk - t * KT);
+        vf.load(vs, vg, t * KT, sp.lk - t * KT);
+    };
+    const int t0 = SPLIT ? wave : 0, dt = SPLIT ? kWaves : 1;
+    if (t0 < ntiles) fetch(ka, va, t0);
 
+    const int64_t mine = (sp.q0 + min(row, sp.lq - 1)) * p.H + head;  // this lane's (query, head)
     Frag qf[NT], gf[NT];
     float delta = 0.f;
     {
@@ -90,10 +109,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
         const T* yg = static_cast<const T*>(p.y) + mine * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int at = (2 * t + half) * O::kE;
-            qf[t] = __builtin_bit_cast(Frag, ld16(qg + at));
-            gf[t] = __builtin_bit_cast(Frag, ld16(gg + at));
-            const Frag yf = __builtin_bit_cast(Frag, ld16(yg + at));
+            const int e0 = (2 * t + half) * O::kE;
+            qf[t] = signed_frag<T>(qg + e0, p.scale);
+            gf[t] = __builtin_bit_cast(Frag, ld16(gg + e0));
+            const Frag yf = __builtin_bit_cast(Frag, ld16(yg + e0));
 #pragma unroll
             for (int e = 0; e < O::kE; ++e) delta += (float)gf[t][e] * (float)yf[e];
         }
@@ -104,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
     if (lse2 == -INFINITY || row >= sp.lq) lse2 = INFINITY;
 
     Score sc;
-    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
+    sc.init<T>(p.scale, p.cap, CAP);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     const int md = p.bk.max_distance, reach = 2 * md + 1;
@@ -117,141 +136,166 @@ __global__ void __launch_bounds__(kThreads, 2) attn_dq_kernel(AttnParams p) {
         if (grad)
             for (int i = lane; i < reach; i += kWave) sums[i] = 0.f;
     }
-    float far_lo = 0.f, far_hi = 0.f;
+    // far cells' dS and p, below (first) and above the reach, and the row's sum of dS
+    float far_ds[2] = {0.f, 0.f}, far_p[2] = {0.f, 0.f}, row_ds = 0.f;
     const int qpos = row + shift;
 
     f32x16 acc[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
 
-    uint4 kb[L::kLoads], vb[L::kLoads];
-    for (int pass = grad ? 0 : 1; pass < 2; ++pass) {
-        float exact = 0.f;
-        if (ntiles > 0) {
-            L::load(kb, kg, p.k_stride, 0, sp.lk - 1);
-            L::load(vb, vg, p.v_stride, 0, sp.lk - 1);
-            L::store(ks[0], kb);
-            L::store(vs[0], vb);
+    auto settle = [&]() {
+        __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
+        if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
+    };
+    // p and dS of 32 keys from kn on (dS before the cap's derivative, which is returned in `slope`); true: some
+    // are nearer than the table's reach
+    auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope) {
+        f32x16 x[1] = {f32x16{}}, dp{};
+#pragma unroll
+        for (int i = 0; i < NT; ++i) x[0] = O::mma(L::rows(kt, 32 * n, i, lane), qf[i], x[0]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, lane), gf[i], dp);
+        if constexpr (CAP) {
+            sc.template capped<T>(x);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) slope[r] = sc.slope(x[0][r]);
         }
-        __syncthreads();
-        for (int t = 0; t < ntiles; ++t) {
-            const int k0 = t * KT;
-            if (t + 1 < ntiles) {
-                L::load(kb, kg, p.k_stride, k0 + KT, sp.lk - 1);
-                L::load(vb, vg, p.v_stride, k0 + KT, sp.lk - 1);
-            }
-            const T* kt = ks[t & 1];
-            const T* vt = vs[t & 1];
-            if (k0 < wave_most) {
+        const bool near = add_bias<BIAS, 1>(x, CAP ? 1.f : sc.a, slope2, lut, md, kn + 4 * half - qpos, kn - (row0 + 31 + shift),
+                                            kn + 31 - (row0 + shift));
+        if (kn + 32 > wave_least) {
+            const int left = my_limit - kn - 4 * half;
 #pragma unroll
-                for (int n = 0; n < NS; ++n) {
-                    f32x16 s{}, dp{};
+            for (int r = 0; r < 16; ++r) x[0][r] = acc_row(r) < left ? x[0][r] : -INFINITY;
+        }
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) s = O::mma(L::rows(kt, 32 * n, i, lane), qf[i], s);
+        for (int r = 0; r < 16; ++r) {
+            s[r] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x[0][r], sc.a, -lse2) : x[0][r] - lse2);
+            ds[r] = s[r] * (dp[r] - delta);
+        }
+        return near;
+    };
+    auto step = [&](const T* kt, const T* vt, T* kn_, T* vn_, int t) {
+        const int k0 = t * KT;
+        if (DOUBLE && t + dt < ntiles) fetch(kn_, vn_, t + dt);
+        if (k0 < wave_most) {
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, lane), gf[i], dp);
-                    const int kn = k0 + 32 * n, rel0 = kn + 4 * half - qpos;
-                    f32x16 slope;  // derivative of the cap
-                    if constexpr (CAP) {
+            for (int n = 0; n < NS; ++n) {
+                const int kn = k0 + 32 * n;
+                f32x16 s, ds, slope;
+                const bool near = weights(kt, vt, n, kn, s, ds, slope);
+                if constexpr (BIAS == kBiasBuckets) {
+                    if (grad) {
+                        float a = 0.f, b = 0.f;
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            const float u = sc.template tanh_of<T>(s[r]);
-                            s[r] = sc.c2 * u;
-                            slope[r] = 1.f - u * u;
+                            a += ds[r];
+                            b += s[r];
                         }
+                        row_ds += a;
+                        const bool above = kn >= row0 + shift;
+                        far_ds[0] += near || above ? 0.f : a;
+                        far_p[0] += near || above ? 0.f : b;
+                        far_ds[1] += near || !above ? 0.f : a;
+                        far_p[1] += near || !above ? 0.f : b;
                     }
-                    const float a = CAP ? 1.f : sc.a;
-                    bool near = false;
-                    if constexpr (BIAS == kBiasNone) {
-                        if constexpr (!CAP) s *= a;
-                    } else if constexpr (BIAS == kBiasSlopes) {
-                        const float rel = (float)rel0;
+                }
+                if constexpr (CAP) ds *= slope;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] = s[r] * a - slope2 * fabsf(rel + (float)acc_row(r));
-                    } else {
-                        const int lowest = kn - (row0 + 31 + shift), highest = kn + 31 - (row0 + shift);
-                        near = highest > -md && lowest < md;
-                        if (!near) {
-                            const float b = lut[highest <= -md ? 0 : 2 * md];
+                for (int kk = 0; kk < PK; ++kk) {
+                    const Frag sf = O::pack(ds, kk);
 #pragma unroll
-                            for (int r = 0; r < 16; ++r) s[r] = s[r] * a + b;
-                        } else {
+                    for (int d = 0; d < DT; ++d) acc[d] = O::mma(L::cols(kt, 32 * n, kk, 32 * d, lane), sf, acc[d]);
+                }
+            }
+        }
+        settle();
+        if (!DOUBLE && t + dt < ntiles) {
+            fetch(kn_, vn_, t + dt);
+            settle();
+        }
+    };
+    settle();
+    if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();
+    for (int t = t0; t < ntiles; t += 2 * dt) {
+        step(ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
+        if (t + dt < ntiles) step(DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);
+    }
+
+    if constexpr (SPLIT) {
+        __syncthreads();
+        Join<T, D>::keep(k_a, v_a, acc, lane, wave);
+        row_ds += other_half(row_ds);
+        if (half == 0) off_by[32 * wave + lane] = row_ds;
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), d4 = i % (D / 4);
+            if (row0 + r >= sp.lq) break;
+            const f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, nullptr) * p.scale;
+            store4(static_cast<T*>(p.dq) + ((sp.q0 + row0 + r) * p.H + head) * D + 4 * d4, v[0], v[1], v[2], v[3]);
+        }
+        row_ds = 0.f;
 #pragma unroll
-                            for (int r = 0; r < 16; ++r) s[r] = s[r] * a + lut[min(max(rel0 + acc_row(r), -md), md) + md];
+        for (int w = 0; w < kWaves; ++w) row_ds += off_by[32 * w + lane % 32];
+        __syncthreads();  // (the tiles are free again)
+    } else {
+        row_ds += other_half(row_ds);
+        if (row < sp.lq) {
+            T* out = static_cast<T*>(p.dq) + mine * D;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                acc[d] *= p.scale;
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    store4(out + 32 * d + 2 * r + 4 * half, acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]);
+            }
+        }
+    }
+    if (grad) delta += row_ds;
+    if (row < sp.lq && half == 0 && (!SPLIT || wave == 0)) p.delta[mine] = delta;
+    if constexpr (BIAS == kBiasBuckets) {
+        if (!grad) return;
+        float far_lo = far_ds[0] - row_ds * far_p[0], far_hi = far_ds[1] - row_ds * far_p[1];
+        // tiles with a relative position inside the reach of any of the workgroup's queries
+        const int q_first = sp.tile * OWN + shift, q_last = q_first + OWN - 1;
+        const int n0 = max(q_first - md, 0) / KT, n1 = min(ntiles, q_last + md < 0 ? 0 : (q_last + md) / KT + 1);
+        for (int t = n0 + t0; t < n1; t += dt) {
+            const int k0 = t * KT;
+            fetch(ka, va, t);
+            settle();
+            if (k0 < wave_most) {
+#pragma unroll 1
+                for (int n = 0; n < NS; ++n) {
+                    const int kn = k0 + 32 * n;
+                    if (kn + 31 - (row0 + shift) <= -md || kn - (row0 + 31 + shift) >= md) continue;
+                    f32x16 s, ds, slope;
+                    weights(ka, va, n, kn, s, ds, slope);
+                    // sums along the diagonals of 16 keys x 32 queries: lane j takes relative position
+                    // base + j, from the corner key 0, query 31 on
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) block[(acc_row(r) + 4 * half) * kDiagStride + lane % 32] = ds[8 * b + r];
+                        __builtin_amdgcn_wave_barrier();
+                        const int off = lane - 31, rel = kn + 16 * b - (row0 + shift) + off;
+                        float add = 0.f;
+#pragma unroll
+                        for (int key = 0; key < kDiagRows; ++key) {
+                            const int q = key - off;
+                            const float x = block[key * kDiagStride + min(max(q, 0), 31)];
+                            add += q >= 0 && q < 32 ? x : 0.f;
                         }
-                    }
-                    if (kn + 32 > wave_least) {
-                        const int left = my_limit - kn - 4 * half;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] = acc_row(r) < left ? s[r] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = exp2_hw(s[r] - lse2);
-                    if (pass == 0) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) exact += s[r] * dp[r];
-                        continue;
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
-                    if constexpr (BIAS == kBiasBuckets) {
-                        if (grad && !near) {
-                            float add = 0.f;
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) add += s[r];
-                            if (kn < row0 + shift) far_lo += add; else far_hi += add;
-                        } else if (grad) {
-                            // sums along the diagonals of 16 keys x 32 queries: lane j takes relative
-                            // position base + j, from the corner key 0, query 31 on
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                                for (int r = 0; r < 8; ++r) block[(acc_row(r) + 4 * half) * kDiagStride + lane % 32] = s[8 * b + r];
-                                __builtin_amdgcn_wave_barrier();
-                                const int off = lane - 31, rel = kn + 16 * b - (row0 + shift) + off;
-                                float add = 0.f;
-                                for (int key = max(off, 0); key < kDiagRows && key - off < 32; ++key)
-                                    add += block[key * kDiagStride + key - off];
-                                if (lane < 31 + kDiagRows) {
-                                    if (rel <= -md) far_lo += add;
-                                    else if (rel >= md) far_hi += add;
-                                    else sums[rel + md] += add;
-                                }
-                                __builtin_amdgcn_wave_barrier();
-                            }
+                        if (lane < 31 + kDiagRows) {
+                            if (rel <= -md) far_lo += add;
+                            else if (rel >= md) far_hi += add;
+                            else sums[rel + md] += add;
                         }
-                    }
-                    if constexpr (CAP) s *= slope;
-#pragma unroll
-                    for (int kk = 0; kk < PK; ++kk) {
-                        const Frag sf = O::pack(s, kk);
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) acc[d] = O::mma(L::cols(kt, 32 * n, kk, 32 * d, lane), sf, acc[d]);
+                        __builtin_amdgcn_wave_barrier();
                     }
                 }
             }
-            if (t + 1 < ntiles) {
-                L::store(ks[(t + 1) & 1], kb);
-                L::store(vs[(t + 1) & 1], vb);
-            }
-            lds_barrier();
+            settle();
         }
-        if (pass == 0) delta = exact + other_half(exact);
-    }
-
-    if (row < sp.lq) {
-        if (half == 0) p.delta[mine] = delta;
-        T* out = static_cast<T*>(p.dq) + mine * D;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            acc[d] *= p.scale;
-#pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                store4(out + 32 * d + 2 * r + 4 * half, acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]);
-        }
-    }
-    if constexpr (BIAS == kBiasBuckets) {
-        if (!grad) return;
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1) {
             far_lo += __shfl_xor(far_lo, off, kWave);
@@ -290,37 +334,71 @@ __global__ void __launch_bounds__(kThreads) attn_dtable_kernel(AttnParams p) {
     }
 }
 
-template <typename T, int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(kThreads, sizeof(T) * D >= 256 ? 1 : 2) attn_dkv_kernel(AttnParams p) {
+template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 2) attn_dkv_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
-    constexpr int QT = O::kKT, NS = QT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
-    __shared__ __attribute__((aligned(16))) T qs[2][L::kElems];
-    __shared__ __attribute__((aligned(16))) T gs[2][L::kElems];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][QT];  // [buffer][lse in log2 units, D][query]
+    constexpr int OWN = kOwn<SPLIT>, QT = SPLIT ? 32 : O::kKT, NS = QT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
+    constexpr int COPIES = SPLIT ? kWaves : 1, ELEMS = COPIES * QT * D, THREADS = SPLIT ? kWave : kThreads;
+    constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;
+    __shared__ __attribute__((aligned(16))) T q_a[ELEMS];
+    __shared__ __attribute__((aligned(16))) T g_a[ELEMS];
+    __shared__ __attribute__((aligned(16))) T q_b[DOUBLE ? ELEMS : 8];
+    __shared__ __attribute__((aligned(16))) T g_b[DOUBLE ? ELEMS : 8];
+    __shared__ __attribute__((aligned(16))) float stat[2][COPIES][2][QT];  // [buffer][wave][lse in log2 units, D][query]
     extern __shared__ float extra[];
     float* lut = extra;
 
     int slot, kvh;
     work_item(blockIdx.x, p.k_slots, p.Hk, slot, kvh);
     slot = p.k_slots - 1 - slot;  // under a causal mask the first keys are seen by the most queries
-    const Span sp = find_span(p, slot, true);
+    const Span sp = find_span(p, slot, OWN, true);
     if (sp.tile < 0) return;
     const int group = p.H / p.Hk;
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, half = lane / 32;
+    const int lane = threadIdx.x % kWave, half = lane / 32;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int shift = sp.lk - sp.lq;
     int prefix = 0;
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
 
     // queries [first(j), lq) see key j
     auto first = [&](int j) { return !p.causal || j < prefix ? 0 : max(j - shift, 0); };
-    const int row0 = sp.tile * kBM + wave * 32, key = row0 + lane % 32;
-    const int t0 = first(sp.tile * kBM) / QT, t1 = (sp.lq + QT - 1) / QT;
+    const int row0 = sp.tile * OWN + (SPLIT ? 0 : wave * 32), key = row0 + lane % 32;
+    const int t0 = first(sp.tile * OWN) / QT, t1 = (sp.lq + QT - 1) / QT;
     const int my_first = key < sp.lk ? first(key) : sp.lq;
     const int wave_least = row0 < sp.lk ? first(row0) : sp.lq;  // the earliest query that any key of the wave meets
     const int wave_most = row0 + 32 <= sp.lk ? first(row0 + 31) : sp.lq;  // from here on every key meets every query
     const int per_head = max(t1 - t0, 0), ntiles = per_head * group;
+
+    Feed<T, D, QT, THREADS> qf, gf;
+    qf.init(p.q_stride);
+    gf.init((int64_t)p.H * D);
+    const int tid = SPLIT ? lane : (int)threadIdx.x;
+    // a tile's queries and dy go straight to LDS; its statistics (threads 0 .. QT - 1: lse, the next QT: D) wait in a
+    // register until then
+    float sb = 0.f;
+    auto fetch = [&](T* qs, T* gs, int it) {
+        const int head = kvh * group + it / per_head, row = (t0 + it % per_head) * QT;
+        qf.load(qs, static_cast<const T*>(p.q) + sp.q0 * p.q_stride + (int64_t)head * D, row, sp.lq - row);
+        gf.load(gs, static_cast<const T*>(p.dy) + (sp.q0 * p.H + head) * D, row, sp.lq - row);
+        if (tid < 2 * QT) {
+            const int64_t at = (sp.q0 + min(row + tid % QT, sp.lq - 1)) * p.H + head;
+            sb = tid < QT ? p.lse[at] * kLog2e : p.delta[at];
+            if (tid < QT && sb == -INFINITY) sb = INFINITY;  // (sees nothing: all its weights are zero)
+        }
+    };
+    const int copy = SPLIT ? wave : 0;
+    auto settle = [&](int buf) {  // (every thread's statistics of the next tile, where it has fetched any)
+        if (tid < 2 * QT) stat[buf][copy][tid / QT][tid % QT] = sb;
+        __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
+        if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
+    };
+    const int at = copy * QT * D;
+    T *qa = q_a + at, *ga = g_a + at, *qb = q_b + (DOUBLE ? at : 0), *gb = g_b + (DOUBLE ? at : 0);
+    // SPLIT: a wave takes every fourth tile
+    const int i0 = SPLIT ? wave : 0, di = SPLIT ? kWaves : 1;
+    if (i0 < ntiles) fetch(qa, ga, i0);
 
     const int64_t krow = sp.k0 + min(key, sp.lk - 1);
     Frag kf[NT], vf[NT];
@@ -329,114 +407,78 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) * D >= 256 ? 1 : 2) attn_d
         const T* vg = static_cast<const T*>(p.v) + krow * p.v_stride + (int64_t)kvh * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            kf[t] = __builtin_bit_cast(Frag, ld16(kg + (2 * t + half) * O::kE));
+            kf[t] = signed_frag<T>(kg + (2 * t + half) * O::kE, p.scale);
             vf[t] = __builtin_bit_cast(Frag, ld16(vg + (2 * t + half) * O::kE));
         }
     }
     Score sc;
-    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
+    sc.init<T>(p.scale, p.cap, CAP);
     const int md = p.bk.max_distance;
+    if constexpr (BIAS == kBiasBuckets) {
+        // one head's bias, refilled where the head changes; SPLIT: the waves are on different heads at a time,
+        // so that every head's is there at once
+        if constexpr (SPLIT)
+            for (int h = 0; h < group; ++h) fill_bias(lut + h * (2 * md + 1), p, kvh * group + h);
+        else fill_bias(lut, p, kvh * group);
+    }
 
     f32x16 dk[DT], dv[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) dk[d] = dv[d] = f32x16{};
 
-    uint4 qb[L::kLoads], gb[L::kLoads];
-    float sb = 0.f;  // threads 0 .. QT - 1: lse, the next QT: D
-    auto fetch = [&](int it) {
-        const int head = kvh * group + it / per_head, first_row = (t0 + it % per_head) * QT;
-        L::load(qb, static_cast<const T*>(p.q) + sp.q0 * p.q_stride + (int64_t)head * D, p.q_stride, first_row, sp.lq - 1);
-        L::load(gb, static_cast<const T*>(p.dy) + (sp.q0 * p.H + head) * D, (int64_t)p.H * D, first_row, sp.lq - 1);
-        if (threadIdx.x < 2 * QT) {
-            const int64_t at = (sp.q0 + min(first_row + (int)threadIdx.x % QT, sp.lq - 1)) * p.H + head;
-            if (threadIdx.x < QT) {
-                sb = p.lse[at] * kLog2e;
-                if (sb == -INFINITY) sb = INFINITY;
-            } else {
-                sb = p.delta[at];
-            }
-        }
-    };
-    auto put = [&](int buf) {
-        L::store(qs[buf], qb);
-        L::store(gs[buf], gb);
-        if (threadIdx.x < 2 * QT) stat[buf][threadIdx.x / QT][threadIdx.x % QT] = sb;
-    };
-    if (ntiles > 0) {
-        fetch(0);
-        put(0);
-    }
-
-    for (int it = 0; it < ntiles; ++it) {
-        const int head = kvh * group + it / per_head, q0 = (t0 + it % per_head) * QT;
+    auto step = [&](const T* qt, const T* gt, T* qn_, T* gn_, int it, int buf) {
+        const int h = it / per_head, head = kvh * group + h, q0 = (t0 + it % per_head) * QT;
+        const float* bias = lut;
         if constexpr (BIAS == kBiasBuckets) {
-            if (it % per_head == 0) {  // (the barrier at the end of the last round: nobody reads the old one)
+            if constexpr (SPLIT) {
+                bias = lut + h * (2 * md + 1);
+            } else if (h > 0 && it % per_head == 0) {  // (the barrier before this: nobody reads the old one)
                 fill_bias(lut, p, head);
+                __syncthreads();
             }
         }
-        if (it == 0 || (BIAS == kBiasBuckets && it % per_head == 0)) __syncthreads();
         float slope2 = 0.f;
         if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
-        if (it + 1 < ntiles) fetch(it + 1);
-        const T* qt = qs[it & 1];
-        const T* gt = gs[it & 1];
+        if (DOUBLE && it + di < ntiles) fetch(qn_, gn_, it + di);
         if (q0 + QT > wave_least) {
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                f32x16 s{}, dp{};
+                f32x16 s[1] = {f32x16{}}, dp{};
 #pragma unroll
-                for (int i = 0; i < NT; ++i) s = O::mma(L::rows(qt, 32 * n, i, lane), kf[i], s);
+                for (int i = 0; i < NT; ++i) s[0] = O::mma(L::rows(qt, 32 * n, i, lane), kf[i], s[0]);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(gt, 32 * n, i, lane), vf[i], dp);
                 const int qn = q0 + 32 * n;
-                const int rel0 = key - (qn + shift + 4 * half);  // of register 0; later queries are further on
                 f32x16 slope;
                 if constexpr (CAP) {
+                    sc.template capped<T>(s);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float u = sc.template tanh_of<T>(s[r]);
-                        s[r] = sc.c2 * u;
-                        slope[r] = 1.f - u * u;
-                    }
+                    for (int r = 0; r < 16; ++r) slope[r] = sc.slope(s[0][r]);
                 }
-                const float a = CAP ? 1.f : sc.a;
-                if constexpr (BIAS == kBiasNone) {
-                    if constexpr (!CAP) s *= a;
-                } else if constexpr (BIAS == kBiasSlopes) {
-                    const float rel = (float)rel0;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = s[r] * a - slope2 * fabsf(rel - (float)acc_row(r));
-                } else {
-                    const int lowest = row0 - (qn + 31 + shift), highest = row0 + 31 - (qn + shift);
-                    if (highest <= -md || lowest >= md) {
-                        const float b = lut[highest <= -md ? 0 : 2 * md];
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] = s[r] * a + b;
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] = s[r] * a + lut[min(max(rel0 - acc_row(r), -md), md) + md];
-                    }
-                }
+                // (of register 0; later queries are further back)
+                add_bias<BIAS, -1>(s, CAP ? 1.f : sc.a, slope2, bias, md, key - (qn + shift + 4 * half), row0 - (qn + 31 + shift),
+                                   row0 + 31 - (qn + shift));
                 if (qn < wave_most || qn + 32 > sp.lq) {
                     const int lo = my_first - qn - 4 * half, hi = sp.lq - qn - 4 * half;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = acc_row(r) >= lo && acc_row(r) < hi ? s[r] : -INFINITY;
+                    for (int r = 0; r < 16; ++r) s[0][r] = acc_row(r) >= lo && acc_row(r) < hi ? s[0][r] : -INFINITY;
                 }
-                const float* ls = &stat[it & 1][0][32 * n + 4 * half];
-                const float* de = &stat[it & 1][1][32 * n + 4 * half];
+                const float* ls = &stat[buf][copy][0][32 * n + 4 * half];
+                const float* de = &stat[buf][copy][1][32 * n + 4 * half];
 #pragma unroll
                 for (int r = 0; r < 16; r += 4) {
                     const f32x4 lv = as_f32x4(ld16(ls + acc_row(r))), dl = as_f32x4(ld16(de + acc_row(r)));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[r + e] = exp2_hw(s[r + e] - lv[e]);
-                        dp[r + e] = s[r + e] * (dp[r + e] - dl[e]);
+                        const float x = s[0][r + e];
+                        s[0][r + e] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x, sc.a, -lv[e]) : x - lv[e]);
+                        dp[r + e] = s[0][r + e] * (dp[r + e] - dl[e]);
                     }
                 }
                 if constexpr (CAP) dp *= slope;
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk) {
-                    const Frag pf = O::pack(s, kk), sf = O::pack(dp, kk);
+                    const Frag pf = O::pack(s[0], kk), sf = O::pack(dp, kk);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         dv[d] = O::mma(L::cols(gt, 32 * n, kk, 32 * d, lane), pf, dv[d]);
@@ -445,10 +487,37 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) * D >= 256 ? 1 : 2) attn_d
                 }
             }
         }
-        if (it + 1 < ntiles) put((it + 1) & 1);
-        lds_barrier();
+        if constexpr (!DOUBLE) {
+            settle(1);  // (a buffer that nobody reads)
+            if (it + di < ntiles) fetch(qn_, gn_, it + di);
+            settle(0);
+        } else {
+            settle(buf ^ 1);
+        }
+    };
+    settle(0);
+    if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();
+    for (int it = i0; it < ntiles; it += 2 * di) {
+        step(qa, ga, DOUBLE ? qb : qa, DOUBLE ? gb : ga, it, 0);
+        if (it + di < ntiles) step(DOUBLE ? qb : qa, DOUBLE ? gb : ga, qa, ga, it + di, DOUBLE ? 1 : 0);
     }
 
+    if constexpr (SPLIT) {
+        auto write = [&](const f32x16(&acc)[DT], void* to, float scale) {
+            __syncthreads();
+            Join<T, D>::keep(q_a, g_a, acc, lane, wave);
+            __syncthreads();
+            for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), d4 = i % (D / 4);
+                if (row0 + r >= sp.lk) break;
+                const f32x4 v = Join<T, D>::sum(q_a, g_a, r, d4, nullptr) * scale;
+                store4(static_cast<T*>(to) + ((sp.k0 + row0 + r) * p.Hk + kvh) * D + 4 * d4, v[0], v[1], v[2], v[3]);
+            }
+        };
+        write(dk, p.dk, p.scale);
+        write(dv, p.dv, 1.f);
+        return;
+    }
     if (key >= sp.lk) return;
     T* dkg = static_cast<T*>(p.dk) + ((sp.k0 + key) * p.Hk + kvh) * D;
     T* dvg = static_cast<T*>(p.dv) + ((sp.k0 + key) * p.Hk + kvh) * D;
@@ -463,31 +532,42 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) * D >= 256 ? 1 : 2) attn_d
     }
 }
 
+// Bytes of LDS that a workgroup may have (160 KB), less the largest fixed part of a split kernel.
+constexpr size_t kSplitBiasLds = 163840 - 139264;
+
+template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+int launch_dq(AttnParams p, hipStream_t stream) {
+    p.q_slots = (int)slots_of(p.cu_q, p.total_q, p.nseq, kOwn<SPLIT>);
+    const int64_t grid = (int64_t)p.q_slots * p.H;
+    const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr);
+    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dq_kernel<T, D, CAP, BIAS, SPLIT>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+        return -1;
+    if (grid > 0) hipLaunchKernelGGL((attn_dq_kernel<T, D, CAP, BIAS, SPLIT>), dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
+    if (p.dtable) hipLaunchKernelGGL(attn_dtable_kernel, dim3((unsigned)p.H), dim3(kThreads), 0, stream, p);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+int launch_dkv(AttnParams p, hipStream_t stream) {
+    p.k_slots = (int)slots_of(p.cu_k, p.total_k, p.nseq, kOwn<SPLIT>);
+    const int64_t grid = (int64_t)p.k_slots * p.Hk;
+    const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (SPLIT ? p.H / p.Hk : 1);
+    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dkv_kernel<T, D, CAP, BIAS, SPLIT>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+        return -1;
+    if (grid > 0) hipLaunchKernelGGL((attn_dkv_kernel<T, D, CAP, BIAS, SPLIT>), dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
 template <typename T, int D, bool CAP, int BIAS>
 int launch_bwd(const AttnParams& p, hipStream_t stream) {
-    const int64_t q_grid = (int64_t)p.q_slots * p.H, k_grid = (int64_t)p.k_slots * p.Hk;
-    const size_t q_lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr);
-    const size_t k_lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false);
-    if (BIAS == kBiasBuckets) {
-        if (hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dq_kernel<T, D, CAP, BIAS>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)q_lds) != hipSuccess ||
-            hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dkv_kernel<T, D, CAP, BIAS>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)k_lds) != hipSuccess)
-            return -1;
-    }
-    if (q_grid > 0) {
-        hipLaunchKernelGGL((attn_dq_kernel<T, D, CAP, BIAS>), dim3((unsigned)q_grid), dim3(kThreads), q_lds, stream, p);
-        if (hipGetLastError() != hipSuccess) return -1;
-    }
-    if (p.dtable) {
-        hipLaunchKernelGGL(attn_dtable_kernel, dim3((unsigned)p.H), dim3(kThreads), 0, stream, p);
-        if (hipGetLastError() != hipSuccess) return -1;
-    }
-    if (k_grid > 0) {
-        hipLaunchKernelGGL((attn_dkv_kernel<T, D, CAP, BIAS>), dim3((unsigned)k_grid), dim3(kThreads), k_lds, stream, p);
-        if (hipGetLastError() != hipSuccess) return -1;
-    }
-    return 0;
+    // (a bias for every head of a group, or the sums by distance, may not fit beside a split kernel's tiles)
+    const bool dq_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr) <= kSplitBiasLds;
+    const bool dkv_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (p.H / p.Hk) <= kSplitBiasLds;
+    const bool dq_split = dq_fits && slots_of(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H < kSplitBelow;
+    const bool dkv_split = dkv_fits && slots_of(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
+    int rc = dq_split ? launch_dq<T, D, CAP, BIAS, true>(p, stream) : launch_dq<T, D, CAP, BIAS, false>(p, stream);
+    if (rc == 0) rc = dkv_split ? launch_dkv<T, D, CAP, BIAS, true>(p, stream) : launch_dkv<T, D, CAP, BIAS, false>(p, stream);
+    return rc;
 }
 template <typename T, int D, bool CAP>
 int launch_bwd(const AttnParams& p, int bias, hipStream_t stream) {
@@ -511,10 +591,7 @@ int launch_bwd(const AttnParams& p, int D, int bias, hipStream_t stream) {
 }  // namespace
 }  // namespace attn
 
-int launch_attn_backward(const AttnParams& in, int dtype, int D, int bias, hipStream_t stream) {
-    AttnParams p = in;
-    p.q_slots = (int)attn::slots_of(p.cu_q, p.total_q, p.nseq);
-    p.k_slots = (int)attn::slots_of(p.cu_k, p.total_k, p.nseq);
+int launch_attn_backward(const AttnParams& p, int dtype, int D, int bias, hipStream_t stream) {
     return dtype == 1 ? attn::launch_bwd<__bf16>(p, D, bias, stream) : attn::launch_bwd<float>(p, D, bias, stream);
 }
 

@@ -25,7 +25,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 // start of a running maximum (log2 units): below any finite score, and finite, so that a row that
 // has seen nothing but masked scores (minus infinity) takes exp2(-inf) = 0 and not a NaN
 constexpr float kNoMax = -1e30f;
-constexpr int kBM = 128;  // rows of a workgroup's own tile: 4 waves of 32
+// Rows of a workgroup's own tile.  With enough work for the chip each of its four waves owns 32 rows and they
+// share what they stream.  With too little (SPLIT) all four own the same 32 rows, each streams every
+// fourth tile through LDS of its own, and their results are joined at the end: four times the
+// workgroups, and a quarter of the way for each.
+template <bool SPLIT> constexpr int kOwn = SPLIT ? 32 : 128;
+// Workgroups of 128 rows below which the waves split instead.
+constexpr int64_t kSplitBelow = 512;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -68,10 +74,6 @@ template <typename T, int D> struct Tile {
     static constexpr int RB = D * (int)sizeof(T);
     static constexpr int RPB = RB >= 256 ? 1 : 256 / RB;
     static constexpr int MASK = CH / 2 - 1 < 7 ? CH / 2 - 1 : 7;
-    static constexpr int kRows = Op<T>::kKT;
-    static constexpr int kElems = kRows * D;
-    static constexpr int kLoads = kRows * CH / kThreads;  // 16-byte chunks a thread stages
-    static_assert(kRows * CH % kThreads == 0, "every thread stages whole chunks");
     static __device__ __forceinline__ int swz(int row) { return 2 * ((row / RPB) & MASK); }
     static __device__ __forceinline__ int at(int row, int c) { return (row * CH + (c ^ swz(row))) * kE; }
 
@@ -83,24 +85,6 @@ template <typename T, int D> struct Tile {
     // operand whose index is a column (lane % 32 of col0 ..), contracting over rows row0 + kK * kk ..
     // in the row order of an accumulator (see the top of this file)
     static __device__ __forceinline__ typename Op<T>::Frag cols(const T* s, int row0, int kk, int col0, int lane);
-
-    // global -> registers: rows first .. of a [tokens][stride] tensor, rows past `last` read as `last`
-    // (a copy of a real row, whose weight is zero)
-    static __device__ __forceinline__ void load(uint4 (&buf)[kLoads], const T* g, int64_t stride, int first, int last) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int idx = (int)threadIdx.x + kThreads * i;
-            const int row = min(first + idx / CH, last);
-            buf[i] = ld16(g + (int64_t)row * stride + (idx % CH) * kE);
-        }
-    }
-    static __device__ __forceinline__ void store(T* s, const uint4 (&buf)[kLoads]) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int idx = (int)threadIdx.x + kThreads * i;
-            st16(s + at(idx / CH, idx % CH), buf[i]);
-        }
-    }
 };
 
 template <typename T, int D>
@@ -124,6 +108,52 @@ __device__ __forceinline__ typename Op<T>::Frag Tile<T, D>::cols(const T* s, int
         return v;
     }
 }
+
+// What the kernels know a wave's outstanding memory operations by (s_waitcnt of gfx9: vmcnt in bits 3:0 and
+// 15:14, expcnt in 6:4, lgkmcnt in 11:8): everything loaded to LDS has arrived, and with kAll every LDS
+// read has returned too.
+constexpr int kLoadsDone = 0x0F70, kAllDone = 0x0070;
+
+// Streams ROWS-row tiles of a [tokens][stride] tensor into LDS by THREADS threads, with loads that write LDS
+// themselves (global_load_lds_dwordx4): 16 bytes a lane land in lane order behind a wave's LDS address, so
+// the chunk order of Tile is made on the global side.  A thread's byte offsets within a tile do not
+// change, so a whole tile costs no address arithmetic; in a last, partial tile the rows past the end are
+// read as the last row (a copy of a real row, whose weight is zero).
+template <typename T, int D, int ROWS, int THREADS> struct Feed {
+    using L = Tile<T, D>;
+    static constexpr int kLoads = ROWS * L::CH / THREADS;
+    static_assert(ROWS * L::CH % THREADS == 0, "every thread loads whole chunks");
+    typedef const __attribute__((address_space(1))) void* Global;
+    typedef __attribute__((address_space(3))) void* Local;
+    uint32_t off[kLoads];
+    uint32_t pitch;  // bytes from one token to the next
+
+    static __device__ __forceinline__ int row(int i) { return ((int)threadIdx.x % THREADS + THREADS * i) / L::CH; }
+    static __device__ __forceinline__ uint32_t col(int i) {
+        const int c = ((int)threadIdx.x % THREADS + THREADS * i) % L::CH;
+        return (uint32_t)(c ^ L::swz(row(i))) * 16u;
+    }
+    __device__ __forceinline__ void init(int64_t stride) {
+        pitch = (uint32_t)(stride * (int64_t)sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)row(i) * pitch + col(i);
+    }
+    // rows 0 .. of `g`, the tensor's row `first`; `left` >= 1 rows are there
+    __device__ __forceinline__ void load(T* s, const T* g, int first, int left) const {
+        const char* base = reinterpret_cast<const char*>(g) + (int64_t)first * pitch;
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x % THREADS / kWave);
+        if (left >= ROWS) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                __builtin_amdgcn_global_load_lds((Global)(base + off[i]), (Local)(s + (wave * kWave + THREADS * i) * L::kE), 16, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                __builtin_amdgcn_global_load_lds((Global)(base + (uint32_t)min(row(i), left - 1) * pitch + col(i)),
+                                                 (Local)(s + (wave * kWave + THREADS * i) * L::kE), 16, 0, 0);
+        }
+    }
+};
 
 // Row of accumulator register r in the lower lane half (the upper half: + 4).
 __device__ __forceinline__ constexpr int acc_row(int r) { return (r % 4) + 8 * (r / 4); }
@@ -154,7 +184,7 @@ __device__ __forceinline__ void span_of(const int64_t* cu, int64_t total, int64_
     len = (int)(b - a);
 }
 
-// Sequence and tile of a slot.  Sequence s owns the slots from floor(cu[s] / kBM) + s on, one more than
+// Sequence and tile of a slot.  Sequence s owns the slots from floor(cu[s] / own) + s on, one more than
 // its whole tiles at most, so that a workgroup finds its work from the offsets alone, with no list made
 // on the way: a search 64 sequences wide (one step for 64 sequences, two for 4096).
 template <typename F>
@@ -172,40 +202,40 @@ __device__ __forceinline__ int64_t last_at_most(int64_t nseq, int64_t x, F start
     }
     return __builtin_amdgcn_readfirstlane((int)lo);
 }
-__device__ __forceinline__ int slot_sequence(const int64_t* cu, int64_t total, int64_t nseq, int slot) {
-    return (int)last_at_most(nseq, slot, [&](int64_t s) { return clamp64(cu[s], 0, total) / kBM + s; });
+__device__ __forceinline__ int slot_sequence(const int64_t* cu, int64_t total, int64_t nseq, int own, int slot) {
+    return (int)last_at_most(nseq, slot, [&](int64_t s) { return clamp64(cu[s], 0, total) / own + s; });
 }
 // The sequence whose tokens token t of a packed axis is among, if it is among any.
 __device__ __forceinline__ int64_t last_start(const int64_t* cu, int64_t nseq, int64_t t) {
     return last_at_most(nseq, t, [&](int64_t s) { return cu[s]; });
 }
 
-// (by_keys: the slots count tiles of the key axis)
-__device__ __forceinline__ Span find_span(const AttnParams& p, int slot, bool by_keys) {
+// (own: rows of a tile; by_keys: the slots count tiles of the key axis)
+__device__ __forceinline__ Span find_span(const AttnParams& p, int slot, int own, bool by_keys) {
     const int64_t* cu = by_keys ? p.cu_k : p.cu_q;
     const int64_t total = by_keys ? p.total_k : p.total_q;
     Span sp;
     int s, tile;
     if (!cu) {
-        const int per = (int)((total / p.nseq + kBM - 1) / kBM);
+        const int per = (int)((total / p.nseq + own - 1) / own);
         s = slot / per;
         tile = slot % per;
     } else {
-        s = slot_sequence(cu, total, p.nseq, slot);
-        tile = slot - (int)(clamp64(cu[s], 0, total) / kBM + s);
+        s = slot_sequence(cu, total, p.nseq, own, slot);
+        tile = slot - (int)(clamp64(cu[s], 0, total) / own + s);
     }
     sp.seq = s;
     span_of(p.cu_q, p.total_q, p.nseq, s, sp.q0, sp.lq);
     span_of(p.cu_k, p.total_k, p.nseq, s, sp.k0, sp.lk);
     const int len = by_keys ? sp.lk : sp.lq;
-    sp.tile = tile >= 0 && (int64_t)tile * kBM < len ? tile : -1;
+    sp.tile = tile >= 0 && (int64_t)tile * own < len ? tile : -1;
     return sp;
 }
 
 // Slots of an axis: its whole tiles, and one more for each sequence.
-inline int64_t slots_of(const int64_t* cu, int64_t total, int64_t nseq) {
+inline int64_t slots_of(const int64_t* cu, int64_t total, int64_t nseq, int own) {
     if (nseq == 0) return 0;
-    return cu ? total / kBM + nseq : nseq * ((total / nseq + kBM - 1) / kBM);
+    return cu ? total / own + nseq : nseq * ((total / nseq + own - 1) / own);
 }
 
 // Workgroup -> (slot, head).  Heads run fastest, the slots from the last (under a causal mask the
@@ -234,20 +264,139 @@ __device__ __forceinline__ void fill_bias(float* lut, const AttnParams& p, int h
     for (int i = threadIdx.x; i <= 2 * m; i += kThreads) lut[i] = p.table[(int64_t)bucket_of(p.bk, i - m) * p.H + head] * kLog2e;
 }
 
-// What turns a raw product q.k into a score in log2 units, and the derivative of the cap.
-//   no cap: x * scale * log2 e.   cap c: c tanh(x scale / c) log2 e, with tanh(u) = 1 - 2 / (1 + e^2u).
+// What turns a raw product x = q.k into a score in log2 units, and the derivative of the cap.
+//   no cap: x * a, a = |scale| log2 e (the sign of the scale is in the operands: see `signed_frag`)
+//   cap c:  c tanh(x |scale| / c) log2 e
 struct Score {
-    float a;     // no cap: scale log2 e; cap: 2 scale log2 e / c (bf16) or scale / c (fp32)
-    float c2;    // c log2 e
-    __device__ __forceinline__ void init(float scale, float cap, bool capped, bool fp32) {
+    float a;       // no cap: |scale| log2 e; cap: 2 |scale| log2 e / c (bf16) or |scale| / c (fp32)
+    float c2;      // c log2 e
+    float rc2;     // 1 / c2
+    float k[4];    // cap, bf16: c2 tanh(x |scale| / c) = x (k0 + k1 x^2 + k2 x^4 + k3 x^6) where x^2 <= small
+    float small;
+    template <typename T> __device__ __forceinline__ void init(float scale, float cap, bool capped) {
+        // (a scale of zero: a finite factor times a masked score has to stay minus infinity)
+        const float s = fmaxf(fabsf(scale), 1e-30f), u = capped ? s / cap : 0.f;
         c2 = cap * kLog2e;
-        a = !capped ? scale * kLog2e : fp32 ? scale / cap : 2.f * scale * kLog2e / cap;
+        rc2 = capped ? 1.f / c2 : 0.f;
+        a = !capped ? s * kLog2e : sizeof(T) == 4 ? u : 2.f * u * kLog2e;
+        k[0] = c2 * u;
+        k[1] = k[0] * u * u * (-1.f / 3.f);
+        k[2] = k[0] * (u * u) * (u * u) * (2.f / 15.f);
+        k[3] = k[0] * (u * u) * (u * u) * (u * u) * (-17.f / 315.f);
+        small = capped ? 0.0625f / (u * u) : 0.f;
     }
-    // tanh of the capped score: from the hardware's exp2 and reciprocal for bf16 inputs (an absolute
-    // error of some 1e-7, times c in the score), from the math library for fp32 ones
-    template <typename T> __device__ __forceinline__ float tanh_of(float x) const {
-        if constexpr (sizeof(T) == 2) return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + exp2_hw(x * a));
-        else return tanhf(x * a);
+    // The capped scores of N products, in place.  bf16: the series of tanh where all of the wave's arguments
+    // are within 1/4 (its next term, 62/2835 u^9, is under 1e-7 there): 5 full-rate operations a score;
+    // otherwise tanh u = 1 - 2 / (1 + e^2u) from the hardware's exp2 and reciprocal (off by some 1e-7),
+    // which the unit for them takes 8 times as long for.  fp32: the math library's.
+    template <typename T, int N> __device__ __forceinline__ void capped(f32x16 (&s)[N]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[n][r] = c2 * tanhf(s[n][r] * a);
+        } else {
+            float most = 0.f;
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(s[n][r]));
+            if (__all(most * most <= small)) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float x = s[n][r], q = x * x;
+                        s[n][r] = x * (k[0] + q * (k[1] + q * (k[2] + q * k[3])));
+                    }
+            } else {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[n][r] = c2 - 2.f * c2 * __builtin_amdgcn_rcpf(1.f + exp2_hw(s[n][r] * a));
+            }
+        }
+    }
+    template <typename T> __device__ __forceinline__ float capped(float x) const {
+        if constexpr (sizeof(T) == 4) return c2 * tanhf(x * a);
+        else return c2 - 2.f * c2 * __builtin_amdgcn_rcpf(1.f + exp2_hw(x * a));
+    }
+    // derivative of the cap at a capped score
+    __device__ __forceinline__ float slope(float s) const {
+        const float t = s * rc2;
+        return 1.f - t * t;
+    }
+};
+
+// 16 bytes of an operand that meets only scores, with the sign of the scale.
+template <typename T> __device__ __forceinline__ typename Op<T>::Frag signed_frag(const T* g, float scale) {
+    typename Op<T>::Frag f = __builtin_bit_cast(typename Op<T>::Frag, ld16(g));
+    if (scale < 0.f) f = -f;
+    return f;
+}
+
+// Adds the bias to scores s, N 32-row blocks whose register 0 has relative position rel (key - query), and
+// register r STEP * acc_row(r) further on (block n: STEP * 32 n).  Factor a on the scores first.  [lowest, highest]:
+// relative positions in any lane.  Returns whether some of them are nearer than the table's reach.
+template <int BIAS, int STEP, int N>
+__device__ __forceinline__ bool add_bias(f32x16 (&s)[N], float a, float slope2, const float* lut, int md, int rel, int lowest,
+                                         int highest) {
+    if constexpr (BIAS == kBiasSlopes) {
+        const float at = (float)rel;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                s[n][r] = s[n][r] * a - slope2 * fabsf(at + (float)(STEP * (32 * n + acc_row(r))));
+        return true;
+    } else if constexpr (BIAS == kBiasBuckets) {
+        if (highest <= -md || lowest >= md) {
+            const float b = lut[highest <= -md ? 0 : 2 * md];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[n][r] = s[n][r] * a + b;
+            return false;
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                s[n][r] = s[n][r] * a + lut[min(max(rel + STEP * (32 * n + acc_row(r)), -md), md) + md];
+        return true;
+    } else {
+        return true;
+    }
+}
+
+// Joins the four waves' accumulators of the same 32 rows (SPLIT), each weighted by w[wave][row] where w is given.  A
+// wave keeps its own in one of the four regions that two of the kernel's tile arrays give; the sums of row
+// `row`, columns d .. d + 3 come out for thread (row, d / 4).
+template <typename T, int D> struct Join {
+    static constexpr int kRegion = 32 * D;  // floats
+    static constexpr int kPer = (int)sizeof(T);  // regions in one array of 4 x 32 x D elements
+    static __device__ __forceinline__ float* region(T* a, T* b, int wave) {
+        return reinterpret_cast<float*>(wave < kPer ? a : b) + (wave % kPer) * kRegion;
+    }
+    static __device__ __forceinline__ int place(int row, int d4) { return row * D + 4 * (d4 ^ (row % 8)); }
+    static __device__ __forceinline__ void keep(T* a, T* b, const f32x16 (&acc)[D / 32], int lane, int wave) {
+        float* mine = region(a, b, wave);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                *reinterpret_cast<f32x4*>(mine + place(lane % 32, 8 * d + r / 2 + lane / 32)) =
+                    f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
+    }
+    static __device__ __forceinline__ f32x4 sum(T* a, T* b, int row, int d4, const float* w) {
+        f32x4 v{};
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(region(a, b, i) + place(row, d4));
+            v += w ? w[32 * i + row] * x : x;
+        }
+        return v;
     }
 };
 

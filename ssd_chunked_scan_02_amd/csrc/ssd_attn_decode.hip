@@ -70,12 +70,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
     const int b0 = split * per, b1 = min(b0 + per, blocks);
 
     Score sc;
-    sc.init(p.scale, p.cap, CAP, sizeof(T) == 4);
+    sc.init<T>(p.scale, p.cap, CAP);
     const int head = head0 + min(col, heads - 1);
     Frag qf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-        qf[t] = __builtin_bit_cast(Frag, ld16(static_cast<const T*>(p.q) + (int64_t)s * p.q_stride + (int64_t)head * D + t * O::kK + g * E));
+        qf[t] = signed_frag<T>(static_cast<const T*>(p.q) + (int64_t)s * p.q_stride + (int64_t)head * D + t * O::kK + g * E, p.scale);
     float slope2 = 0.f, far = 0.f;
     const int md = p.bk.max_distance;
     const float* bias = extra;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
             for (int r = 0; r < 4; ++r) {
                 const int key = key0 + 16 * n + r;
                 float x = sv[n][r];
-                x = CAP ? sc.c2 * sc.template tanh_of<T>(x) : x * sc.a;
+                x = CAP ? sc.template capped<T>(x) : x * sc.a;
                 if constexpr (BIAS == kBiasSlopes) x -= slope2 * (float)(len - 1 - key);
                 if constexpr (BIAS == kBiasBuckets) x += all_far ? far : bias[bucket[min(max(len - 1 - key, 0), md)] + col];
                 x = key < len && (here >> n & 1) ? x : -INFINITY;

@@ -95,3 +95,23 @@ def grad_bounds(ref, dtype, D, n, H, Hk, cap):
     if "dtable" in ref:  # (its D is exact: no part of y's error)
         got["dtable"] = 1.1 * rel * ref["dtable_abs"] + 1e-30
     return got
+
+
+def some_heads(d, outputs, keep=3):
+    """The case and its outputs cut to the first, a middle and the last key head and their queries' heads
+    (heads are independent of each other, so each is checked as if it were alone)."""
+    H, Hk = d["q"].shape[1], d["k"].shape[1]
+    if Hk <= keep:
+        return d, outputs
+    kv = [0, Hk // 2, Hk - 1]
+    qh = [g * (H // Hk) + i for g in kv for i in range(H // Hk)]
+    axis = {"q": (1, qh), "k": (1, kv), "v": (1, kv), "dy": (1, qh), "slopes": (0, qh), "table": (1, qh), "y": (1, qh),
+            "lse": (1, qh), "dq": (1, qh), "dk": (1, kv), "dv": (1, kv), "dtable": (1, qh)}
+
+    def cut(n, x):
+        if x is None:
+            return None
+        at, rows = axis[n]
+        return x[:, rows] if at == 1 else x[rows]
+
+    return {n: cut(n, x) for n, x in d.items()}, {n: cut(n, x) for n, x in outputs.items()}
