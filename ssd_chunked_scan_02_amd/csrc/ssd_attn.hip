@@ -19,8 +19,9 @@ constexpr float kLazy = 8.f;  // log2 growth of a maximum that is let pass witho
 // Scores capped to at most 2^80 need no maximum at all: weights in [2^-80, 2^80] times 2^24 keys and any
 // sensible value stay inside fp32 (and bf16, which has its range).
 constexpr float kNoMaxNeeded = 80.f;
+enum Cap { kCapNone = 0, kCapped = 1, kCapBounds = 2 };  // kCapBounds: without a bias, by a cap that needs no maximum
 
-template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+template <typename T, int D, int CAPPED, int BIAS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_fwd_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
@@ -28,6 +29,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     constexpr int OWN = kOwn<SPLIT>, KT = SPLIT ? 32 : O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
     constexpr int ELEMS = (SPLIT ? kWaves : 1) * KT * D;
     constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;  // (two buffers of split fp32 tiles of 128 would not fit)
+    constexpr bool CAP = CAPPED != kCapNone, NO_MAX = CAPPED == kCapBounds;
     constexpr bool RAW = !CAP && BIAS == kBiasNone;  // scores stay raw products until the exponential
     __shared__ __attribute__((aligned(16))) T k_a[ELEMS];
     __shared__ __attribute__((aligned(16))) T v_a[ELEMS];
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         for (int t = 0; t < NT; ++t) qf[t] = signed_frag<T>(qg + (2 * t + half) * O::kE, p.scale);
     }
     Score sc;
-    sc.init<T>(p.scale, p.cap, CAP);
+    sc.init<T>(fabsf(p.scale), p.cap, CAP);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     if constexpr (BIAS == kBiasBuckets) fill_bias(lut, p, head);
@@ -85,8 +87,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
-    const bool no_max = CAP && BIAS == kBiasNone && sc.c2 <= kNoMaxNeeded;
-    float m = no_max ? 0.f : kNoMax, l = 0.f;  // l: this lane half's share
+    float m = NO_MAX ? 0.f : kNoMax, l = 0.f;  // l: this lane half's share
     const int qpos = row + shift;
 
     auto settle = [&]() {  // what was on its way to LDS is there, and (SPLIT: this wave's) reads are over
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[n][r] = 32 * n + acc_row(r) < left ? s[n][r] : -INFINITY;
             }
-            if (!no_max) {
+            if constexpr (!NO_MAX) {
                 float mx = s[0][0];
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[n][r] = exp2_hw(RAW ? __builtin_fmaf(s[n][r], sc.a, -m) : no_max ? s[n][r] : s[n][r] - m);
+                    s[n][r] = exp2_hw(RAW ? __builtin_fmaf(s[n][r], sc.a, -m) : NO_MAX ? s[n][r] : s[n][r] - m);
                     add += s[n][r];
                 }
             l += add;
@@ -194,43 +195,46 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         }
         return;
     }
+    // (the store exchanges words between a row's two lanes, which leave or stay together)
     if (row >= sp.lq) return;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (an empty row is zero; a NaN stays one)
     T* yg = static_cast<T*>(p.y) + ((sp.q0 + row) * p.H + head) * D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-            store4(yg + 32 * d + 2 * r + 4 * half, o[d][r] * inv, o[d][r + 1] * inv, o[d][r + 2] * inv, o[d][r + 3] * inv);
+        for (int r = 0; r < 16; r += 8) store_rows(yg + 32 * d, o[d], r, half, inv);
     if (p.lse && half == 0) p.lse[(sp.q0 + row) * p.H + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-template <typename T, int D, bool CAP, int BIAS>
+template <typename T, int D, int CAPPED, int BIAS>
 int launch_fwd(AttnParams p, hipStream_t stream) {
     const int64_t whole = slots_of(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H;
     const bool split = whole < kSplitBelow;
     p.q_slots = (int)slots_of(p.cu_q, p.total_q, p.nseq, split ? kOwn<true> : kOwn<false>);
+    set_each(p, split ? kOwn<true> : kOwn<false>, 1);
     const int64_t grid = (int64_t)p.q_slots * p.H;
     if (grid == 0) return 0;
-    if (split) hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAP, BIAS, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAP, BIAS, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+    if (split) hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAPPED, BIAS, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAPPED, BIAS, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
-template <typename T, int D, bool CAP>
+template <typename T, int D, int CAPPED>
 int launch_fwd(const AttnParams& p, int bias, hipStream_t stream) {
     switch (bias) {
-        case kBiasNone: return launch_fwd<T, D, CAP, kBiasNone>(p, stream);
-        case kBiasSlopes: return launch_fwd<T, D, CAP, kBiasSlopes>(p, stream);
-        default: return launch_fwd<T, D, CAP, kBiasBuckets>(p, stream);
+        case kBiasNone:
+            if (CAPPED == kCapped && p.cap * kLog2e <= kNoMaxNeeded) return launch_fwd<T, D, CAPPED ? kCapBounds : kCapNone, kBiasNone>(p, stream);
+            return launch_fwd<T, D, CAPPED, kBiasNone>(p, stream);
+        case kBiasSlopes: return launch_fwd<T, D, CAPPED, kBiasSlopes>(p, stream);
+        default: return launch_fwd<T, D, CAPPED, kBiasBuckets>(p, stream);
     }
 }
 template <typename T>
 int launch_fwd(const AttnParams& p, int D, int bias, hipStream_t stream) {
     const bool cap = p.cap > 0.f;
     switch (D) {
-        case 32: return cap ? launch_fwd<T, 32, true>(p, bias, stream) : launch_fwd<T, 32, false>(p, bias, stream);
-        case 64: return cap ? launch_fwd<T, 64, true>(p, bias, stream) : launch_fwd<T, 64, false>(p, bias, stream);
-        case 128: return cap ? launch_fwd<T, 128, true>(p, bias, stream) : launch_fwd<T, 128, false>(p, bias, stream);
+        case 32: return cap ? launch_fwd<T, 32, kCapped>(p, bias, stream) : launch_fwd<T, 32, kCapNone>(p, bias, stream);
+        case 64: return cap ? launch_fwd<T, 64, kCapped>(p, bias, stream) : launch_fwd<T, 64, kCapNone>(p, bias, stream);
+        case 128: return cap ? launch_fwd<T, 128, kCapped>(p, bias, stream) : launch_fwd<T, 128, kCapNone>(p, bias, stream);
         default: return -2;
     }
 }

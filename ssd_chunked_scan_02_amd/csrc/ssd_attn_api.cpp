@@ -149,17 +149,23 @@ int code(int rc) { return rc == 0 ? SSD_OK : rc == -2 ? SSD_ERR_UNSUPPORTED : SS
 
 size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// Workspace of the backward pass: D per (query, head), then the table's partial gradients.  The slots
-// are bounded without the offsets, so that the size does not depend on how a call gives its sequences.
+// Workspace of the backward pass: D per (query, head), the table's partial gradients, and the orders of
+// the query and key tiles (twice each: as found and as sorted).  The tiles are bounded without the
+// offsets, so that the size does not depend on how a call gives its sequences; table gradients of small
+// problems come in tiles of 32 queries.
 struct BackwardWorkspace {
-    size_t delta, part, total;
+    size_t delta, part, plan_q, plan_k, total;
 };
 BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
     BackwardWorkspace w{};
-    const size_t slots = (size_t)(d->total_q / 128 + d->nseq + 1);
+    const int64_t q_slots = d->total_q / 128 + d->nseq + 1, k_slots = d->total_k / 128 + d->nseq + 1;
+    int64_t parts = q_slots;
+    if (d->total_q / 128 * d->nheads < ssd::kSplitBelow) parts = d->total_q / 32 + d->nseq + 1;
     w.delta = align16((size_t)d->total_q * (size_t)d->nheads * 4);
-    w.part = table ? align16(slots * (size_t)d->nheads * (size_t)d->num_buckets * 4) : 0;
-    w.total = w.delta + w.part;
+    w.part = table ? align16((size_t)parts * (size_t)d->nheads * (size_t)d->num_buckets * 4) : 0;
+    w.plan_q = align16((size_t)q_slots * 16);
+    w.plan_k = align16((size_t)k_slots * 16);
+    w.total = w.delta + w.part + w.plan_q + w.plan_k;
     return w;
 }
 
@@ -253,7 +259,12 @@ int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, co
     p.dv = dv;
     p.dtable = dtable;
     p.delta = static_cast<float*>(workspace);
-    p.table_part = dtable ? reinterpret_cast<float*>(static_cast<char*>(workspace) + w.delta) : nullptr;
+    char* at = static_cast<char*>(workspace) + w.delta;
+    p.table_part = dtable ? reinterpret_cast<float*>(at) : nullptr;
+    if (p.cu_q && p.nseq > 1) {
+        p.plan_q = reinterpret_cast<int2*>(at + w.part);
+        p.plan_k = reinterpret_cast<int2*>(at + w.part + w.plan_q);
+    }
     return code(ssd::launch_attn_backward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
 }
 

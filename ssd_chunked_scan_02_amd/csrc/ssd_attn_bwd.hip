@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     work_item(blockIdx.x, p.q_slots, p.H, slot, head);
     const Span sp = find_span(p, slot, OWN, false);
     const bool grad = BIAS == kBiasBuckets && p.dtable != nullptr;
-    float* part = grad ? p.table_part + ((int64_t)slot * p.H + head) * p.bk.total : nullptr;
+    float* part = grad ? p.table_part + ((int64_t)sp.slot * p.H + head) * p.bk.total : nullptr;
     if (sp.tile < 0) {
         if (grad)
             for (int i = threadIdx.x; i < p.bk.total; i += kThreads) part[i] = 0.f;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int e0 = (2 * t + half) * O::kE;
-            qf[t] = signed_frag<T>(qg + e0, p.scale);
+            qf[t] = __builtin_bit_cast(Frag, ld16(qg + e0));
             gf[t] = __builtin_bit_cast(Frag, ld16(gg + e0));
             const Frag yf = __builtin_bit_cast(Frag, ld16(yg + e0));
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     if (lse2 == -INFINITY || row >= sp.lq) lse2 = INFINITY;
 
     Score sc;
-    sc.init<T>(p.scale, p.cap, CAP);
+    sc.init<T>(p.scale, p.cap, CAP, !CAP && BIAS == kBiasNone);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     const int md = p.bk.max_distance, reach = 2 * md + 1;
@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     // p and dS of 32 keys from kn on (dS before the cap's derivative, which is returned in `slope`); true: some
     // are nearer than the table's reach
     auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope) {
-        f32x16 x[1] = {f32x16{}}, dp{};
+        f32x16 x[1] = {f32x16{}}, dp;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] = -delta;  // the accumulator starts at -D: dP - D at no cost
 #pragma unroll
         for (int i = 0; i < NT; ++i) x[0] = O::mma(L::rows(kt, 32 * n, i, lane), qf[i], x[0]);
 #pragma unroll
@@ -166,12 +168,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         if (kn + 32 > wave_least) {
             const int left = my_limit - kn - 4 * half;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[0][r] = acc_row(r) < left ? x[0][r] : -INFINITY;
+            for (int r = 0; r < 16; ++r) x[0][r] = acc_row(r) < left ? x[0][r] : sc.none;
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             s[r] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x[0][r], sc.a, -lse2) : x[0][r] - lse2);
-            ds[r] = s[r] * (dp[r] - delta);
+            ds[r] = s[r] * dp[r];
         }
         return near;
     };
@@ -179,7 +181,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         const int k0 = t * KT;
         if (DOUBLE && t + dt < ntiles) fetch(kn_, vn_, t + dt);
         if (k0 < wave_most) {
-#pragma unroll
+            // (64-wide heads: both halves of a tile at once; 128-wide: one after the other, in the registers of two
+            // waves a SIMD)
+#pragma unroll sizeof(T) * D >= 256 ? 1 : NS
             for (int n = 0; n < NS; ++n) {
                 const int kn = k0 + 32 * n;
                 f32x16 s, ds, slope;
@@ -243,12 +247,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         if (row < sp.lq) {
             T* out = static_cast<T*>(p.dq) + mine * D;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                acc[d] *= p.scale;
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; r += 4)
-                    store4(out + 32 * d + 2 * r + 4 * half, acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]);
-            }
+                for (int r = 0; r < 16; r += 8) store_rows(out + 32 * d, acc[d], r, half, p.scale);
         }
     }
     if (grad) delta += row_ds;
@@ -318,6 +319,71 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     }
 }
 
+// The slots of the query (block 0) and key axis (block 1) in order of their work, most first: a counting sort by
+// the number of 64-row steps, empty slots last.  The order among equals varies from run to run, and is of no
+// consequence: a workgroup's results are its own, and lie where its tile does.
+constexpr int kPlanThreads = 1024, kPlanBins = 2048;
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, int q_own, int k_own) {
+    __shared__ int bins[kPlanBins];
+    __shared__ int scan[kPlanThreads];
+    const bool keys = blockIdx.x == 1;
+    const int own = keys ? k_own : q_own;
+    if (own == 0) return;
+    const int64_t* cu = keys ? p.cu_k : p.cu_q;
+    int2* plan = keys ? p.plan_k : p.plan_q;
+    const int tq = (int)p.total_q, tk = (int)p.total_k, total = keys ? tk : tq, nseq = (int)p.nseq;
+    const int slots = total / own + nseq;
+    int2* raw = plan + slots;  // (sequence, tile) by slot
+    for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
+    __syncthreads();
+    auto bin_of = [&](int s, int tile) {
+        const int q0 = offset_at(p.cu_q, s, tq), lq = max(offset_at(p.cu_q, s + 1, tq) - q0, 0);
+        const int k0 = offset_at(p.cu_k, s, tk), lk = max(offset_at(p.cu_k, s + 1, tk) - k0, 0), shift = lk - lq;
+        const int prefix = p.prefix ? (int)clamp64(p.prefix[s], 0, lk) : 0;
+        int rows;
+        if (keys) rows = lq - (!p.causal || tile * own < prefix ? 0 : max(tile * own - shift, 0));
+        else rows = p.causal ? max(min(max(min(tile * own + own, lq) + shift, prefix), lk), 0) : lk;
+        return kPlanBins - 1 - min(max((rows + 63) / 64, 0) + 1, kPlanBins - 1);
+    };
+    for (int slot = threadIdx.x; slot < slots; slot += kPlanThreads) {
+        int lo = 0, n = nseq;  // the last sequence that starts at this slot or before
+        while (n > 1) {
+            const int mid = n / 2;
+            if (offset_at(cu, lo + mid, total) / own + lo + mid <= slot) {
+                lo += mid;
+                n -= mid;
+            } else {
+                n = mid;
+            }
+        }
+        int tile = slot - (offset_at(cu, lo, total) / own + lo);
+        const int len = offset_at(cu, lo + 1, total) - offset_at(cu, lo, total);
+        if (tile < 0 || (int64_t)tile * own >= len) tile = -1;
+        raw[slot] = int2{tile < 0 ? slot : lo, tile};
+        atomicAdd(&bins[tile < 0 ? kPlanBins - 1 : bin_of(lo, tile)], 1);
+    }
+    __syncthreads();
+    // exclusive sums of the bins, two a thread
+    const int a = bins[2 * threadIdx.x], b = bins[2 * threadIdx.x + 1];
+    scan[threadIdx.x] = a + b;
+    __syncthreads();
+    for (int off = 1; off < kPlanThreads; off <<= 1) {
+        const int v = threadIdx.x >= off ? scan[threadIdx.x - off] : 0;
+        __syncthreads();
+        scan[threadIdx.x] += v;
+        __syncthreads();
+    }
+    const int before = scan[threadIdx.x] - a - b;
+    bins[2 * threadIdx.x] = before;
+    bins[2 * threadIdx.x + 1] = before + a;
+    __syncthreads();
+    for (int slot = threadIdx.x; slot < slots; slot += kPlanThreads) {
+        const int2 e = raw[slot];
+        const int at = atomicAdd(&bins[e.y < 0 ? kPlanBins - 1 : bin_of(e.x, e.y)], 1);
+        plan[slots - 1 - at] = e;  // (workgroups take slots from the last one down)
+    }
+}
+
 // dtable[b, h]: the query tiles' sums, in order.
 __global__ void __launch_bounds__(kThreads) attn_dtable_kernel(AttnParams p) {
     __shared__ double sums[kThreads];
@@ -334,30 +400,46 @@ __global__ void __launch_bounds__(kThreads) attn_dtable_kernel(AttnParams p) {
     }
 }
 
-template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 2) attn_dkv_kernel(AttnParams p) {
+// How a workgroup of the key-gradient kernel shares its work.
+enum Share {
+    kAlone = 0,   // four waves, 32 keys each
+    kSplit = 1,   // four waves on the same 32 keys (see kOwn)
+    kPaired = 2,  // eight waves, two on the same 32 keys, each with half of a tile's queries, and the keys and
+                  // values in LDS: the gradients of 128-wide heads alone fill half a SIMD's registers, and so two
+                  // waves still fit on each
+};
+
+template <typename T, int D, bool CAP, int BIAS, int SHARE>
+__global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SHARE != kAlone || sizeof(T) * D >= 256 ? 1 : 2)
+    attn_dkv_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
-    constexpr int OWN = kOwn<SPLIT>, QT = SPLIT ? 32 : O::kKT, NS = QT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
-    constexpr int COPIES = SPLIT ? kWaves : 1, ELEMS = COPIES * QT * D, THREADS = SPLIT ? kWave : kThreads;
+    constexpr bool SPLIT = SHARE == kSplit, PAIRED = SHARE == kPaired;
+    constexpr int OWN = kOwn<SPLIT>, QT = SPLIT ? 32 : O::kKT, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
+    constexpr int NS = PAIRED ? 1 : QT / 32;  // 32-query blocks of a tile that are this wave's
+    constexpr int BLOCK = PAIRED ? 2 * kThreads : kThreads;
+    constexpr int COPIES = SPLIT ? kWaves : 1, ELEMS = COPIES * QT * D, THREADS = SPLIT ? kWave : BLOCK;
     constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;
     __shared__ __attribute__((aligned(16))) T q_a[ELEMS];
     __shared__ __attribute__((aligned(16))) T g_a[ELEMS];
     __shared__ __attribute__((aligned(16))) T q_b[DOUBLE ? ELEMS : 8];
     __shared__ __attribute__((aligned(16))) T g_b[DOUBLE ? ELEMS : 8];
+    __shared__ __attribute__((aligned(16))) T k_own[PAIRED ? OWN * D : 8];
+    __shared__ __attribute__((aligned(16))) T v_own[PAIRED ? OWN * D : 8];
     __shared__ __attribute__((aligned(16))) float stat[2][COPIES][2][QT];  // [buffer][wave][lse in log2 units, D][query]
     extern __shared__ float extra[];
     float* lut = extra;
 
     int slot, kvh;
     work_item(blockIdx.x, p.k_slots, p.Hk, slot, kvh);
-    slot = p.k_slots - 1 - slot;  // under a causal mask the first keys are seen by the most queries
+    if (!p.plan_k) slot = p.k_slots - 1 - slot;  // under a causal mask the first keys are seen by the most queries
     const Span sp = find_span(p, slot, OWN, true);
     if (sp.tile < 0) return;
     const int group = p.H / p.Hk;
     const int lane = threadIdx.x % kWave, half = lane / 32;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int all_waves = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int wave = all_waves % kWaves, n_own = all_waves / kWaves;  // (PAIRED: which 32 queries of a tile)
     const int shift = sp.lk - sp.lq;
     int prefix = 0;
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
@@ -376,7 +458,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 
     gf.init((int64_t)p.H * D);
     const int tid = SPLIT ? lane : (int)threadIdx.x;
     // a tile's queries and dy go straight to LDS; its statistics (threads 0 .. QT - 1: lse, the next QT: D) wait in a
-    // register until then
+    // register until then.  They are what the accumulators of S and dP start from: -D, and where the scores
+    // stay raw products until the exponential, -lse in their units.
+    constexpr bool RAW = !CAP && BIAS == kBiasNone;
+    Score sc;
+    sc.init<T>(p.scale, p.cap, CAP, !CAP && BIAS == kBiasNone);
+    const float unit = RAW ? -kLog2e / sc.a : kLog2e;
     float sb = 0.f;
     auto fetch = [&](T* qs, T* gs, int it) {
         const int head = kvh * group + it / per_head, row = (t0 + it % per_head) * QT;
@@ -384,8 +471,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 
         gf.load(gs, static_cast<const T*>(p.dy) + (sp.q0 * p.H + head) * D, row, sp.lq - row);
         if (tid < 2 * QT) {
             const int64_t at = (sp.q0 + min(row + tid % QT, sp.lq - 1)) * p.H + head;
-            sb = tid < QT ? p.lse[at] * kLog2e : p.delta[at];
-            if (tid < QT && sb == -INFINITY) sb = INFINITY;  // (sees nothing: all its weights are zero)
+            sb = tid < QT ? p.lse[at] : -p.delta[at];
+            // (a query that sees nothing: all its weights are zero)
+            if (tid < QT) sb = (sb == -INFINITY ? INFINITY : sb) * unit;
         }
     };
     const int copy = SPLIT ? wave : 0;
@@ -400,19 +488,26 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 
     const int i0 = SPLIT ? wave : 0, di = SPLIT ? kWaves : 1;
     if (i0 < ntiles) fetch(qa, ga, i0);
 
-    const int64_t krow = sp.k0 + min(key, sp.lk - 1);
-    Frag kf[NT], vf[NT];
-    {
+    Frag kf[PAIRED ? 1 : NT], vf[PAIRED ? 1 : NT];
+    if constexpr (PAIRED) {
+        Feed<T, D, OWN, BLOCK> own;
+        const int row = sp.tile * OWN;
+        own.init(p.k_stride);
+        own.load(k_own, static_cast<const T*>(p.k) + sp.k0 * p.k_stride + (int64_t)kvh * D, row, sp.lk - row);
+        own.init(p.v_stride);
+        own.load(v_own, static_cast<const T*>(p.v) + sp.k0 * p.v_stride + (int64_t)kvh * D, row, sp.lk - row);
+    } else {
+        const int64_t krow = sp.k0 + min(key, sp.lk - 1);
         const T* kg = static_cast<const T*>(p.k) + krow * p.k_stride + (int64_t)kvh * D;
         const T* vg = static_cast<const T*>(p.v) + krow * p.v_stride + (int64_t)kvh * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            kf[t] = signed_frag<T>(kg + (2 * t + half) * O::kE, p.scale);
+            kf[t] = __builtin_bit_cast(Frag, ld16(kg + (2 * t + half) * O::kE));
             vf[t] = __builtin_bit_cast(Frag, ld16(vg + (2 * t + half) * O::kE));
         }
     }
-    Score sc;
-    sc.init<T>(p.scale, p.cap, CAP);
+    auto k_frag = [&](int i) { return PAIRED ? L::rows(k_own, 32 * wave, i, lane) : kf[PAIRED ? 0 : i]; };
+    auto v_frag = [&](int i) { return PAIRED ? L::rows(v_own, 32 * wave, i, lane) : vf[PAIRED ? 0 : i]; };
     const int md = p.bk.max_distance;
     if constexpr (BIAS == kBiasBuckets) {
         // one head's bias, refilled where the head changes; SPLIT: the waves are on different heads at a time,
@@ -442,12 +537,26 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 
         if (DOUBLE && it + di < ntiles) fetch(qn_, gn_, it + di);
         if (q0 + QT > wave_least) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                f32x16 s[1] = {f32x16{}}, dp{};
+            for (int j = 0; j < NS; ++j) {
+                const int n = PAIRED ? n_own : j;
+                const float* ls = &stat[buf][copy][0][32 * n + 4 * half];
+                const float* de = &stat[buf][copy][1][32 * n + 4 * half];
+                f32x16 s[1] = {f32x16{}}, dp;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) s[0] = O::mma(L::rows(qt, 32 * n, i, lane), kf[i], s[0]);
+                for (int r = 0; r < 16; r += 4) {
+                    const f32x4 dl = as_f32x4(ld16(de + acc_row(r)));
 #pragma unroll
-                for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(gt, 32 * n, i, lane), vf[i], dp);
+                    for (int e = 0; e < 4; ++e) dp[r + e] = dl[e];
+                    if constexpr (RAW) {
+                        const f32x4 lv = as_f32x4(ld16(ls + acc_row(r)));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[0][r + e] = lv[e];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) s[0] = O::mma(L::rows(qt, 32 * n, i, lane), k_frag(i), s[0]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(gt, 32 * n, i, lane), v_frag(i), dp);
                 const int qn = q0 + 32 * n;
                 f32x16 slope;
                 if constexpr (CAP) {
@@ -461,18 +570,17 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 
                 if (qn < wave_most || qn + 32 > sp.lq) {
                     const int lo = my_first - qn - 4 * half, hi = sp.lq - qn - 4 * half;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[0][r] = acc_row(r) >= lo && acc_row(r) < hi ? s[0][r] : -INFINITY;
+                    for (int r = 0; r < 16; ++r) s[0][r] = acc_row(r) >= lo && acc_row(r) < hi ? s[0][r] : sc.none;
                 }
-                const float* ls = &stat[buf][copy][0][32 * n + 4 * half];
-                const float* de = &stat[buf][copy][1][32 * n + 4 * half];
 #pragma unroll
                 for (int r = 0; r < 16; r += 4) {
-                    const f32x4 lv = as_f32x4(ld16(ls + acc_row(r))), dl = as_f32x4(ld16(de + acc_row(r)));
+                    f32x4 lv{};
+                    if constexpr (!RAW) lv = as_f32x4(ld16(ls + acc_row(r)));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float x = s[0][r + e];
-                        s[0][r + e] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x, sc.a, -lv[e]) : x - lv[e]);
-                        dp[r + e] = s[0][r + e] * (dp[r + e] - dl[e]);
+                        s[0][r + e] = exp2_hw(RAW ? x * sc.a : x - lv[e]);
+                        dp[r + e] *= s[0][r + e];
                     }
                 }
                 if constexpr (CAP) dp *= slope;
@@ -518,18 +626,51 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 256 ? 1 : 
         write(dv, p.dv, 1.f);
         return;
     }
-    if (key >= sp.lk) return;
     T* dkg = static_cast<T*>(p.dk) + ((sp.k0 + key) * p.Hk + kvh) * D;
     T* dvg = static_cast<T*>(p.dv) + ((sp.k0 + key) * p.Hk + kvh) * D;
+    if constexpr (PAIRED) {
+        // the second wave of a pair hands its sums over, a tile's buffer for each pair
+        static_assert(!PAIRED || ELEMS * sizeof(T) == 32 * D * 4, "one buffer holds one wave's sums");
+        float* over = reinterpret_cast<float*>(wave == 0 ? q_a : wave == 1 ? g_a : wave == 2 ? q_b : g_b);
+        auto merge = [&](f32x16(&acc)[DT], T* out, float f) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-        dk[d] *= p.scale;
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            store4(dkg + 32 * d + 2 * r + 4 * half, dk[d][r], dk[d][r + 1], dk[d][r + 2], dk[d][r + 3]);
-            store4(dvg + 32 * d + 2 * r + 4 * half, dv[d][r], dv[d][r + 1], dv[d][r + 2], dv[d][r + 3]);
-        }
+                for (int r = 0; r < 16; r += 4) {
+                    f32x4* at = reinterpret_cast<f32x4*>(over + ((4 * d + r / 4) * kWave + lane) * 4);
+                    if (n_own == 1) *at = f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
+                }
+            __syncthreads();
+            if (n_own == 0) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4) {
+                        const f32x4 x = *reinterpret_cast<const f32x4*>(over + ((4 * d + r / 4) * kWave + lane) * 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[d][r + e] += x[e];
+                    }
+                if (key < sp.lk) {
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; r += 8) store_rows(out + 32 * d, acc[d], r, half, f);
+                }
+            }
+            __syncthreads();
+        };
+        merge(dk, dkg, p.scale);
+        merge(dv, dvg, 1.f);
+        return;
     }
+    if (key >= sp.lk) return;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 8) {
+            store_rows(dkg + 32 * d, dk[d], r, half, p.scale);
+            store_rows(dvg + 32 * d, dv[d], r, half, 1.f);
+        }
 }
 
 // Bytes of LDS that a workgroup may have (160 KB), less the largest fixed part of a split kernel.
@@ -538,6 +679,7 @@ constexpr size_t kSplitBiasLds = 163840 - 139264;
 template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
 int launch_dq(AttnParams p, hipStream_t stream) {
     p.q_slots = (int)slots_of(p.cu_q, p.total_q, p.nseq, kOwn<SPLIT>);
+    set_each(p, kOwn<SPLIT>, 1);
     const int64_t grid = (int64_t)p.q_slots * p.H;
     const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr);
     if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dq_kernel<T, D, CAP, BIAS, SPLIT>),
@@ -547,15 +689,19 @@ int launch_dq(AttnParams p, hipStream_t stream) {
     if (p.dtable) hipLaunchKernelGGL(attn_dtable_kernel, dim3((unsigned)p.H), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
-template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+template <typename T, int D, bool CAP, int BIAS, int SHARE>
 int launch_dkv(AttnParams p, hipStream_t stream) {
-    p.k_slots = (int)slots_of(p.cu_k, p.total_k, p.nseq, kOwn<SPLIT>);
+    constexpr int OWN = kOwn<SHARE == kSplit>;
+    p.k_slots = (int)slots_of(p.cu_k, p.total_k, p.nseq, OWN);
+    set_each(p, 1, OWN);
     const int64_t grid = (int64_t)p.k_slots * p.Hk;
-    const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (SPLIT ? p.H / p.Hk : 1);
-    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dkv_kernel<T, D, CAP, BIAS, SPLIT>),
+    const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (SHARE == kSplit ? p.H / p.Hk : 1);
+    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dkv_kernel<T, D, CAP, BIAS, SHARE>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return -1;
-    if (grid > 0) hipLaunchKernelGGL((attn_dkv_kernel<T, D, CAP, BIAS, SPLIT>), dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
+    if (grid > 0)
+        hipLaunchKernelGGL((attn_dkv_kernel<T, D, CAP, BIAS, SHARE>), dim3((unsigned)grid),
+                           dim3(SHARE == kPaired ? 2 * kThreads : kThreads), lds, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 template <typename T, int D, bool CAP, int BIAS>
@@ -565,8 +711,17 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
     const bool dkv_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (p.H / p.Hk) <= kSplitBiasLds;
     const bool dq_split = dq_fits && slots_of(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H < kSplitBelow;
     const bool dkv_split = dkv_fits && slots_of(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
-    int rc = dq_split ? launch_dq<T, D, CAP, BIAS, true>(p, stream) : launch_dq<T, D, CAP, BIAS, false>(p, stream);
-    if (rc == 0) rc = dkv_split ? launch_dkv<T, D, CAP, BIAS, true>(p, stream) : launch_dkv<T, D, CAP, BIAS, false>(p, stream);
+    AttnParams d = p;
+    d.plan_q = d.plan_k = nullptr;
+    if (p.plan_q && !(dq_split && dkv_split)) {
+        // sequences of different lengths, and more than a round of workgroups: the longest first
+        hipLaunchKernelGGL(attn_plan_kernel, dim3(2), dim3(kPlanThreads), 0, stream, p, dq_split ? 0 : kOwn<false>, dkv_split ? 0 : kOwn<false>);
+        if (!dq_split) d.plan_q = p.plan_q;
+        if (!dkv_split) d.plan_k = p.plan_k;
+    }
+    constexpr int WHOLE = sizeof(T) == 2 && D == 128 ? kPaired : kAlone;
+    int rc = dq_split ? launch_dq<T, D, CAP, BIAS, true>(d, stream) : launch_dq<T, D, CAP, BIAS, false>(d, stream);
+    if (rc == 0) rc = dkv_split ? launch_dkv<T, D, CAP, BIAS, kSplit>(d, stream) : launch_dkv<T, D, CAP, BIAS, WHOLE>(d, stream);
     return rc;
 }
 template <typename T, int D, bool CAP>

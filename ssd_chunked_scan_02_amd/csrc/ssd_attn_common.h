@@ -30,8 +30,6 @@ constexpr float kNoMax = -1e30f;
 // fourth tile through LDS of its own, and their results are joined at the end: four times the
 // workgroups, and a quarter of the way for each.
 template <bool SPLIT> constexpr int kOwn = SPLIT ? 32 : 128;
-// Workgroups of 128 rows below which the waves split instead.
-constexpr int64_t kSplitBelow = 512;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -167,66 +165,78 @@ struct Span {
     int lq, lk;      // their numbers
     int tile;        // tile of the axis the slots count; negative: the slot is empty
     int seq;
+    int slot;        // place of the tile in the axis's own order
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// Offsets as a call gave them, clamped into the axis, so that no offsets lead outside a tensor.
-__device__ __forceinline__ void span_of(const int64_t* cu, int64_t total, int64_t nseq, int64_t s, int64_t& first, int& len) {
-    if (!cu) {
-        const int64_t each = total / nseq;
-        first = s * each;
-        len = (int)each;
-        return;
+// Offset s as a call gave it, clamped into the axis, so that no offsets lead outside a tensor.
+__device__ __forceinline__ int offset_at(const int64_t* cu, int64_t s, int total) { return (int)clamp64(cu[s], 0, total); }
+
+// The last s in [0, nseq) with start(s) <= x, 64 sequences at a time: one step for 64 sequences, two for
+// 4096.  Called by whole waves.
+template <typename F> __device__ __forceinline__ int last_at_most(int nseq, F le) {
+    const int lane = threadIdx.x % kWave;
+    int lo = 0, n = nseq;
+    while (n > 1) {
+        const int step = (n - 1) / kWave + 1;
+        const int64_t s = lo + (int64_t)step * lane;
+        const int cnt = __popcll(__ballot(s < lo + n && le((int)s)));
+        const int at = cnt > 0 ? step * (cnt - 1) : 0;
+        lo += at;
+        n = min(n - at, step);
     }
-    const int64_t a = clamp64(cu[s], 0, total), b = clamp64(cu[s + 1], a, total);
-    first = a;
-    len = (int)(b - a);
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Sequence and tile of a slot.  Sequence s owns the slots from floor(cu[s] / own) + s on, one more than
 // its whole tiles at most, so that a workgroup finds its work from the offsets alone, with no list made
-// on the way: a search 64 sequences wide (one step for 64 sequences, two for 4096).
-template <typename F>
-__device__ __forceinline__ int64_t last_at_most(int64_t nseq, int64_t x, F start) {
-    const int lane = threadIdx.x % kWave;
-    int64_t lo = 0, n = nseq;  // the last s in [lo, lo + n) with start(s) <= x
-    while (n > 1) {
-        const int64_t step = (n + kWave - 1) / kWave;
-        const int64_t s = lo + step * lane;
-        const bool le = s < lo + n && start(s) <= x;
-        const int cnt = __popcll(__ballot(le));
-        const int64_t at = cnt > 0 ? step * (cnt - 1) : 0;
-        lo += at;
-        n = n - at < step ? n - at : step;
-    }
-    return __builtin_amdgcn_readfirstlane((int)lo);
-}
-__device__ __forceinline__ int slot_sequence(const int64_t* cu, int64_t total, int64_t nseq, int own, int slot) {
-    return (int)last_at_most(nseq, slot, [&](int64_t s) { return clamp64(cu[s], 0, total) / own + s; });
-}
-// The sequence whose tokens token t of a packed axis is among, if it is among any.
-__device__ __forceinline__ int64_t last_start(const int64_t* cu, int64_t nseq, int64_t t) {
-    return last_at_most(nseq, t, [&](int64_t s) { return cu[s]; });
-}
-
+// on the way; a list (p.plan_q, p.plan_k) orders the slots by their work instead.
 // (own: rows of a tile; by_keys: the slots count tiles of the key axis)
 __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, int own, bool by_keys) {
     const int64_t* cu = by_keys ? p.cu_k : p.cu_q;
-    const int64_t total = by_keys ? p.total_k : p.total_q;
-    Span sp;
+    const int2* plan = by_keys ? p.plan_k : p.plan_q;
+    const int tq = (int)p.total_q, tk = (int)p.total_k;
+    Span sp{};
     int s, tile;
-    if (!cu) {
-        const int per = (int)((total / p.nseq + own - 1) / own);
-        s = slot / per;
-        tile = slot % per;
+    sp.slot = slot;
+    if (plan) {
+        const int2 e = plan[slot];
+        s = __builtin_amdgcn_readfirstlane(e.x);
+        tile = __builtin_amdgcn_readfirstlane(e.y);
+        if (tile < 0) {  // (an empty slot's entry is its place and not a sequence)
+            sp.slot = s;
+            sp.tile = -1;
+            return sp;
+        }
+        sp.slot = offset_at(cu, s, by_keys ? tk : tq) / own + s + tile;
+    } else if (!cu) {
+        const int per = by_keys ? p.each_k_tiles : p.each_q_tiles;
+        s = (int)((uint32_t)slot / (uint32_t)per);
+        tile = slot - s * per;
     } else {
-        s = slot_sequence(cu, total, p.nseq, own, slot);
-        tile = slot - (int)(clamp64(cu[s], 0, total) / own + s);
+        const int total = by_keys ? tk : tq;
+        s = last_at_most((int)p.nseq, [&](int i) { return offset_at(cu, i, total) / own + i <= slot; });
+        tile = slot - (offset_at(cu, s, total) / own + s);
     }
     sp.seq = s;
-    span_of(p.cu_q, p.total_q, p.nseq, s, sp.q0, sp.lq);
-    span_of(p.cu_k, p.total_k, p.nseq, s, sp.k0, sp.lk);
+    int q0, k0;
+    if (p.cu_q) {
+        q0 = offset_at(p.cu_q, s, tq);
+        sp.lq = max(offset_at(p.cu_q, s + 1, tq) - q0, 0);
+    } else {
+        sp.lq = p.each_q;
+        q0 = s * sp.lq;
+    }
+    if (p.cu_k) {
+        k0 = offset_at(p.cu_k, s, tk);
+        sp.lk = max(offset_at(p.cu_k, s + 1, tk) - k0, 0);
+    } else {
+        sp.lk = p.each_k;
+        k0 = s * sp.lk;
+    }
+    sp.q0 = q0;
+    sp.k0 = k0;
     const int len = by_keys ? sp.lk : sp.lq;
     sp.tile = tile >= 0 && (int64_t)tile * own < len ? tile : -1;
     return sp;
@@ -237,14 +247,41 @@ inline int64_t slots_of(const int64_t* cu, int64_t total, int64_t nseq, int own)
     if (nseq == 0) return 0;
     return cu ? total / own + nseq : nseq * ((total / nseq + own - 1) / own);
 }
+// Lengths and tiles of equal sequences.
+inline void set_each(AttnParams& p, int q_own, int k_own) {
+    p.each_q = p.nseq ? (int)(p.total_q / p.nseq) : 0;
+    p.each_k = p.nseq ? (int)(p.total_k / p.nseq) : 0;
+    p.each_q_tiles = (p.each_q + q_own - 1) / q_own;
+    p.each_k_tiles = (p.each_k + k_own - 1) / k_own;
+}
 
 // Workgroup -> (slot, head).  Heads run fastest, the slots from the last (under a causal mask the
 // longest) to the first.  Workgroups reach the 8 XCDs in turn, so with 8 or more heads an XCD keeps a
 // run of neighbouring heads, which share keys and values in its L2.
-__device__ __forceinline__ void work_item(int64_t id, int slots, int H, int& slot, int& head) {
-    const int x = (int)(id % H);
-    slot = slots - 1 - (int)(id / H);
-    head = H % 8 == 0 ? (x % 8) * (H / 8) + x / 8 : x;
+__device__ __forceinline__ void work_item(uint32_t id, int slots, uint32_t H, int& slot, int& head) {
+    const uint32_t at = id / H, x = id - at * H;
+    slot = slots - 1 - (int)at;
+    head = (int)(H % 8 == 0 ? (x % 8) * (H / 8) + x / 8 : x);
+}
+
+// Two neighbouring groups of four accumulator rows (r .. r + 3 and r + 4 .. r + 7) of a 32-row tile hold, over
+// both lane halves, rows 2 r .. 2 r + 7 and 2 r + 8 .. 2 r + 15.  Swapping one against the other between the halves
+// gives each lane eight rows in a row: 2 r + 8 half .., one 16-byte store in bf16 (two in fp32).
+template <typename T> __device__ __forceinline__ void store_rows(T* out, const f32x16& v, int r, int half, float f) {
+    if constexpr (sizeof(T) == 2) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)(v[r + 2 * i] * f), (__bf16)(v[r + 2 * i + 1] * f)});
+        // (word i of the first group against word i of the second: the first's upper lanes for the second's lower)
+        const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+        st16(out + 2 * r + 8 * half, uint4{a[0], b[0], a[1], b[1]});
+    } else {
+        store4(out + 2 * r + 4 * half, v[r] * f, v[r + 1] * f, v[r + 2] * f, v[r + 3] * f);
+        store4(out + 2 * r + 8 + 4 * half, v[r + 4] * f, v[r + 5] * f, v[r + 6] * f, v[r + 7] * f);
+    }
 }
 
 // Bucket of a relative position (key - query).
@@ -265,17 +302,18 @@ __device__ __forceinline__ void fill_bias(float* lut, const AttnParams& p, int h
 }
 
 // What turns a raw product x = q.k into a score in log2 units, and the derivative of the cap.
-//   no cap: x * a, a = |scale| log2 e (the sign of the scale is in the operands: see `signed_frag`)
-//   cap c:  c tanh(x |scale| / c) log2 e
+//   no cap: x * a, a = scale log2 e
+//   cap c:  c tanh(x scale / c) log2 e
 struct Score {
-    float a;       // no cap: |scale| log2 e; cap: 2 |scale| log2 e / c (bf16) or |scale| / c (fp32)
+    float a;       // no cap: scale log2 e; cap: 2 scale log2 e / c (bf16) or scale / c (fp32)
     float c2;      // c log2 e
     float rc2;     // 1 / c2
-    float k[4];    // cap, bf16: c2 tanh(x |scale| / c) = x (k0 + k1 x^2 + k2 x^4 + k3 x^6) where x^2 <= small
+    float k[4];    // cap, bf16: c2 tanh(x scale / c) = x (k0 + k1 x^2 + k2 x^4 + k3 x^6) where x^2 <= small
     float small;
-    template <typename T> __device__ __forceinline__ void init(float scale, float cap, bool capped) {
+    float none;    // a masked score, or (raw) a masked product
+    template <typename T> __device__ __forceinline__ void init(float scale, float cap, bool capped, bool raw = false) {
         // (a scale of zero: a finite factor times a masked score has to stay minus infinity)
-        const float s = fmaxf(fabsf(scale), 1e-30f), u = capped ? s / cap : 0.f;
+        const float s = fabsf(scale) < 1e-30f ? 1e-30f : scale, u = capped ? s / cap : 0.f;
         c2 = cap * kLog2e;
         rc2 = capped ? 1.f / c2 : 0.f;
         a = !capped ? s * kLog2e : sizeof(T) == 4 ? u : 2.f * u * kLog2e;
@@ -283,6 +321,7 @@ struct Score {
         k[1] = k[0] * u * u * (-1.f / 3.f);
         k[2] = k[0] * (u * u) * (u * u) * (2.f / 15.f);
         k[3] = k[0] * (u * u) * (u * u) * (u * u) * (-17.f / 315.f);
+        none = raw && s < 0.f ? INFINITY : -INFINITY;
         small = capped ? 0.0625f / (u * u) : 0.f;
     }
     // The capped scores of N products, in place.  bf16: the series of tanh where all of the wave's arguments
@@ -329,7 +368,8 @@ struct Score {
     }
 };
 
-// 16 bytes of an operand that meets only scores, with the sign of the scale.
+// 16 bytes of a query for the forward pass, with the sign of the scale: its maxima are taken of raw products,
+// whose factor has to be positive then.
 template <typename T> __device__ __forceinline__ typename Op<T>::Frag signed_frag(const T* g, float scale) {
     typename Op<T>::Frag f = __builtin_bit_cast(typename Op<T>::Frag, ld16(g));
     if (scale < 0.f) f = -f;

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
     const int b0 = split * per, b1 = min(b0 + per, blocks);
 
     Score sc;
-    sc.init<T>(p.scale, p.cap, CAP);
+    sc.init<T>(fabsf(p.scale), p.cap, CAP);
     const int head = head0 + min(col, heads - 1);
     Frag qf[NT];
 #pragma unroll
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
     const int64_t tok = blockIdx.x;
     int64_t s = tok, end = tok + 1;
     if (p.cu) {
-        s = last_start(p.cu, p.nseq, tok);
+        s = last_at_most((int)p.nseq, [&](int i) { return p.cu[i] <= tok; });
         end = p.cu[s + 1];
         if (tok < p.cu[s] || tok >= end) return;  // a token of no sequence
     }

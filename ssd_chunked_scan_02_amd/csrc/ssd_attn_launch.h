@@ -24,6 +24,9 @@ struct AttnBuckets {
     int borders[kMaxBorders];
 };
 
+// Workgroups of 128 rows below which the four waves of one split instead (kOwn in ssd_attn_common.h).
+constexpr int64_t kSplitBelow = 512;
+
 struct AttnParams {
     const void* q;
     const void* k;
@@ -47,6 +50,9 @@ struct AttnParams {
     int H, Hk;
     int causal;
     int q_slots, k_slots; // tiles of the packed axes (bounds: some are empty)
+    int each_q, each_k, each_q_tiles, each_k_tiles;  // equal sequences: their lengths and tiles
+    int2* plan_q;         // workspace: (sequence, tile) of the slots in order of their work, or null
+    int2* plan_k;
     float scale, cap;
     AttnBuckets bk;
 };
