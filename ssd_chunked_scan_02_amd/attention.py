@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from . import SSD_OK, SSDError, _DTYPE_CODE, _check, _on_stream, _ptr, _stream_handle, load_library
+from . import SSD_OK, SSDError, _DTYPE_CODE, _check, _on_stream, load_library
 
 
 class AttnDims(ctypes.Structure):
@@ -51,8 +51,44 @@ def declare(lib):
     lib.ssd_kv_append.restype = i32
 
 
+# The calls below are short (a decode step's kernels take some microseconds), so the checks first ask whether
+# everything is as it should be, in as few steps as that takes, and only then what is not.
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t, name, shape, dtype, device):
+    """As _check."""
+    if t is not None and not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _check(t, name, shape, dtype, device)
+
+
+def _call(name, device, stream, *args):
+    """The library's function on the caller's stream of the tensors' device, which is made the current one for it
+    where it is another's."""
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream.cuda_stream
+    function = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        rc = function(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = function(*args, handle)
+    if rc != SSD_OK:
+        raise SSDError(rc, name)
+
+
 def _token_stride(t, name, dim, dtype, device):
     """Elements from one token to the next of a tensor [..., tokens, heads, D] whose tokens are dense."""
+    if dim == 3 and t.dim() == 3 and t.dtype is dtype and t.device == device and device.type == "cuda":
+        tokens, heads, D = t.shape
+        step, s1, s0 = t.stride()
+        if s0 == 1 and s1 == D and step >= heads * D and tokens > 1:
+            return step
     if t.dim() != dim:
         raise ValueError("%s must have %d dimensions, got shape %s" % (name, dim, tuple(t.shape)))
     if not t.is_cuda:
@@ -78,7 +114,7 @@ def _token_stride(t, name, dim, dtype, device):
 
 
 def _offsets(t, name, device, n=None):
-    if t is None:
+    if t is None or (n is not None and t.dtype is torch.int64 and t.shape == (n,) and t.device == device and t.is_contiguous()):
         return
     if t.dtype != torch.int64 or t.dim() != 1 or t.device != device or not t.is_contiguous() or (n is None and t.numel() < 1):
         raise ValueError("%s must be a contiguous 1-D int64 tensor on q's device" % name)
@@ -87,13 +123,15 @@ def _offsets(t, name, device, n=None):
 
 
 def _bias_args(slopes, table, H, device):
+    if slopes is None and table is None:
+        return 0
     if slopes is not None and table is not None:
         raise ValueError("slopes and table are two forms of the bias: give at most one")
-    _check(slopes, "slopes", (H,), torch.float32, device)
+    _dense(slopes, "slopes", (H,), torch.float32, device)
     if table is not None:
         if table.dim() != 2:
             raise ValueError("table must be [num_buckets, H]")
-        _check(table, "table", (table.shape[0], H), torch.float32, device)
+        _dense(table, "table", (table.shape[0], H), torch.float32, device)
     return 0 if table is None else table.shape[0]
 
 
@@ -142,19 +180,15 @@ def ssd_attn_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal: bool =
     dev = q.device
     if y is None:
         y = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _check(y, "y", q.shape, q.dtype, dev)
+    _dense(y, "y", q.shape, q.dtype, dev)
     if lse is True:
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
     elif lse is False:
         lse = None
-    _check(lse, "lse", q.shape[:-1], torch.float32, dev)
+    _dense(lse, "lse", q.shape[:-1], torch.float32, dev)
     _on_stream(stream, y, lse)
-    with torch.cuda.device(dev):
-        rc = load_library().ssd_attn_forward(
-            ctypes.byref(dims), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _ptr(prefix), _ptr(q), _ptr(k), _ptr(v),
-            _ptr(slopes), _ptr(table), _ptr(y), _ptr(lse), _stream_handle(stream, dev))
-    if rc != SSD_OK:
-        raise SSDError(rc, "ssd_attn_forward")
+    _call("ssd_attn_forward", dev, stream, ctypes.byref(dims), _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(prefix),
+          _addr(q), _addr(k), _addr(v), _addr(slopes), _addr(table), _addr(y), _addr(lse))
     return y, lse
 
 
@@ -172,9 +206,9 @@ def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, c
     dims = _dims(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, softcap, slopes, table, max_distance, bidirectional,
                  prefix)
     dev = q.device
-    _check(y, "y", q.shape, q.dtype, dev)
-    _check(dy, "dy", q.shape, q.dtype, dev)
-    _check(lse, "lse", q.shape[:-1], torch.float32, dev)
+    _dense(y, "y", q.shape, q.dtype, dev)
+    _dense(dy, "dy", q.shape, q.dtype, dev)
+    _dense(lse, "lse", q.shape[:-1], torch.float32, dev)
     if want_dtable is None:
         want_dtable = table is not None
     if want_dtable and table is None:
@@ -189,13 +223,9 @@ def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, c
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _on_stream(stream, workspace, *out.values())
-    with torch.cuda.device(dev):
-        rc = load_library().ssd_attn_backward(
-            ctypes.byref(dims), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _ptr(prefix), _ptr(q), _ptr(k), _ptr(v),
-            _ptr(slopes), _ptr(table), _ptr(y), _ptr(lse), _ptr(dy), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-            _ptr(out.get("dtable")), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
-    if rc != SSD_OK:
-        raise SSDError(rc, "ssd_attn_backward")
+    _call("ssd_attn_backward", dev, stream, ctypes.byref(dims), _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(prefix),
+          _addr(q), _addr(k), _addr(v), _addr(slopes), _addr(table), _addr(y), _addr(lse), _addr(dy), _addr(out["dq"]),
+          _addr(out["dk"]), _addr(out["dv"]), _addr(out.get("dtable")), _addr(workspace), ws_bytes)
     return out
 
 
@@ -207,14 +237,14 @@ def _cache_dims(q, heads, k_cache, v_cache, block_table, seq_lens, strides, scal
         raise TypeError("the cache's tensors must be float32 or bfloat16, got %s" % q.dtype)
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, page_size, Hk, D], got shape %s" % (tuple(k_cache.shape),))
-    _check(k_cache, "k_cache", k_cache.shape, q.dtype, dev)
-    _check(v_cache, "v_cache", k_cache.shape, q.dtype, dev)
+    _dense(k_cache, "k_cache", k_cache.shape, q.dtype, dev)
+    _dense(v_cache, "v_cache", k_cache.shape, q.dtype, dev)
     pages, size, Hk, D = k_cache.shape
-    _offsets(seq_lens, "seq_lens", dev)
     nseq = seq_lens.numel()
+    _offsets(seq_lens, "seq_lens", dev, nseq)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [nseq, max_pages]")
-    _check(block_table, "block_table", (nseq, block_table.shape[1]), torch.int32, dev)
+    _dense(block_table, "block_table", (nseq, block_table.shape[1]), torch.int32, dev)
     return AttnCache(nseq, heads, Hk, D, pages, size, block_table.shape[1], *strides,
                      D ** -0.5 if scale is None else float(scale), float(softcap), _DTYPE_CODE[q.dtype], buckets,
                      int(max_distance), int(bool(bidirectional)))
@@ -241,18 +271,14 @@ def ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
         raise ValueError("q %s does not fit %d sequences of head dim %d" % (tuple(q.shape), dims.nseq, dims.headdim))
     if y is None:
         y = torch.empty((nseq, H, D), dtype=q.dtype, device=dev)
-    _check(y, "y", (nseq, H, D), q.dtype, dev)
+    _dense(y, "y", (nseq, H, D), q.dtype, dev)
     need = ssd_attn_decode_workspace_bytes(dims)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _on_stream(stream, y, workspace)
-    with torch.cuda.device(dev):
-        rc = load_library().ssd_attn_decode(
-            ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(slopes),
-            _ptr(table), _ptr(y), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
-    if rc != SSD_OK:
-        raise SSDError(rc, "ssd_attn_decode")
+    _call("ssd_attn_decode", dev, stream, ctypes.byref(dims), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table),
+          _addr(seq_lens), _addr(slopes), _addr(table), _addr(y), _addr(workspace), ws_bytes)
     return y
 
 
@@ -278,20 +304,16 @@ def ssd_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None
     if cu_seqlens is None and tokens != dims.nseq:
         raise ValueError("%d tokens for %d sequences: give cu_seqlens" % (tokens, dims.nseq))
     if inv_freq is not None:
-        _check(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, dev)
+        _dense(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, dev)
     if q is None:
         if q_out is not None:
             raise ValueError("q_out needs q")
     else:
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _check(q_out, "q_out", q.shape, q.dtype, dev)
+        _dense(q_out, "q_out", q.shape, q.dtype, dev)
     _on_stream(stream, q_out)
-    with torch.cuda.device(dev):
-        rc = load_library().ssd_kv_append(
-            ctypes.byref(dims), tokens, _ptr(cu_seqlens), _ptr(seq_lens), _ptr(block_table), _ptr(k), _ptr(v), _ptr(q),
-            _ptr(inv_freq), 0 if inv_freq is None else inv_freq.numel(), int(bool(interleaved)), _ptr(k_cache),
-            _ptr(v_cache), _ptr(q_out), _stream_handle(stream, dev))
-    if rc != SSD_OK:
-        raise SSDError(rc, "ssd_kv_append")
+    _call("ssd_kv_append", dev, stream, ctypes.byref(dims), tokens, _addr(cu_seqlens), _addr(seq_lens), _addr(block_table),
+          _addr(k), _addr(v), _addr(q), _addr(inv_freq), 0 if inv_freq is None else inv_freq.numel(), int(bool(interleaved)),
+          _addr(k_cache), _addr(v_cache), _addr(q_out))
     return q_out

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
         if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
     };
+    const typename L::Lanes z(lane);
     auto step = [&](const T* kt, const T* vt, T* kn, T* vn, int t) {
         const int k0 = t * KT;
         if (DOUBLE && t + dt < ntiles) fetch(kn, vn, t + dt);
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             for (int n = 0; n < NS; ++n) {
                 s[n] = f32x16{};
 #pragma unroll
-                for (int i = 0; i < NT; ++i) s[n] = O::mma(L::rows(kt, 32 * n, i, lane), qf[i], s[n]);
+                for (int i = 0; i < NT; ++i) s[n] = O::mma(L::rows(kt, 32 * n, i, z), qf[i], s[n]);
             }
             if constexpr (CAP) sc.template capped<T>(s);
             add_bias<BIAS, 1>(s, CAP ? 1.f : sc.a, slope2, lut, p.bk.max_distance, k0 + 4 * half - qpos,
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                 for (int kk = 0; kk < PK; ++kk) {
                     const Frag pf = O::pack(s[n], kk);
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) o[d] = O::mma(L::cols(vt, 32 * n, kk, 32 * d, lane), pf, o[d]);
+                    for (int d = 0; d < DT; ++d) o[d] = O::mma(L::cols(vt, 32 * n, kk, 32 * d, z), pf, o[d]);
                 }
         }
         settle();
@@ -208,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 
 template <typename T, int D, int CAPPED, int BIAS>
 int launch_fwd(AttnParams p, hipStream_t stream) {
-    const int64_t whole = slots_of(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H;
+    const int64_t whole = attn_slots(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H;
     const bool split = whole < kSplitBelow;
-    p.q_slots = (int)slots_of(p.cu_q, p.total_q, p.nseq, split ? kOwn<true> : kOwn<false>);
+    p.q_slots = (int)attn_slots(p.cu_q, p.total_q, p.nseq, split ? kOwn<true> : kOwn<false>);
     set_each(p, split ? kOwn<true> : kOwn<false>, 1);
     const int64_t grid = (int64_t)p.q_slots * p.H;
     if (grid == 0) return 0;

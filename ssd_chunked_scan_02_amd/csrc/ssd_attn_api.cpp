@@ -74,6 +74,10 @@ int make_buckets(ssd::AttnBuckets& out, int num_buckets, int max_distance, int b
         if (std::fabs(x - near) < 1e-9 * x) d = reached(near, e, f, max_distance, k) ? near : near + 1;
         out.borders[at++] = d;
     }
+    for (int d = 0, b = 0; d <= max_distance; ++d) {
+        while (b < out.nborders && out.borders[b] <= d) ++b;
+        out.of[d] = (uint8_t)b;
+    }
     return SSD_OK;
 }
 
@@ -152,9 +156,10 @@ size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 // Workspace of the backward pass: D per (query, head), the table's partial gradients, and the orders of
 // the query and key tiles (twice each: as found and as sorted).  The tiles are bounded without the
 // offsets, so that the size does not depend on how a call gives its sequences; table gradients of small
-// problems come in tiles of 32 queries.
+// problems come in tiles of 32 queries, and their key gradients in parts (an equal batch has the fewest
+// tiles, and so the most parts).
 struct BackwardWorkspace {
-    size_t delta, part, plan_q, plan_k, total;
+    size_t delta, part, dkv, plan_q, plan_k, total;
 };
 BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
     BackwardWorkspace w{};
@@ -163,9 +168,11 @@ BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
     if (d->total_q / 128 * d->nheads < ssd::kSplitBelow) parts = d->total_q / 32 + d->nseq + 1;
     w.delta = align16((size_t)d->total_q * (size_t)d->nheads * 4);
     w.part = table ? align16((size_t)parts * (size_t)d->nheads * (size_t)d->num_buckets * 4) : 0;
+    const int n = d->nseq > 0 ? ssd::attn_key_parts(nullptr, d->total_k - d->total_k % d->nseq, d->nseq, d->nkvheads) : 1;
+    w.dkv = n > 1 ? align16((size_t)(2 * n) * (size_t)d->total_k * (size_t)d->nkvheads * (size_t)d->headdim * 4) : 0;
     w.plan_q = align16((size_t)q_slots * 16);
     w.plan_k = align16((size_t)k_slots * 16);
-    w.total = w.delta + w.part + w.plan_q + w.plan_k;
+    w.total = w.delta + w.part + w.dkv + w.plan_q + w.plan_k;
     return w;
 }
 
@@ -261,9 +268,10 @@ int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, co
     p.delta = static_cast<float*>(workspace);
     char* at = static_cast<char*>(workspace) + w.delta;
     p.table_part = dtable ? reinterpret_cast<float*>(at) : nullptr;
+    p.dkv_part = w.dkv > 0 ? reinterpret_cast<float*>(at + w.part) : nullptr;
     if (p.cu_q && p.nseq > 1) {
-        p.plan_q = reinterpret_cast<int2*>(at + w.part);
-        p.plan_k = reinterpret_cast<int2*>(at + w.part + w.plan_q);
+        p.plan_q = reinterpret_cast<int2*>(at + w.part + w.dkv);
+        p.plan_k = reinterpret_cast<int2*>(at + w.part + w.dkv + w.plan_q);
     }
     return code(ssd::launch_attn_backward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
 }

@@ -34,16 +34,17 @@ __host__ __device__ inline int bias_floats(int bias, int md, bool grad) {
     return reach + (grad ? kWaves * (reach + kDiagBlock) + 2 * kWaves : 0);
 }
 
-// Sum of a bucket's cells over the sums by relative position (a wave's array, interior only: distances of
-// max_distance and more are summed apart).
-__device__ __forceinline__ float fold_bucket(const AttnBuckets& b, const float* sums, int bucket) {
+// A thread's share (every `step`-th distance from `from` on) of a bucket's cells in the sums by relative position;
+// interior only: distances of max_distance and more are summed apart.
+__device__ __forceinline__ float fold_bucket(const AttnBuckets& b, const float* sums, int bucket, int from, int step) {
     const int n = b.nborders + 1, in = bucket % n;
     const bool behind = b.both && bucket >= n;
     const int lo = in == 0 ? 0 : b.borders[in - 1], hi = in == n - 1 ? b.max_distance : b.borders[in];
     float v = 0.f;
-    for (int d = behind && lo == 0 ? 1 : lo; d < hi; ++d) v += sums[b.max_distance + (behind ? d : -d)];
+    for (int d = lo + from; d < hi; d += step)
+        if (!behind || d > 0) v += sums[b.max_distance + (behind ? d : -d)];
     if (!b.both && in == 0)
-        for (int d = 1; d < b.max_distance; ++d) v += sums[b.max_distance + d];
+        for (int d = 1 + from; d < b.max_distance; d += step) v += sums[b.max_distance + d];
     return v;
 }
 
@@ -150,14 +151,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     };
     // p and dS of 32 keys from kn on (dS before the cap's derivative, which is returned in `slope`); true: some
     // are nearer than the table's reach
+    typename L::Lanes z(lane);
     auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope) {
+        if constexpr (sizeof(T) * D >= 256) z.renew();
         f32x16 x[1] = {f32x16{}}, dp;
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] = -delta;  // the accumulator starts at -D: dP - D at no cost
 #pragma unroll
-        for (int i = 0; i < NT; ++i) x[0] = O::mma(L::rows(kt, 32 * n, i, lane), qf[i], x[0]);
+        for (int i = 0; i < NT; ++i) x[0] = O::mma(L::rows(kt, 32 * n, i, z), qf[i], x[0]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, lane), gf[i], dp);
+        for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, z), gf[i], dp);
         if constexpr (CAP) {
             sc.template capped<T>(x);
 #pragma unroll
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                 for (int kk = 0; kk < PK; ++kk) {
                     const Frag sf = O::pack(ds, kk);
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) acc[d] = O::mma(L::cols(kt, 32 * n, kk, 32 * d, lane), sf, acc[d]);
+                    for (int d = 0; d < DT; ++d) acc[d] = O::mma(L::cols(kt, 32 * n, kk, 32 * d, z), sf, acc[d]);
                 }
             }
         }
@@ -307,14 +310,44 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             far[kWaves + wave] = far_hi;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < p.bk.total; i += kThreads) {
-            float v = 0.f;
-            for (int w = 0; w < kWaves; ++w) {
-                v += fold_bucket(p.bk, extra + reach + w * reach, i);
-                if (i == p.bk.nborders) v += far[w];  // the last bucket of the first direction
-                if (i == (p.bk.both ? p.bk.total - 1 : 0)) v += far[kWaves + w];
+        float* all = extra + reach;
+        for (int i = threadIdx.x; i < reach; i += kThreads) {
+            float v = all[i];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += all[w * reach + i];
+            all[i] = v;
+        }
+        __syncthreads();
+        // as many lanes to a bucket as there are, in powers of two
+        const int lanes = 1 << (31 - __clz(kThreads / p.bk.total)), i = (int)threadIdx.x / lanes;
+        const int per = min(lanes, kWave);
+        if (i < p.bk.total) {
+            float v = fold_bucket(p.bk, all, i, threadIdx.x % lanes, lanes);
+            for (int off = per / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+            if (lanes <= kWave) {
+                if (threadIdx.x % lanes == 0) {
+                    for (int w = 0; w < kWaves; ++w) {
+                        if (i == p.bk.nborders) v += far[w];  // the last bucket of the first direction
+                        if (i == (p.bk.both ? p.bk.total - 1 : 0)) v += far[kWaves + w];
+                    }
+                    part[i] = v;
+                }
+            } else if (lane == 0) {  // (two buckets: two waves each)
+                block[0] = v;
             }
-            part[i] = v;
+        }
+        if (lanes > kWave) {
+            __syncthreads();
+            if ((int)threadIdx.x < p.bk.total) {
+                const int b = threadIdx.x, waves = lanes / kWave;
+                float v = 0.f;
+                for (int w = 0; w < waves; ++w) v += extra[(1 + kWaves) * reach + (b * waves + w) * kDiagBlock];
+                for (int w = 0; w < kWaves; ++w) {
+                    if (b == p.bk.nborders) v += far[w];
+                    if (b == (p.bk.both ? p.bk.total - 1 : 0)) v += far[kWaves + w];
+                }
+                part[b] = v;
+            }
         }
     }
 }
@@ -432,7 +465,9 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
     float* lut = extra;
 
     int slot, kvh;
-    work_item(blockIdx.x, p.k_slots, p.Hk, slot, kvh);
+    work_item(blockIdx.x, p.k_slots, SPLIT ? p.Hk * p.parts : p.Hk, slot, kvh);
+    const int part = SPLIT ? kvh % p.parts : 0;
+    if constexpr (SPLIT) kvh /= p.parts;
     if (!p.plan_k) slot = p.k_slots - 1 - slot;  // under a causal mask the first keys are seen by the most queries
     const Span sp = find_span(p, slot, OWN, true);
     if (sp.tile < 0) return;
@@ -451,7 +486,10 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
     const int my_first = key < sp.lk ? first(key) : sp.lq;
     const int wave_least = row0 < sp.lk ? first(row0) : sp.lq;  // the earliest query that any key of the wave meets
     const int wave_most = row0 + 32 <= sp.lk ? first(row0 + 31) : sp.lq;  // from here on every key meets every query
-    const int per_head = max(t1 - t0, 0), ntiles = per_head * group;
+    const int per_head = max(t1 - t0, 0), all_tiles = per_head * group;
+    // (SPLIT: this workgroup's part of them)
+    const int first_tile = SPLIT ? (int)((int64_t)all_tiles * part / p.parts) : 0;
+    const int ntiles = SPLIT ? (int)((int64_t)all_tiles * (part + 1) / p.parts) : all_tiles;
 
     Feed<T, D, QT, THREADS> qf, gf;
     qf.init(p.q_stride);
@@ -485,7 +523,7 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
     const int at = copy * QT * D;
     T *qa = q_a + at, *ga = g_a + at, *qb = q_b + (DOUBLE ? at : 0), *gb = g_b + (DOUBLE ? at : 0);
     // SPLIT: a wave takes every fourth tile
-    const int i0 = SPLIT ? wave : 0, di = SPLIT ? kWaves : 1;
+    const int i0 = SPLIT ? first_tile + wave : 0, di = SPLIT ? kWaves : 1;
     if (i0 < ntiles) fetch(qa, ga, i0);
 
     Frag kf[PAIRED ? 1 : NT], vf[PAIRED ? 1 : NT];
@@ -506,8 +544,9 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
             vf[t] = __builtin_bit_cast(Frag, ld16(vg + (2 * t + half) * O::kE));
         }
     }
-    auto k_frag = [&](int i) { return PAIRED ? L::rows(k_own, 32 * wave, i, lane) : kf[PAIRED ? 0 : i]; };
-    auto v_frag = [&](int i) { return PAIRED ? L::rows(v_own, 32 * wave, i, lane) : vf[PAIRED ? 0 : i]; };
+    typename L::Lanes z(lane);
+    auto k_frag = [&](int i) { return PAIRED ? L::rows(k_own, 32 * wave, i, z) : kf[PAIRED ? 0 : i]; };
+    auto v_frag = [&](int i) { return PAIRED ? L::rows(v_own, 32 * wave, i, z) : vf[PAIRED ? 0 : i]; };
     const int md = p.bk.max_distance;
     if constexpr (BIAS == kBiasBuckets) {
         // one head's bias, refilled where the head changes; SPLIT: the waves are on different heads at a time,
@@ -539,6 +578,7 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 const int n = PAIRED ? n_own : j;
+                if constexpr (PAIRED) z.renew();
                 const float* ls = &stat[buf][copy][0][32 * n + 4 * half];
                 const float* de = &stat[buf][copy][1][32 * n + 4 * half];
                 f32x16 s[1] = {f32x16{}}, dp;
@@ -554,9 +594,9 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < NT; ++i) s[0] = O::mma(L::rows(qt, 32 * n, i, lane), k_frag(i), s[0]);
+                for (int i = 0; i < NT; ++i) s[0] = O::mma(L::rows(qt, 32 * n, i, z), k_frag(i), s[0]);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(gt, 32 * n, i, lane), v_frag(i), dp);
+                for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(gt, 32 * n, i, z), v_frag(i), dp);
                 const int qn = q0 + 32 * n;
                 f32x16 slope;
                 if constexpr (CAP) {
@@ -589,8 +629,8 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
                     const Frag pf = O::pack(s[0], kk), sf = O::pack(dp, kk);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
-                        dv[d] = O::mma(L::cols(gt, 32 * n, kk, 32 * d, lane), pf, dv[d]);
-                        dk[d] = O::mma(L::cols(qt, 32 * n, kk, 32 * d, lane), sf, dk[d]);
+                        dv[d] = O::mma(L::cols(gt, 32 * n, kk, 32 * d, z), pf, dv[d]);
+                        dk[d] = O::mma(L::cols(qt, 32 * n, kk, 32 * d, z), sf, dk[d]);
                     }
                 }
             }
@@ -619,11 +659,13 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
                 const int r = i / (D / 4), d4 = i % (D / 4);
                 if (row0 + r >= sp.lk) break;
                 const f32x4 v = Join<T, D>::sum(q_a, g_a, r, d4, nullptr) * scale;
-                store4(static_cast<T*>(to) + ((sp.k0 + row0 + r) * p.Hk + kvh) * D + 4 * d4, v[0], v[1], v[2], v[3]);
+                const int64_t at = ((sp.k0 + row0 + r) * p.Hk + kvh) * D + 4 * d4;
+                if (p.parts > 1) store4(static_cast<float*>(to) + part * p.total_k * p.Hk * D + at, v[0], v[1], v[2], v[3]);
+                else store4(static_cast<T*>(to) + at, v[0], v[1], v[2], v[3]);
             }
         };
-        write(dk, p.dk, p.scale);
-        write(dv, p.dv, 1.f);
+        write(dk, p.parts > 1 ? p.dkv_part : p.dk, p.scale);
+        write(dv, p.parts > 1 ? p.dkv_part + p.parts * p.total_k * p.Hk * D : p.dv, 1.f);
         return;
     }
     T* dkg = static_cast<T*>(p.dk) + ((sp.k0 + key) * p.Hk + kvh) * D;
@@ -673,12 +715,32 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
         }
 }
 
+// dk (blockIdx.y = 0) and dv (1) of one tile and key head from its parts, in order.
+template <typename T, int D> __global__ void __launch_bounds__(kThreads) attn_parts_kernel(AttnParams p) {
+    constexpr int OWN = kOwn<true>;
+    int slot, kvh;
+    work_item(blockIdx.x, p.k_slots, p.Hk, slot, kvh);
+    const Span sp = find_span(p, slot, OWN, true);
+    if (sp.tile < 0) return;
+    const int64_t tensor = p.total_k * p.Hk * D;
+    const float* from = p.dkv_part + blockIdx.y * p.parts * tensor;
+    T* to = static_cast<T*>(blockIdx.y ? p.dv : p.dk);
+    for (int i = threadIdx.x; i < OWN * (D / 4); i += kThreads) {
+        const int r = sp.tile * OWN + i / (D / 4);
+        if (r >= sp.lk) break;
+        const int64_t at = ((sp.k0 + r) * p.Hk + kvh) * D + 4 * (i % (D / 4));
+        f32x4 v{};
+        for (int n = 0; n < p.parts; ++n) v += as_f32x4(ld16(from + n * tensor + at));
+        store4(to + at, v[0], v[1], v[2], v[3]);
+    }
+}
+
 // Bytes of LDS that a workgroup may have (160 KB), less the largest fixed part of a split kernel.
 constexpr size_t kSplitBiasLds = 163840 - 139264;
 
 template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
 int launch_dq(AttnParams p, hipStream_t stream) {
-    p.q_slots = (int)slots_of(p.cu_q, p.total_q, p.nseq, kOwn<SPLIT>);
+    p.q_slots = (int)attn_slots(p.cu_q, p.total_q, p.nseq, kOwn<SPLIT>);
     set_each(p, kOwn<SPLIT>, 1);
     const int64_t grid = (int64_t)p.q_slots * p.H;
     const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr);
@@ -692,9 +754,10 @@ int launch_dq(AttnParams p, hipStream_t stream) {
 template <typename T, int D, bool CAP, int BIAS, int SHARE>
 int launch_dkv(AttnParams p, hipStream_t stream) {
     constexpr int OWN = kOwn<SHARE == kSplit>;
-    p.k_slots = (int)slots_of(p.cu_k, p.total_k, p.nseq, OWN);
+    p.k_slots = (int)attn_slots(p.cu_k, p.total_k, p.nseq, OWN);
     set_each(p, 1, OWN);
-    const int64_t grid = (int64_t)p.k_slots * p.Hk;
+    p.parts = SHARE == kSplit && p.dkv_part ? attn_key_parts(p.cu_k, p.total_k, p.nseq, p.Hk) : 1;
+    const int64_t grid = (int64_t)p.k_slots * p.Hk * p.parts;
     const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (SHARE == kSplit ? p.H / p.Hk : 1);
     if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dkv_kernel<T, D, CAP, BIAS, SHARE>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
@@ -702,6 +765,8 @@ int launch_dkv(AttnParams p, hipStream_t stream) {
     if (grid > 0)
         hipLaunchKernelGGL((attn_dkv_kernel<T, D, CAP, BIAS, SHARE>), dim3((unsigned)grid),
                            dim3(SHARE == kPaired ? 2 * kThreads : kThreads), lds, stream, p);
+    if (p.parts > 1)
+        hipLaunchKernelGGL((attn_parts_kernel<T, D>), dim3((unsigned)(p.k_slots * p.Hk), 2), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 template <typename T, int D, bool CAP, int BIAS>
@@ -709,8 +774,8 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
     // (a bias for every head of a group, or the sums by distance, may not fit beside a split kernel's tiles)
     const bool dq_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr) <= kSplitBiasLds;
     const bool dkv_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (p.H / p.Hk) <= kSplitBiasLds;
-    const bool dq_split = dq_fits && slots_of(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H < kSplitBelow;
-    const bool dkv_split = dkv_fits && slots_of(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
+    const bool dq_split = dq_fits && attn_slots(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H < kSplitBelow;
+    const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
     AttnParams d = p;
     d.plan_q = d.plan_k = nullptr;
     if (p.plan_q && !(dq_split && dkv_split)) {

@@ -75,37 +75,51 @@ template <typename T, int D> struct Tile {
     static __device__ __forceinline__ int swz(int row) { return 2 * ((row / RPB) & MASK); }
     static __device__ __forceinline__ int at(int row, int c) { return (row * CH + (c ^ swz(row))) * kE; }
 
-    // operand whose index is a row (lane % 32 of row0 ..), contracting over columns kK * t ..
-    static __device__ __forceinline__ typename Op<T>::Frag rows(const T* s, int row0, int t, int lane) {
-        const uint4 v = ld16(s + at(row0 + lane % 32, 2 * t + lane / 32));
-        return __builtin_bit_cast(typename Op<T>::Frag, v);
-    }
-    // operand whose index is a column (lane % 32 of col0 ..), contracting over rows row0 + kK * kk ..
-    // in the row order of an accumulator (see the top of this file)
-    static __device__ __forceinline__ typename Op<T>::Frag cols(const T* s, int row0, int kk, int col0, int lane);
-};
+    // A lane's part of the byte addresses of its operands: rows() and cols() add to it what does not depend on
+    // the lane, by one xor (the swizzle's bits and a chunk's are the same ones) and an immediate offset.
+    struct Lanes {
+        uint32_t row, col;
+        __device__ __forceinline__ explicit Lanes(int lane) {
+            const int r = lane % 32, h = lane / 32;
+            row = (uint32_t)(r * RB + (h + swz(r)) * 16);
+            if constexpr (sizeof(T) == 2) {
+                const int q = lane % 4, kr = 4 * h + (lane % 16) / 4;
+                col = (uint32_t)(kr * RB + ((2 * ((lane / 16) % 2) + q / 2) ^ swz(kr)) * 16 + (q % 2) * 8);
+            } else {
+                col = (uint32_t)(4 * h * RB + (((lane % 32) * 4) ^ (swz(4 * h) * 16)));
+            }
+        }
+        // Keeps the compiler from holding every address of a loop in a register of its own.
+        __device__ __forceinline__ void renew() { asm volatile("" : "+v"(row), "+v"(col)); }
+    };
 
-template <typename T, int D>
-__device__ __forceinline__ typename Op<T>::Frag Tile<T, D>::cols(const T* s, int row0, int kk, int col0, int lane) {
-    const int h = lane / 32;
-    if constexpr (sizeof(T) == 2) {
-        // ds_read_b64_tr_b16: a 16-lane group whose lane 4 r + q points at row r, columns 4 q .. 4 q + 3
-        // returns column i of those four rows in its lane i
-        const int r = (lane % 16) / 4, q = lane % 4;
-        const int col = col0 + 16 * ((lane / 16) % 2) + 4 * q;
-        const int row = row0 + 16 * kk + 4 * h + r;
-        const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(s + at(row, col / 8) + col % 8));
-        const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(s + at(row + 8, col / 8) + col % 8));
-        const v8i16 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        return __builtin_bit_cast(bf16x8, v);
-    } else {
-        const int col = col0 + lane % 32, row = row0 + 8 * kk + 4 * h;
-        f32x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = s[at(row + i, col / 4) + col % 4];
-        return v;
+    // operand whose index is a row (lane % 32 of row0 .., a multiple of 32), contracting over columns kK * t ..
+    static __device__ __forceinline__ typename Op<T>::Frag rows(const T* s, int row0, int t, const Lanes& z) {
+        return __builtin_bit_cast(typename Op<T>::Frag, ld16(reinterpret_cast<const char*>(s) + (z.row ^ (32u * t)) + row0 * RB));
     }
-}
+    // operand whose index is a column (lane % 32 of col0 .., a multiple of 32), contracting over rows
+    // row0 + kK * kk .. in the row order of an accumulator (see the top of this file)
+    static __device__ __forceinline__ typename Op<T>::Frag cols(const T* s, int row0, int kk, int col0, const Lanes& z) {
+        const char* at = reinterpret_cast<const char*>(s);
+        if constexpr (sizeof(T) == 2) {
+            // ds_read_b64_tr_b16: a 16-lane group whose lane 4 r + q points at row r, columns 4 q .. 4 q + 3
+            // returns column i of those four rows in its lane i
+            static_assert(sizeof(T) != 2 || RPB * (MASK + 1) <= 8, "eight rows on, the swizzle is the same");
+            at += (z.col ^ (uint32_t)(2 * col0)) + (row0 + 16 * kk) * RB;
+            const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)at);
+            const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(at + 8 * RB));
+            const v8i16 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            return __builtin_bit_cast(bf16x8, v);
+        } else {
+            // (row 4 h + i of eight: its swizzle is that of 4 h, in `col`, and of i)
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = *reinterpret_cast<const float*>(at + (z.col ^ (uint32_t)(swz(i) * 16) ^ (uint32_t)(4 * col0)) + (row0 + 8 * kk + i) * RB);
+            return v;
+        }
+    }
+};
 
 // What the kernels know a wave's outstanding memory operations by (s_waitcnt of gfx9: vmcnt in bits 3:0 and
 // 15:14, expcnt in 6:4, lgkmcnt in 11:8): everything loaded to LDS has arrived, and with kAll every LDS
@@ -242,11 +256,6 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, int own
     return sp;
 }
 
-// Slots of an axis: its whole tiles, and one more for each sequence.
-inline int64_t slots_of(const int64_t* cu, int64_t total, int64_t nseq, int own) {
-    if (nseq == 0) return 0;
-    return cu ? total / own + nseq : nseq * ((total / nseq + own - 1) / own);
-}
 // Lengths and tiles of equal sequences.
 inline void set_each(AttnParams& p, int q_own, int k_own) {
     p.each_q = p.nseq ? (int)(p.total_q / p.nseq) : 0;
@@ -284,15 +293,10 @@ template <typename T> __device__ __forceinline__ void store_rows(T* out, const f
     }
 }
 
-// Bucket of a relative position (key - query).
+// Bucket of a relative position (key - query) of at most max_distance.
 __device__ __forceinline__ int bucket_of(const AttnBuckets& b, int rel) {
-    const int d = b.both ? abs(rel) : (rel < 0 ? -rel : 0);
-    int lo = 0, hi = b.nborders;  // borders at most d
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (b.borders[mid] <= d) lo = mid + 1; else hi = mid;
-    }
-    return lo + (b.both && rel > 0 ? b.nborders + 1 : 0);
+    if (b.both) return b.of[abs(rel)] + (rel > 0 ? b.nborders + 1 : 0);
+    return b.of[rel < 0 ? -rel : 0];
 }
 
 // The head's bias, in log2 units, of relative positions -max_distance .. max_distance.

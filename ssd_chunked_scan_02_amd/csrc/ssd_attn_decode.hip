@@ -269,7 +269,7 @@ template <typename T, int D, bool CAP, int BIAS>
 int launch_decode(const DecodeParams& p, hipStream_t stream) {
     const int64_t group = p.H / p.Hk, grid = p.nseq * p.Hk * ((group + kG - 1) / kG) * p.splits;
     const size_t lds = BIAS == kBiasBuckets ? 4 * (size_t)(p.bk.total * kG + p.bk.max_distance + 1) : 0;
-    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<T, D, CAP, BIAS>),
+    if (lds > 0 && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<T, D, CAP, BIAS>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return -1;
     hipLaunchKernelGGL((attn_decode_kernel<T, D, CAP, BIAS>), dim3((unsigned)grid), dim3(kThreads), lds, stream, p);

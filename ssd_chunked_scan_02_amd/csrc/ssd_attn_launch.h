@@ -22,10 +22,22 @@ struct AttnBuckets {
     int max_distance;  // >= every border
     int nborders;      // buckets of one direction - 1
     int borders[kMaxBorders];
+    uint8_t of[kMaxDistance + 1];  // a direction's bucket by distance, to max_distance
 };
 
 // Workgroups of 128 rows below which the four waves of one split instead (kOwn in ssd_attn_common.h).
 constexpr int64_t kSplitBelow = 512;
+// Tiles of a packed axis, at most: its whole tiles, and one more for each sequence.
+inline int64_t attn_slots(const int64_t* cu, int64_t total, int64_t nseq, int own) {
+    if (nseq == 0) return 0;
+    return cu ? total / own + nseq : nseq * ((total / nseq + own - 1) / own);
+}
+// Key gradients of a small problem: parts of a tile's queries, so that the workgroups reach the 256 CUs twice.
+inline int attn_key_parts(const int64_t* cu_k, int64_t total_k, int64_t nseq, int64_t Hk) {
+    if (attn_slots(cu_k, total_k, nseq, 128) * Hk >= kSplitBelow) return 1;
+    const int64_t grid = attn_slots(cu_k, total_k, nseq, 32) * Hk, n = grid > 0 ? 512 / grid : 1;
+    return n < 1 ? 1 : n > 8 ? 8 : (int)n;
+}
 
 struct AttnParams {
     const void* q;
@@ -51,6 +63,8 @@ struct AttnParams {
     int causal;
     int q_slots, k_slots; // tiles of the packed axes (bounds: some are empty)
     int each_q, each_k, each_q_tiles, each_k_tiles;  // equal sequences: their lengths and tiles
+    int parts;            // key gradients: workgroups that share one tile's queries (1: none)
+    float* dkv_part;      // workspace [2][parts, total_k, Hk, D], or null
     int2* plan_q;         // workspace: (sequence, tile) of the slots in order of their work, or null
     int2* plan_k;
     float scale, cap;
