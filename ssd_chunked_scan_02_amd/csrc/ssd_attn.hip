@@ -3,7 +3,7 @@
 //     visible j;  y_i = sum_j p_ij v_j;  lse_i = log sum_j exp s_ij.
 //
 // One pass over the keys with a running maximum m and sum l (in log2 units): a workgroup of four waves
-// owns 128 queries of one head and document, 32 a wave, and streams 64-key tiles (32 in fp32) through
+// owns 128 query rows (of one head, or of all heads of a group) of a document, 32 a wave, and streams 64-key tiles (32 in fp32) through
 // LDS, double buffered, the next tile on its way to LDS while the present one is used.  A wave forms
 // S^T = K Q^T (queries in lanes), so m and l are one number a lane, and P^T in its accumulator layout is
 // the operand of O^T += V^T P^T (ssd_attn_common.h).  O is rescaled only when a row's maximum has grown by
@@ -38,11 +38,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     __shared__ float lut[BIAS == kBiasBuckets ? 2 * kMaxDistance + 1 : 1];
     __shared__ float stat[SPLIT ? 3 : 1][SPLIT ? kWaves * 32 : 1];  // m, l, weight of a wave's share by row
 
-    int slot, head;
-    work_item(blockIdx.x, p.q_slots, p.H, slot, head);
+    int slot, unit;
+    work_item(blockIdx.x, p.q_slots, (uint32_t)p.H / (uint32_t)p.pack, slot, unit);
     const Span sp = find_span(p, slot, OWN, false);
     if (sp.tile < 0) return;
-    const int kvh = head / (p.H / p.Hk);
+    const int head0 = unit * p.pack, kvh = (int)((uint32_t)head0 / ((uint32_t)p.H / (uint32_t)p.Hk));
     const int lane = threadIdx.x % kWave, half = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int shift = sp.lk - sp.lq;  // position of query 0 on the key axis
@@ -52,11 +52,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     // keys [0, limit(i)) are visible to query i
     auto limit = [&](int i) { return p.causal ? max(min(max(i + shift + 1, prefix), sp.lk), 0) : sp.lk; };
     const int row0 = sp.tile * OWN + (SPLIT ? 0 : wave * 32), row = row0 + lane % 32;
-    const int wg_limit = limit(min(sp.tile * OWN + OWN, sp.lq) - 1);
+    auto query_of = [&](int r) { return (int)((uint32_t)r / (uint32_t)p.pack); };
+    const int mine = query_of(min(row, sp.rows - 1)), head = head0 + min(row, sp.rows - 1) - mine * p.pack;
+    const int wg_limit = limit(query_of(min(sp.tile * OWN + OWN, sp.rows) - 1));
     const int ntiles = (wg_limit + KT - 1) / KT;
-    const int my_limit = row < sp.lq ? limit(row) : 0;
-    const int wave_most = row0 < sp.lq ? limit(min(row0 + 32, sp.lq) - 1) : 0;  // any query of the wave
-    const int wave_least = limit(row0);                                         // every query of the wave
+    const int my_limit = row < sp.rows ? limit(mine) : 0;
+    const int wave_most = row0 < sp.rows ? limit(query_of(min(row0 + 32, sp.rows) - 1)) : 0;  // any query of the wave
+    const int wave_least = limit(query_of(row0));                                             // every query of the wave
 
     const T* kg = static_cast<const T*>(p.k) + sp.k0 * p.k_stride + (int64_t)kvh * D;
     const T* vg = static_cast<const T*>(p.v) + sp.k0 * p.v_stride + (int64_t)kvh * D;
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 
     Frag qf[NT];
     {
-        const T* qg = static_cast<const T*>(p.q) + (sp.q0 + min(row, sp.lq - 1)) * p.q_stride + (int64_t)head * D;
+        const T* qg = static_cast<const T*>(p.q) + (sp.q0 + mine) * p.q_stride + (int64_t)head * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t) qf[t] = signed_frag<T>(qg + (2 * t + half) * O::kE, p.scale);
     }
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
     float m = NO_MAX ? 0.f : kNoMax, l = 0.f;  // l: this lane half's share
-    const int qpos = row + shift;
+    const int qpos = mine + shift;
 
     auto settle = [&]() {  // what was on its way to LDS is there, and (SPLIT: this wave's) reads are over
         __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
@@ -184,36 +186,38 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) stat[2][32 * w + lane] = f[w] * inv;
-            if (row < sp.lq && p.lse)
-                p.lse[(sp.q0 + row) * p.H + head] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+            if (row < sp.rows && p.lse)
+                p.lse[(sp.q0 + mine) * p.H + head] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
-            if (row0 + r >= sp.lq) break;
+            if (row0 + r >= sp.rows) break;
             const f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, stat[2]);
-            store4(static_cast<T*>(p.y) + ((sp.q0 + row0 + r) * p.H + head) * D + 4 * d4, v[0], v[1], v[2], v[3]);
+            const int q = query_of(row0 + r);
+            store4(static_cast<T*>(p.y) + ((sp.q0 + q) * p.H + head0 + row0 + r - q * p.pack) * D + 4 * d4, v[0], v[1], v[2], v[3]);
         }
         return;
     }
     // (the store exchanges words between a row's two lanes, which leave or stay together)
-    if (row >= sp.lq) return;
+    if (row >= sp.rows) return;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (an empty row is zero; a NaN stays one)
-    T* yg = static_cast<T*>(p.y) + ((sp.q0 + row) * p.H + head) * D;
+    T* yg = static_cast<T*>(p.y) + ((sp.q0 + mine) * p.H + head) * D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; r += 8) store_rows(yg + 32 * d, o[d], r, half, inv);
-    if (p.lse && half == 0) p.lse[(sp.q0 + row) * p.H + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    if (p.lse && half == 0) p.lse[(sp.q0 + mine) * p.H + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int CAPPED, int BIAS>
 int launch_fwd(AttnParams p, hipStream_t stream) {
-    const int64_t whole = attn_slots(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H;
-    const bool split = whole < kSplitBelow;
-    p.q_slots = (int)attn_slots(p.cu_q, p.total_q, p.nseq, split ? kOwn<true> : kOwn<false>);
+    p.pack = query_pack(p, BIAS);
+    const int units = p.H / p.pack;
+    const bool split = query_slots(p, kOwn<false>) * units < kSplitBelow;
+    p.q_slots = (int)query_slots(p, split ? kOwn<true> : kOwn<false>);
     set_each(p, split ? kOwn<true> : kOwn<false>, 1);
-    const int64_t grid = (int64_t)p.q_slots * p.H;
+    const int64_t grid = (int64_t)p.q_slots * units;
     if (grid == 0) return 0;
     if (split) hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAPPED, BIAS, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
     else hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAPPED, BIAS, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);

@@ -170,7 +170,7 @@ BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
     w.part = table ? align16((size_t)parts * (size_t)d->nheads * (size_t)d->num_buckets * 4) : 0;
     const int n = d->nseq > 0 ? ssd::attn_key_parts(nullptr, d->total_k - d->total_k % d->nseq, d->nseq, d->nkvheads) : 1;
     w.dkv = n > 1 ? align16((size_t)(2 * n) * (size_t)d->total_k * (size_t)d->nkvheads * (size_t)d->headdim * 4) : 0;
-    w.plan_q = align16((size_t)q_slots * 16);
+    w.plan_q = align16((size_t)(d->total_q * (d->nheads / d->nkvheads) / 128 + d->nseq + 1) * 16);
     w.plan_k = align16((size_t)k_slots * 16);
     w.total = w.delta + w.part + w.dkv + w.plan_q + w.plan_k;
     return w;

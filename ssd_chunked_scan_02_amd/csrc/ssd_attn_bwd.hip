@@ -5,7 +5,7 @@
 //     dtable[b] = sum of dS over the cells of bucket b.
 //
 // Two kernels, each owning what it sums, so that nothing is added by atomics and every run gives the
-// same bits: attn_dq_kernel owns 128 queries of a head and streams keys (S^T, dP^T, dq^T), and leaves D for
+// same bits: attn_dq_kernel owns 128 query rows and streams keys (S^T, dP^T, dq^T), and leaves D for
 // attn_dkv_kernel, which owns 128 keys of a key head and streams the queries of every head of its group
 // (S, dP, dv^T, dk^T).  That is 7 products where sharing S and dP would need 5, and no partial
 // gradients through memory.  Both keep their rows' operands and gradients in registers; the tile layout
@@ -49,7 +49,7 @@ __device__ __forceinline__ float fold_bucket(const AttnBuckets& b, const float* 
 }
 
 template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_dq_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : sizeof(T) * D >= 256 ? 2 : 3) attn_dq_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
@@ -63,17 +63,18 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     __shared__ float off_by[SPLIT ? kWaves * 32 : 1];
     extern __shared__ float extra[];
 
-    int slot, head;
-    work_item(blockIdx.x, p.q_slots, p.H, slot, head);
+    int slot, unit;
+    work_item(blockIdx.x, p.q_slots, (uint32_t)p.H / (uint32_t)p.pack, slot, unit);
     const Span sp = find_span(p, slot, OWN, false);
+    const int head0 = unit * p.pack;
     const bool grad = BIAS == kBiasBuckets && p.dtable != nullptr;
-    float* part = grad ? p.table_part + ((int64_t)sp.slot * p.H + head) * p.bk.total : nullptr;
+    float* part = grad ? p.table_part + ((int64_t)sp.slot * p.H + head0) * p.bk.total : nullptr;
     if (sp.tile < 0) {
         if (grad)
             for (int i = threadIdx.x; i < p.bk.total; i += kThreads) part[i] = 0.f;
         return;
     }
-    const int kvh = head / (p.H / p.Hk);
+    const int kvh = (int)((uint32_t)head0 / ((uint32_t)p.H / (uint32_t)p.Hk));
     const int lane = threadIdx.x % kWave, half = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int shift = sp.lk - sp.lq;
@@ -81,11 +82,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
     auto limit = [&](int i) { return p.causal ? max(min(max(i + shift + 1, prefix), sp.lk), 0) : sp.lk; };
     const int row0 = sp.tile * OWN + (SPLIT ? 0 : wave * 32), row = row0 + lane % 32;
-    const int wg_limit = limit(min(sp.tile * OWN + OWN, sp.lq) - 1);
+    auto query_of = [&](int r) { return (int)((uint32_t)r / (uint32_t)p.pack); };
+    const int query = query_of(min(row, sp.rows - 1)), head = head0 + min(row, sp.rows - 1) - query * p.pack;
+    const int wg_limit = limit(query_of(min(sp.tile * OWN + OWN, sp.rows) - 1));
     const int ntiles = (wg_limit + KT - 1) / KT;
-    const int my_limit = row < sp.lq ? limit(row) : 0;
-    const int wave_most = row0 < sp.lq ? limit(min(row0 + 32, sp.lq) - 1) : 0;
-    const int wave_least = limit(row0);
+    const int my_limit = row < sp.rows ? limit(query) : 0;
+    const int wave_most = row0 < sp.rows ? limit(query_of(min(row0 + 32, sp.rows) - 1)) : 0;
+    const int wave_least = limit(query_of(row0));
 
     const T* kg = static_cast<const T*>(p.k) + sp.k0 * p.k_stride + (int64_t)kvh * D;
     const T* vg = static_cast<const T*>(p.v) + sp.k0 * p.v_stride + (int64_t)kvh * D;
@@ -101,11 +104,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     const int t0 = SPLIT ? wave : 0, dt = SPLIT ? kWaves : 1;
     if (t0 < ntiles) fetch(ka, va, t0);
 
-    const int64_t mine = (sp.q0 + min(row, sp.lq - 1)) * p.H + head;  // this lane's (query, head)
+    const int64_t mine = (sp.q0 + query) * p.H + head;  // this lane's (query, head)
     Frag qf[NT], gf[NT];
     float delta = 0.f;
     {
-        const T* qg = static_cast<const T*>(p.q) + (sp.q0 + min(row, sp.lq - 1)) * p.q_stride + (int64_t)head * D;
+        const T* qg = static_cast<const T*>(p.q) + (sp.q0 + query) * p.q_stride + (int64_t)head * D;
         const T* gg = static_cast<const T*>(p.dy) + mine * D;
         const T* yg = static_cast<const T*>(p.y) + mine * D;
 #pragma unroll
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     delta += other_half(delta);
     float lse2 = p.lse[mine] * kLog2e;
     // a row that sees nothing, and the tile's rows past the last query: all their weights are zero
-    if (lse2 == -INFINITY || row >= sp.lq) lse2 = INFINITY;
+    if (lse2 == -INFINITY || row >= sp.rows) lse2 = INFINITY;
 
     Score sc;
     sc.init<T>(p.scale, p.cap, CAP, !CAP && BIAS == kBiasNone);
@@ -133,13 +136,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     float* block = extra + (1 + kWaves) * reach + wave * kDiagBlock;            // dS [key][query]
     float* far = extra + (1 + kWaves) * reach + kWaves * kDiagBlock;            // [2][kWaves]
     if constexpr (BIAS == kBiasBuckets) {
-        fill_bias(lut, p, head);
+        fill_bias(lut, p, head0);
         if (grad)
             for (int i = lane; i < reach; i += kWave) sums[i] = 0.f;
     }
     // far cells' dS and p, below (first) and above the reach, and the row's sum of dS
     float far_ds[2] = {0.f, 0.f}, far_p[2] = {0.f, 0.f}, row_ds = 0.f;
-    const int qpos = row + shift;
+    const int qpos = query + shift;
 
     f32x16 acc[DT];
 #pragma unroll
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     // are nearer than the table's reach
     typename L::Lanes z(lane);
     auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope) {
-        if constexpr (sizeof(T) * D >= 256) z.renew();
+        z.renew();
         f32x16 x[1] = {f32x16{}}, dp;
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] = -delta;  // the accumulator starts at -D: dP - D at no cost
@@ -184,9 +187,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         const int k0 = t * KT;
         if (DOUBLE && t + dt < ntiles) fetch(kn_, vn_, t + dt);
         if (k0 < wave_most) {
-            // (64-wide heads: both halves of a tile at once; 128-wide: one after the other, in the registers of two
-            // waves a SIMD)
-#pragma unroll sizeof(T) * D >= 256 ? 1 : NS
+            // (one half of a tile after the other: both at once take the registers of one more wave a SIMD, which is
+            // worth more: 282 -> 263 us at 8 x 2048 tokens, 24 heads of 64, capped; 332 -> 282 us on packed 128-wide heads)
+#pragma unroll 1
             for (int n = 0; n < NS; ++n) {
                 const int kn = k0 + 32 * n;
                 f32x16 s, ds, slope;
@@ -237,9 +240,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         __syncthreads();
         for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
-            if (row0 + r >= sp.lq) break;
+            if (row0 + r >= sp.rows) break;
             const f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, nullptr) * p.scale;
-            store4(static_cast<T*>(p.dq) + ((sp.q0 + row0 + r) * p.H + head) * D + 4 * d4, v[0], v[1], v[2], v[3]);
+            const int q = query_of(row0 + r);
+            store4(static_cast<T*>(p.dq) + ((sp.q0 + q) * p.H + head0 + row0 + r - q * p.pack) * D + 4 * d4, v[0], v[1], v[2], v[3]);
         }
         row_ds = 0.f;
 #pragma unroll
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         __syncthreads();  // (the tiles are free again)
     } else {
         row_ds += other_half(row_ds);
-        if (row < sp.lq) {
+        if (row < sp.rows) {
             T* out = static_cast<T*>(p.dq) + mine * D;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         }
     }
     if (grad) delta += row_ds;
-    if (row < sp.lq && half == 0 && (!SPLIT || wave == 0)) p.delta[mine] = delta;
+    if (row < sp.rows && half == 0 && (!SPLIT || wave == 0)) p.delta[mine] = delta;
     if constexpr (BIAS == kBiasBuckets) {
         if (!grad) return;
         float far_lo = far_ds[0] - row_ds * far_p[0], far_hi = far_ds[1] - row_ds * far_p[1];
@@ -365,7 +369,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, i
     const int64_t* cu = keys ? p.cu_k : p.cu_q;
     int2* plan = keys ? p.plan_k : p.plan_q;
     const int tq = (int)p.total_q, tk = (int)p.total_k, total = keys ? tk : tq, nseq = (int)p.nseq;
-    const int slots = total / own + nseq;
+    const int pack = keys ? 1 : p.pack;
+    const int slots = (int)((int64_t)total * pack / own) + nseq;
+    auto start = [&](int s) { return (int)((int64_t)offset_at(cu, s, total) * pack / own) + s; };
     int2* raw = plan + slots;  // (sequence, tile) by slot
     for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
     __syncthreads();
@@ -375,22 +381,22 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, i
         const int prefix = p.prefix ? (int)clamp64(p.prefix[s], 0, lk) : 0;
         int rows;
         if (keys) rows = lq - (!p.causal || tile * own < prefix ? 0 : max(tile * own - shift, 0));
-        else rows = p.causal ? max(min(max(min(tile * own + own, lq) + shift, prefix), lk), 0) : lk;
+        else rows = p.causal ? max(min(max(min((tile * own + own - 1) / pack + 1, lq) + shift, prefix), lk), 0) : lk;
         return kPlanBins - 1 - min(max((rows + 63) / 64, 0) + 1, kPlanBins - 1);
     };
     for (int slot = threadIdx.x; slot < slots; slot += kPlanThreads) {
         int lo = 0, n = nseq;  // the last sequence that starts at this slot or before
         while (n > 1) {
             const int mid = n / 2;
-            if (offset_at(cu, lo + mid, total) / own + lo + mid <= slot) {
+            if (start(lo + mid) <= slot) {
                 lo += mid;
                 n -= mid;
             } else {
                 n = mid;
             }
         }
-        int tile = slot - (offset_at(cu, lo, total) / own + lo);
-        const int len = offset_at(cu, lo + 1, total) - offset_at(cu, lo, total);
+        int tile = slot - start(lo);
+        const int64_t len = (int64_t)(offset_at(cu, lo + 1, total) - offset_at(cu, lo, total)) * pack;
         if (tile < 0 || (int64_t)tile * own >= len) tile = -1;
         raw[slot] = int2{tile < 0 ? slot : lo, tile};
         atomicAdd(&bins[tile < 0 ? kPlanBins - 1 : bin_of(lo, tile)], 1);
@@ -740,9 +746,9 @@ constexpr size_t kSplitBiasLds = 163840 - 139264;
 
 template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
 int launch_dq(AttnParams p, hipStream_t stream) {
-    p.q_slots = (int)attn_slots(p.cu_q, p.total_q, p.nseq, kOwn<SPLIT>);
+    p.q_slots = (int)query_slots(p, kOwn<SPLIT>);
     set_each(p, kOwn<SPLIT>, 1);
-    const int64_t grid = (int64_t)p.q_slots * p.H;
+    const int64_t grid = (int64_t)p.q_slots * (p.H / p.pack);
     const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr);
     if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dq_kernel<T, D, CAP, BIAS, SPLIT>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
@@ -774,13 +780,16 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
     // (a bias for every head of a group, or the sums by distance, may not fit beside a split kernel's tiles)
     const bool dq_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr) <= kSplitBiasLds;
     const bool dkv_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (p.H / p.Hk) <= kSplitBiasLds;
-    const bool dq_split = dq_fits && attn_slots(p.cu_q, p.total_q, p.nseq, kOwn<false>) * p.H < kSplitBelow;
-    const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
     AttnParams d = p;
+    d.pack = query_pack(p, BIAS);
+    const bool dq_split = dq_fits && query_slots(d, kOwn<false>) * (d.H / d.pack) < kSplitBelow;
+    const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
     d.plan_q = d.plan_k = nullptr;
+    AttnParams with_plan = p;
+    with_plan.pack = d.pack;
     if (p.plan_q && !(dq_split && dkv_split)) {
         // sequences of different lengths, and more than a round of workgroups: the longest first
-        hipLaunchKernelGGL(attn_plan_kernel, dim3(2), dim3(kPlanThreads), 0, stream, p, dq_split ? 0 : kOwn<false>, dkv_split ? 0 : kOwn<false>);
+        hipLaunchKernelGGL(attn_plan_kernel, dim3(2), dim3(kPlanThreads), 0, stream, with_plan, dq_split ? 0 : kOwn<false>, dkv_split ? 0 : kOwn<false>);
         if (!dq_split) d.plan_q = p.plan_q;
         if (!dkv_split) d.plan_k = p.plan_k;
     }

@@ -25,6 +25,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // start of a running maximum (log2 units): below any finite score, and finite, so that a row that
 // has seen nothing but masked scores (minus infinity) takes exp2(-inf) = 0 and not a NaN
 constexpr float kNoMax = -1e30f;
+// Rows of the query axis.  The heads of a group meet the same keys, so that a tile may hold all of them:
+// row R is query R / pack, head R % pack of the group (pack 1: a tile is of one head).  Keys and values
+// are then read once for the group, and tiles are of fewer queries, which wastes less on short documents
+// and on the diagonal.
+//
 // Rows of a workgroup's own tile.  With enough work for the chip each of its four waves owns 32 rows and they
 // share what they stream.  With too little (SPLIT) all four own the same 32 rows, each streams every
 // fourth tile through LDS of its own, and their results are joined at the end: four times the
@@ -177,6 +182,7 @@ __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 
 struct Span {
     int64_t q0, k0;  // first query and key row
     int lq, lk;      // their numbers
+    int rows;        // query rows: lq * pack
     int tile;        // tile of the axis the slots count; negative: the slot is empty
     int seq;
     int slot;        // place of the tile in the axis's own order
@@ -210,7 +216,7 @@ template <typename F> __device__ __forceinline__ int last_at_most(int nseq, F le
 __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, int own, bool by_keys) {
     const int64_t* cu = by_keys ? p.cu_k : p.cu_q;
     const int2* plan = by_keys ? p.plan_k : p.plan_q;
-    const int tq = (int)p.total_q, tk = (int)p.total_k;
+    const int tq = (int)p.total_q, tk = (int)p.total_k, pack = by_keys ? 1 : p.pack;
     Span sp{};
     int s, tile;
     sp.slot = slot;
@@ -223,15 +229,16 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, int own
             sp.tile = -1;
             return sp;
         }
-        sp.slot = offset_at(cu, s, by_keys ? tk : tq) / own + s + tile;
+        sp.slot = (int)((int64_t)offset_at(cu, s, by_keys ? tk : tq) * pack / own) + s + tile;
     } else if (!cu) {
         const int per = by_keys ? p.each_k_tiles : p.each_q_tiles;
         s = (int)((uint32_t)slot / (uint32_t)per);
         tile = slot - s * per;
     } else {
         const int total = by_keys ? tk : tq;
-        s = last_at_most((int)p.nseq, [&](int i) { return offset_at(cu, i, total) / own + i <= slot; });
-        tile = slot - (offset_at(cu, s, total) / own + s);
+        auto start = [&](int i) { return (int)((int64_t)offset_at(cu, i, total) * pack / own) + i; };
+        s = last_at_most((int)p.nseq, [&](int i) { return start(i) <= slot; });
+        tile = slot - start(s);
     }
     sp.seq = s;
     int q0, k0;
@@ -251,16 +258,27 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int slot, int own
     }
     sp.q0 = q0;
     sp.k0 = k0;
-    const int len = by_keys ? sp.lk : sp.lq;
+    sp.rows = sp.lq * pack;
+    const int len = by_keys ? sp.lk : sp.rows;
     sp.tile = tile >= 0 && (int64_t)tile * own < len ? tile : -1;
     return sp;
 }
 
+// Heads in a query tile: a group's, except with a bucket table, whose bias in LDS and sums by distance are
+// of one head (and rows are counted in 32 bits).
+inline int query_pack(const AttnParams& p, int bias) {
+    const int group = p.H / p.Hk;
+    return bias == kBiasBuckets || p.total_q * group >= ((int64_t)1 << 31) - 1024 ? 1 : group;
+}
+inline int64_t query_slots(const AttnParams& p, int own) {
+    // (equal sequences: their rows have to be counted one by one)
+    return attn_slots(p.cu_q, p.total_q * p.pack, p.nseq, own);
+}
 // Lengths and tiles of equal sequences.
 inline void set_each(AttnParams& p, int q_own, int k_own) {
     p.each_q = p.nseq ? (int)(p.total_q / p.nseq) : 0;
     p.each_k = p.nseq ? (int)(p.total_k / p.nseq) : 0;
-    p.each_q_tiles = (p.each_q + q_own - 1) / q_own;
+    p.each_q_tiles = (int)(((int64_t)p.each_q * p.pack + q_own - 1) / q_own);
     p.each_k_tiles = (p.each_k + k_own - 1) / k_own;
 }
 

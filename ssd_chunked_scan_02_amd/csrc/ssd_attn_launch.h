@@ -61,6 +61,7 @@ struct AttnParams {
     int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
     int H, Hk;
     int causal;
+    int pack;             // query heads of a group that share the rows of a query tile (see Rows), or 1
     int q_slots, k_slots; // tiles of the packed axes (bounds: some are empty)
     int each_q, each_k, each_q_tiles, each_k_tiles;  // equal sequences: their lengths and tiles
     int parts;            // key gradients: workgroups that share one tile's queries (1: none)
