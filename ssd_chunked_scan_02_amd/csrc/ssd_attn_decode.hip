@@ -43,8 +43,8 @@ __device__ __forceinline__ int page_of(const DecodeParams& p, int64_t s, int key
     return page >= 0 && page < p.num_pages ? page : -1;
 }
 
-template <typename T, int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p) {
+template <typename T, int D, bool CAP, int BIAS, int NW>
+__global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) attn_decode_kernel(DecodeParams p) {
     using O = Op16<T>;
     using Frag = typename O::Frag;
     constexpr int E = O::kE, NT = D / O::kK, DT = D / 16, CH = D / E;
@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
     constexpr int VS = D + E;                 // LDS row stride of V
     constexpr int kTile = kBlock * VS * (int)sizeof(T);
     constexpr int kJoin = kG * D * 4;         // a wave's O for the join, in the same memory
-    __shared__ __attribute__((aligned(16))) char vmem[kWaves][kTile > kJoin ? kTile : kJoin];
-    __shared__ float stat[kWaves][2][kG];
+    __shared__ __attribute__((aligned(16))) char vmem[NW][kTile > kJoin ? kTile : kJoin];
+    __shared__ float stat[NW][2][kG];
     extern __shared__ float extra[];          // buckets: [total][kG] bias, then bucket by distance
 
     const int group = p.H / p.Hk, tiles = (group + kG - 1) / kG;
@@ -82,9 +82,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
     const int* bucket = reinterpret_cast<const int*>(extra + p.bk.total * kG);
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     if constexpr (BIAS == kBiasBuckets) {
-        for (int i = threadIdx.x; i < p.bk.total * kG; i += kThreads)
+        for (int i = threadIdx.x; i < p.bk.total * kG; i += NW * kWave)
             extra[i] = p.table[(int64_t)(i / kG) * p.H + head0 + min(i % kG, heads - 1)] * kLog2e;
-        for (int i = threadIdx.x; i <= md; i += kThreads) reinterpret_cast<int*>(extra + p.bk.total * kG)[i] = bucket_of(p.bk, -i) * kG;
+        for (int i = threadIdx.x; i <= md; i += NW * kWave) reinterpret_cast<int*>(extra + p.bk.total * kG)[i] = bucket_of(p.bk, -i) * kG;
         __syncthreads();
         far = bias[bucket[md] + col];
     }
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
     };
     int b = b0 + wave;
     if (b < b1) fetch(b);
-    for (; b < b1; b += kWaves) {
+    for (; b < b1; b += NW) {
         Frag kf[2][NT];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
 #pragma unroll
             for (int t = 0; t < NT; ++t) sv[n] = O::mma(kf[n][t], qf[t], sv[n]);
         }
-        if (b + kWaves < b1) fetch(b + kWaves);
+        if (b + NW < b1) fetch(b + NW);
         // register r of tile n: key b * 32 + 16 n + 4 g + r of query head `col`
         const int key0 = b * kBlock + 4 * g;
         const bool all_far = len - 1 - (b * kBlock + kBlock - 1) >= md;
@@ -217,15 +217,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeParams p
 #pragma unroll
     for (int d = 0; d < DT; ++d) st16(mine + 16 * d, __builtin_bit_cast(uint4, o[d]));
     __syncthreads();
-    for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < heads * (D / 4); i += NW * kWave) {
         const int c = i / (D / 4), d = 4 * (i % (D / 4));
         float top = stat[0][0][c];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stat[w][0][c]);
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, stat[w][0][c]);
         float sum = 0.f;
         f32x4 v{};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float f = exp2_hw(stat[w][0][c] - top);
             sum += f * stat[w][1][c];
             v += f * *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(vmem[w]) + c * D + d);
@@ -265,14 +265,14 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(DecodeParams p, int
     store4(static_cast<T*>(p.y) + at * D + d, v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
 }
 
-template <typename T, int D, bool CAP, int BIAS>
+template <typename T, int D, bool CAP, int BIAS, int NW>
 int launch_decode(const DecodeParams& p, hipStream_t stream) {
     const int64_t group = p.H / p.Hk, grid = p.nseq * p.Hk * ((group + kG - 1) / kG) * p.splits;
     const size_t lds = BIAS == kBiasBuckets ? 4 * (size_t)(p.bk.total * kG + p.bk.max_distance + 1) : 0;
-    if (lds > 0 && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<T, D, CAP, BIAS>),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+    if (lds > 0 && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_decode_kernel<T, D, CAP, BIAS, NW>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return -1;
-    hipLaunchKernelGGL((attn_decode_kernel<T, D, CAP, BIAS>), dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
+    hipLaunchKernelGGL((attn_decode_kernel<T, D, CAP, BIAS, NW>), dim3((unsigned)grid), dim3(NW * kWave), lds, stream, p);
     if (hipGetLastError() != hipSuccess) return -1;
     if (p.splits > 1) {
         const int64_t units = p.nseq * p.H;
@@ -281,6 +281,10 @@ int launch_decode(const DecodeParams& p, hipStream_t stream) {
         if (hipGetLastError() != hipSuccess) return -1;
     }
     return 0;
+}
+template <typename T, int D, bool CAP, int BIAS>
+int launch_decode(const DecodeParams& p, hipStream_t stream) {
+    return p.wide ? launch_decode<T, D, CAP, BIAS, 2 * kWaves>(p, stream) : launch_decode<T, D, CAP, BIAS, kWaves>(p, stream);
 }
 template <typename T, int D, bool CAP>
 int launch_decode(const DecodeParams& p, int bias, hipStream_t stream) {

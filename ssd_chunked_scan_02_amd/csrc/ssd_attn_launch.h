@@ -86,6 +86,7 @@ struct DecodeParams {
     float* part_ml;           // workspace [nseq, H, splits, 2]
     int64_t nseq, q_stride;
     int H, Hk, num_pages, page_size, max_pages, splits;
+    int wide;                 // 1: eight waves a workgroup instead of four
     float scale, cap;
     AttnBuckets bk;
 };

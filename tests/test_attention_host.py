@@ -1,0 +1,220 @@
+"""The attention layer's C ABI and binding on a machine without a GPU: every declared function is exported,
+workspaces are sized and bad arguments refused before any HIP call; and the fp64 model's own pins."""
+import ctypes
+import math
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.attention as oa
+import ssd_chunked_scan_02_amd as ssd
+from ssd_chunked_scan_02_amd.attention import AttnCache, AttnDims
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "ssd_attn.h")
+OK, INVALID, UNSUPPORTED, ALIGN = 0, -1, -2, -3
+P = 1 << 20  # an aligned address that no refused call follows
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ssd.library_path()):
+        from ssd_chunked_scan_02_amd.build import build
+        build()
+    return ssd.load_library()
+
+
+def test_header_and_exports(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(ssd_[a-z_]+)\s*\(", text)))
+    assert names == ["ssd_attn_backward", "ssd_attn_backward_workspace_bytes", "ssd_attn_decode",
+                     "ssd_attn_decode_workspace_bytes", "ssd_attn_forward", "ssd_kv_append"]
+    for n in names:
+        assert hasattr(lib, n) and hasattr(ssd, n) and n in ssd.__all__
+
+
+def _dims(**kw):
+    d = dict(nseq=2, total_q=100, total_k=100, nheads=4, nkvheads=2, headdim=64, q_stride=0, k_stride=0, v_stride=0, scale=0.125,
+             softcap=0.0, dtype=1, causal=1, num_buckets=32, max_distance=128, bidirectional=0)
+    d.update(kw)
+    return AttnDims(**d)
+
+
+def _forward(lib, dims, cu_q=None, cu_k=None, prefix=None, q=P, k=P, v=P, slopes=None, table=None, y=P, lse=P):
+    return lib.ssd_attn_forward(ctypes.byref(dims) if dims else None, cu_q, cu_k, prefix, q, k, v, slopes, table, y, lse, None)
+
+
+# (no case here may reach a launch: each is refused, or has nothing to do)
+FORWARD = [
+    (None, {}, INVALID),
+    (dict(nseq=-1), {}, INVALID), (dict(nseq=0), {}, OK), (dict(total_q=0, total_k=0), dict(cu_q=P), OK),
+    (dict(total_q=-1), {}, INVALID), (dict(total_k=1 << 31), dict(cu_q=P, cu_k=P), INVALID),
+    (dict(nheads=0), {}, INVALID), (dict(nheads=3), {}, INVALID), (dict(nkvheads=0), {}, INVALID),
+    (dict(nheads=1 << 17, nkvheads=1), {}, INVALID),
+    (dict(headdim=16), {}, UNSUPPORTED), (dict(headdim=96), {}, UNSUPPORTED), (dict(headdim=0), {}, INVALID),
+    (dict(dtype=2), {}, INVALID), (dict(causal=2), {}, INVALID),
+    (dict(scale=math.nan), {}, INVALID), (dict(scale=math.inf), {}, INVALID),
+    (dict(softcap=-1.0), {}, INVALID), (dict(softcap=math.inf), {}, INVALID),
+    (dict(total_q=101), {}, INVALID),                                       # not two equal sequences
+    ({}, dict(cu_k=P), INVALID),                                            # key offsets without query offsets
+    (dict(total_k=90), dict(cu_q=P), INVALID),                              # one set of offsets for two axes
+    (dict(causal=0), dict(prefix=P), INVALID), ({}, dict(slopes=P, table=P), INVALID),
+    ({}, dict(q=None), INVALID), ({}, dict(k=None), INVALID), ({}, dict(v=None), INVALID), ({}, dict(y=None), INVALID),
+    ({}, dict(q=P + 8), ALIGN), ({}, dict(k=P + 2), ALIGN), ({}, dict(v=P + 4), ALIGN), ({}, dict(y=P + 8), ALIGN),
+    ({}, dict(lse=P + 4), ALIGN), ({}, dict(slopes=P + 4), ALIGN), ({}, dict(cu_q=P + 4), ALIGN), ({}, dict(prefix=P + 4), ALIGN),
+    (dict(q_stride=255), {}, INVALID), (dict(q_stride=260), {}, ALIGN), (dict(k_stride=127), {}, INVALID),
+    (dict(v_stride=1 << 24), {}, INVALID), (dict(nseq=0, nheads=1 << 16, nkvheads=1 << 16, headdim=128), {}, OK),
+    (dict(num_buckets=1), dict(table=P), INVALID), (dict(num_buckets=65), dict(table=P), INVALID),
+    (dict(num_buckets=33, bidirectional=1), dict(table=P), INVALID), (dict(num_buckets=2, bidirectional=1), dict(table=P), INVALID),
+    (dict(num_buckets=130, bidirectional=1), dict(table=P), INVALID), (dict(max_distance=16), dict(table=P), INVALID),
+    (dict(max_distance=1025), dict(table=P), UNSUPPORTED), (dict(bidirectional=2), dict(table=P), INVALID),
+    (dict(nheads=1 << 16, nkvheads=1, headdim=32, total_q=1 << 28, total_k=1 << 28), dict(cu_q=P), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("dims,args,want", FORWARD, ids=range(len(FORWARD)))
+def test_forward_refusals(lib, dims, args, want):
+    assert _forward(lib, None if dims is None else _dims(**dims), **args) == want
+
+
+def test_backward_refusals_and_workspace(lib):
+    dims = _dims()
+    need = ssd.ssd_attn_backward_workspace_bytes(dims)
+    # D per (query, head), two lists of (sequence, tile) pairs for each axis, and the key gradients' parts in fp32: two
+    # sequences of 50 keys are four tiles of 32 for each of two key heads, so eight parts
+    assert need == 100 * 4 * 4 + (100 * 2 // 128 + 3) * 16 + (100 // 128 + 3) * 16 + 2 * 8 * 100 * 2 * 64 * 4
+    table = ssd.ssd_attn_backward_workspace_bytes(dims, True)
+    assert table == need + (100 // 32 + 3) * 4 * 32 * 4
+    assert ssd.ssd_attn_backward_workspace_bytes(_dims(headdim=48)) == 0
+    assert ssd.ssd_attn_backward_workspace_bytes(_dims(nseq=0)) == 0
+
+    def call(d=dims, tab=None, y=P, lse=P, dy=P, dq=P, dk=P, dv=P, dtable=None, ws=P, n=table, **kw):
+        return lib.ssd_attn_backward(ctypes.byref(d), None, None, None, P, P, P, None, tab, y, lse, dy, dq, dk, dv, dtable, ws, n, None)
+
+    for name in ("y", "lse", "dy", "dq", "dk", "dv", "ws"):
+        assert call(**{name: None}) == INVALID, name
+        assert call(**{name: P + 8}) == ALIGN, name
+    assert call(n=need - 1) == INVALID
+    assert call(dtable=P) == INVALID                      # no table
+    assert call(tab=P, dtable=P, n=table - 1) == INVALID
+    assert call(d=_dims(nseq=0), ws=None, n=0) == OK
+    assert call(d=_dims(headdim=40)) == UNSUPPORTED
+
+
+def _cache(**kw):
+    d = dict(nseq=3, nheads=8, nkvheads=2, headdim=64, num_pages=10, page_size=16, max_pages=4, q_stride=0, k_stride=0, v_stride=0,
+             scale=0.125, softcap=0.0, dtype=1, num_buckets=32, max_distance=128, bidirectional=0)
+    d.update(kw)
+    return AttnCache(**d)
+
+
+CACHE = [(dict(page_size=8), UNSUPPORTED), (dict(page_size=24), UNSUPPORTED), (dict(page_size=0), INVALID),
+         (dict(page_size=1 << 17), UNSUPPORTED), (dict(num_pages=-1), INVALID), (dict(num_pages=1 << 31), INVALID),
+         (dict(max_pages=-1), INVALID), (dict(max_pages=1 << 28), UNSUPPORTED), (dict(headdim=256), UNSUPPORTED),
+         (dict(nheads=7), INVALID), (dict(dtype=3), INVALID), (dict(nseq=-1), INVALID), (dict(q_stride=100), INVALID)]
+
+
+@pytest.mark.parametrize("change,want", CACHE, ids=range(len(CACHE)))
+def test_cache_refusals(lib, change, want):
+    c = _cache(**change)
+    assert lib.ssd_attn_decode(ctypes.byref(c), P, P, P, P, P, None, None, P, P, 1 << 30, None) == want
+    assert lib.ssd_kv_append(ctypes.byref(c), c.nseq, None, P, P, P, P, P, None, 0, 0, P, P, P, None) == want
+
+
+def test_decode_refusals_and_workspace(lib):
+    c = _cache()
+    # 3 sequences x 2 key heads: 1024 / 6 splits asked for, but 64 keys are no more than one of 128
+    assert ssd.ssd_attn_decode_workspace_bytes(c) == 0
+    long = _cache(max_pages=1000)
+    n = 64
+    assert ssd.ssd_attn_decode_workspace_bytes(long) == 3 * 8 * n * (64 * 4 + 8)
+    assert ssd.ssd_attn_decode_workspace_bytes(_cache(page_size=4)) == 0
+
+    def call(d=c, q=P, k=P, v=P, bt=P, sl=P, slopes=None, table=None, y=P, ws=P, n=1 << 30):
+        return lib.ssd_attn_decode(ctypes.byref(d), q, k, v, bt, sl, slopes, table, y, ws, n, None)
+
+    for name in ("q", "k", "v", "bt", "sl", "y"):
+        assert call(**{name: None}) == INVALID, name
+    for name in ("q", "k", "v", "y", "ws", "slopes", "table"):
+        assert call(**{name: P + 4}) == ALIGN, name
+    assert call(bt=P + 2) == ALIGN and call(sl=P + 4) == ALIGN
+    assert call(slopes=P, table=P) == INVALID
+    assert call(d=long, n=3 * 8 * n * (64 * 4 + 8) - 1) == INVALID
+    assert call(d=_cache(softcap=-2.0)) == INVALID
+    assert call(d=_cache(nseq=0), q=None, y=None) == OK
+
+
+def test_append_refusals(lib):
+    def call(d=_cache(), tokens=3, cu=None, sl=P, bt=P, k=P, v=P, q=P, inv=None, rot=0, inter=0, kc=P, vc=P, qo=P):
+        return lib.ssd_kv_append(ctypes.byref(d), tokens, cu, sl, bt, k, v, q, inv, rot, inter, kc, vc, qo, None)
+
+    assert call(tokens=4) == INVALID                       # one token per sequence
+    assert call(tokens=-1, cu=P) == INVALID
+    for name in ("sl", "bt", "k", "v", "kc", "vc"):
+        assert call(**{name: None}) == INVALID, name
+    assert call(q=None) == INVALID and call(qo=None) == INVALID
+    for name in ("k", "v", "q", "kc", "vc", "qo", "inv"):
+        assert call(**{name: P + 8}) == ALIGN, name
+    assert call(cu=P + 4) == ALIGN
+    assert call(rot=8) == INVALID                          # no frequencies
+    assert call(inv=P, rot=40) == INVALID and call(inv=P, rot=12) == UNSUPPORTED and call(inv=P, rot=-8) == INVALID
+    assert call(inter=2) == INVALID
+    assert call(tokens=0, cu=P) == OK and call(d=_cache(nseq=0), tokens=0) == OK
+
+
+def test_binding_refuses_cpu_tensors_and_bad_shapes():
+    q = torch.zeros(2, 10, 4, 64)
+    with pytest.raises(ValueError):
+        ssd.ssd_attn_forward(q, q, q)
+    with pytest.raises(TypeError):
+        ssd.ssd_attn_forward(q.half(), q.half(), q.half())
+    with pytest.raises(ValueError):
+        ssd.ssd_attn_forward(q[0], q[0], q[0])             # three dimensions need offsets
+    with pytest.raises(ValueError):
+        ssd.ssd_kv_append(q[0], q[0], q, q, torch.zeros(10, 2, dtype=torch.int32), torch.zeros(10, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        ssd.ssd_attn_decode(q[0], q, q, torch.zeros(10, 2, dtype=torch.int32), torch.zeros(10, dtype=torch.int64))
+
+
+def test_model_buckets_against_known_borders():
+    """32 buckets to distance 128: exact to 15, then 16 2^(3 k / 16) rounded up; both directions halve the
+    table, and the borders 8 2^(k / 2) with k even are whole numbers, each its bucket's first distance."""
+    one = [oa.bucket(-d, 32, 128, False) for d in range(200)]
+    assert one[:17] == list(range(17)) and one[127] == 31 and one[128] == 31 and oa.bucket(5, 32, 128, False) == 0
+    for k in range(16):
+        assert one.index(16 + k) == math.ceil(16 * 2 ** (3 * k / 16) - 1e-9)
+    two = [oa.bucket(d, 32, 128, True) - 16 for d in range(1, 200)]
+    assert [two.index(8 + k) + 1 for k in (0, 2, 4, 6)] == [8, 16, 32, 64]
+    assert oa.bucket(0, 32, 128, True) == 0 and oa.bucket(-64, 32, 128, True) == 14 and oa.bucket(63, 32, 128, True) == 16 + 13
+
+
+def test_model_gradients_against_differences():
+    rng = np.random.RandomState(1)
+    q, k, v, dy = rng.randn(40, 2, 8), rng.randn(40, 1, 8), rng.randn(40, 1, 8), rng.randn(40, 2, 8)
+    table = rng.randn(8, 2)
+    how = dict(cu=[0, 15, 40], cap=2.0, max_distance=20, prefix=[4, 0])
+    got = oa.attention(q, k, v, table=table, dy=dy, **how)
+    for n, x in (("q", q), ("k", k), ("v", v), ("table", table)):
+        way = rng.randn(*x.shape)
+
+        def loss(e):
+            a = dict(q=q, k=k, v=v, table=table)
+            a[n] = x + e * way
+            return (oa.attention(**a, **how)["y"] * dy).sum()
+
+        want = (loss(1e-5) - loss(-1e-5)) / 2e-5
+        assert abs((got["d" + n] * way).sum() - want) < 1e-6 * (1 + abs(want)), n
+
+
+def test_model_against_a_direct_softmax():
+    rng = np.random.RandomState(2)
+    q, k, v = rng.randn(9, 1, 4), rng.randn(9, 1, 4), rng.randn(9, 1, 4)
+    s = q[:, 0] @ k[:, 0].T / 2 - 0.25 * np.abs(np.arange(9)[:, None] - np.arange(9)[None])
+    s[np.triu_indices(9, 1)] = -np.inf
+    p = np.exp(s) / np.exp(s).sum(1, keepdims=True)
+    got = oa.attention(q, k, v, nseq=1, slopes=np.array([0.25]))
+    assert np.allclose(got["y"][:, 0], p @ v[:, 0], rtol=0, atol=1e-14)
+    assert np.allclose(got["lse"][:, 0], np.log(np.exp(s).sum(1)), rtol=0, atol=1e-14)
