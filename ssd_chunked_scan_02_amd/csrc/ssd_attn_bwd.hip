@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     if (lse2 == -INFINITY || row >= sp.rows) lse2 = INFINITY;
 
     Score sc;
-    sc.init<T>(p.scale, p.cap, CAP, !CAP && BIAS == kBiasNone);
+    sc.init<T>(p.scale, p.cap, CAP, BIAS == kBiasNone);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
     const int md = p.bk.max_distance, reach = 2 * md + 1;
@@ -166,8 +166,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, z), gf[i], dp);
         if constexpr (CAP) {
             sc.template capped<T>(x);
+            if constexpr (BIAS != kBiasNone) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) slope[r] = sc.slope(x[0][r]);
+                for (int r = 0; r < 16; ++r) slope[r] = sc.slope(x[0][r]);
+            }
         }
         const bool near = add_bias<BIAS, 1>(x, CAP ? 1.f : sc.a, slope2, lut, md, kn + 4 * half - qpos, kn - (row0 + 31 + shift),
                                             kn + 31 - (row0 + shift));
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         for (int r = 0; r < 16; ++r) {
             s[r] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x[0][r], sc.a, -lse2) : x[0][r] - lse2);
             ds[r] = s[r] * dp[r];
+            // (without a bias the capped score is still there to take the derivative from)
+            if constexpr (CAP && BIAS == kBiasNone) ds[r] *= sc.slope(x[0][r]);
         }
         return near;
     };
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                         far_p[1] += near || !above ? 0.f : b;
                     }
                 }
-                if constexpr (CAP) ds *= slope;
+                if constexpr (CAP && BIAS != kBiasNone) ds *= slope;
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk) {
                     const Frag sf = O::pack(ds, kk);
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
     // stay raw products until the exponential, -lse in their units.
     constexpr bool RAW = !CAP && BIAS == kBiasNone;
     Score sc;
-    sc.init<T>(p.scale, p.cap, CAP, !CAP && BIAS == kBiasNone);
+    sc.init<T>(p.scale, p.cap, CAP, BIAS == kBiasNone);
     const float unit = RAW ? -kLog2e / sc.a : kLog2e;
     float sb = 0.f;
     auto fetch = [&](T* qs, T* gs, int it) {
@@ -607,8 +611,10 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
                 f32x16 slope;
                 if constexpr (CAP) {
                     sc.template capped<T>(s);
+                    if constexpr (BIAS != kBiasNone) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) slope[r] = sc.slope(s[0][r]);
+                        for (int r = 0; r < 16; ++r) slope[r] = sc.slope(s[0][r]);
+                    }
                 }
                 // (of register 0; later queries are further back)
                 add_bias<BIAS, -1>(s, CAP ? 1.f : sc.a, slope2, bias, md, key - (qn + shift + 4 * half), row0 - (qn + 31 + shift),
@@ -627,9 +633,10 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
                         const float x = s[0][r + e];
                         s[0][r + e] = exp2_hw(RAW ? x * sc.a : x - lv[e]);
                         dp[r + e] *= s[0][r + e];
+                        if constexpr (CAP && BIAS == kBiasNone) dp[r + e] *= sc.slope(x);
                     }
                 }
-                if constexpr (CAP) dp *= slope;
+                if constexpr (CAP && BIAS != kBiasNone) dp *= slope;
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk) {
                     const Frag pf = O::pack(s[0], kk), sf = O::pack(dp, kk);

@@ -332,7 +332,7 @@ struct Score {
     float rc2;     // 1 / c2
     float k[4];    // cap, bf16: c2 tanh(x scale / c) = x (k0 + k1 x^2 + k2 x^4 + k3 x^6) where x^2 <= small
     float small;
-    float none;    // a masked score, or (raw) a masked product
+    float none;    // a masked score; raw (no bias): a masked product, or with a cap a score whose derivative is finite
     template <typename T> __device__ __forceinline__ void init(float scale, float cap, bool capped, bool raw = false) {
         // (a scale of zero: a finite factor times a masked score has to stay minus infinity)
         const float s = fabsf(scale) < 1e-30f ? 1e-30f : scale, u = capped ? s / cap : 0.f;
@@ -343,7 +343,7 @@ struct Score {
         k[1] = k[0] * u * u * (-1.f / 3.f);
         k[2] = k[0] * (u * u) * (u * u) * (2.f / 15.f);
         k[3] = k[0] * (u * u) * (u * u) * (u * u) * (-17.f / 315.f);
-        none = raw && s < 0.f ? INFINITY : -INFINITY;
+        none = raw && capped ? -1e15f : raw && s < 0.f ? INFINITY : -INFINITY;
         small = capped ? 0.0625f / (u * u) : 0.f;
     }
     // The capped scores of N products, in place.  bf16: the series of tanh where all of the wave's arguments
