@@ -7,7 +7,10 @@
 // LDS, double buffered, the next tile on its way to LDS while the present one is used.  A wave forms
 // S^T = K Q^T (queries in lanes), so m and l are one number a lane, and P^T in its accumulator layout is
 // the operand of O^T += V^T P^T (ssd_attn_common.h).  O is rescaled only when a row's maximum has grown by
-// more than 2^8: weights are relative to m, so a late m costs no accuracy.  With too few rows to fill
+// more than 2^8: weights are relative to m, so a late m costs no accuracy.  In bf16 a weight is rounded for the
+// product with V; y is divided by the sum of the rounded weights, so that what their rounding has in
+// common drops out (a row of one key gives that value exactly, as the backward pass needs: it forms
+// dy.y - dy.v), and lse comes from the sum of the unrounded ones.  With too few rows to fill
 // the chip the waves split the keys instead (SPLIT).
 #include "ssd_attn_common.h"
 
@@ -36,7 +39,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     __shared__ __attribute__((aligned(16))) T k_b[DOUBLE ? ELEMS : 8];
     __shared__ __attribute__((aligned(16))) T v_b[DOUBLE ? ELEMS : 8];
     __shared__ float lut[BIAS == kBiasBuckets ? 2 * kMaxDistance + 1 : 1];
-    __shared__ float stat[SPLIT ? 3 : 1][SPLIT ? kWaves * 32 : 1];  // m, l, weight of a wave's share by row
+    constexpr bool ROUNDED = sizeof(T) == 2;  // weights lose bits on their way to V
+    __shared__ float stat[SPLIT ? 4 : 1][SPLIT ? kWaves * 32 : 1];  // by row: m, l, weight of a wave's share, sum of rounded weights
 
     int slot, unit;
     work_item(blockIdx.x, p.q_slots, (uint32_t)p.H / (uint32_t)p.pack, slot, unit);
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
-    float m = NO_MAX ? 0.f : kNoMax, l = 0.f;  // l: this lane half's share
+    float m = NO_MAX ? 0.f : kNoMax, l = 0.f, lr = 0.f;  // this lane half's share of the weights, and of the rounded ones
     const int qpos = mine + shift;
 
     auto settle = [&]() {  // what was on its way to LDS is there, and (SPLIT: this wave's) reads are over
@@ -130,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                     const float next = fmaxf(m, mx), keep = exp2_hw(m - next);
                     m = next;
                     l *= keep;
+                    lr *= keep;
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] *= keep;
                 }
@@ -148,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk) {
                     const Frag pf = O::pack(s[n], kk);
+                    if constexpr (ROUNDED) lr = sum_of(pf, lr);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] = O::mma(L::cols(vt, 32 * n, kk, 32 * d, z), pf, o[d]);
                 }
@@ -166,15 +172,17 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     }
 
     l += other_half(l);
+    if constexpr (ROUNDED) lr += other_half(lr); else lr = l;
     if constexpr (SPLIT) {
         if (half == 0) {
             stat[0][32 * wave + lane] = m;
             stat[1][32 * wave + lane] = l;
+            stat[3][32 * wave + lane] = lr;
         }
         __syncthreads();  // (nobody reads a tile any more)
         Join<T, D>::keep(k_a, v_a, o, lane, wave);
         if (threadIdx.x < 32) {
-            float top = kNoMax, sum = 0.f;
+            float top = kNoMax, sum = 0.f, rounded = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[0][32 * w + lane]);
             float f[kWaves];
@@ -182,8 +190,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             for (int w = 0; w < kWaves; ++w) {
                 f[w] = exp2_hw(stat[0][32 * w + lane] - top);
                 sum += f[w] * stat[1][32 * w + lane];
+                rounded += f[w] * stat[3][32 * w + lane];
             }
-            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+            const float inv = rounded > 0.f ? 1.f / rounded : (rounded == 0.f ? 0.f : rounded);
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) stat[2][32 * w + lane] = f[w] * inv;
             if (row < sp.rows && p.lse)
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     }
     // (the store exchanges words between a row's two lanes, which leave or stay together)
     if (row >= sp.rows) return;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (an empty row is zero; a NaN stays one)
+    const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);  // (an empty row is zero; a NaN stays one)
     T* yg = static_cast<T*>(p.y) + ((sp.q0 + mine) * p.H + head) * D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -214,7 +223,7 @@ template <typename T, int D, int CAPPED, int BIAS>
 int launch_fwd(AttnParams p, hipStream_t stream) {
     p.pack = query_pack(p, BIAS);
     const int units = p.H / p.pack;
-    const bool split = query_slots(p, kOwn<false>) * units < kSplitBelow;
+    const bool split = query_slots(p, kOwn<false>) * units < attn_split_below(Tile<T, D>::RB);
     p.q_slots = (int)query_slots(p, split ? kOwn<true> : kOwn<false>);
     set_each(p, split ? kOwn<true> : kOwn<false>, 1);
     const int64_t grid = (int64_t)p.q_slots * units;

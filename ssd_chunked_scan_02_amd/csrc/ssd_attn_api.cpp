@@ -163,12 +163,13 @@ struct BackwardWorkspace {
 };
 BackwardWorkspace backward_workspace(const ssd_attn_dims* d, bool table) {
     BackwardWorkspace w{};
+    const int row_bytes = (int)d->headdim * (d->dtype == SSD_BF16 ? 2 : 4);
     const int64_t q_slots = d->total_q / 128 + d->nseq + 1, k_slots = d->total_k / 128 + d->nseq + 1;
     int64_t parts = q_slots;
-    if (d->total_q / 128 * d->nheads < ssd::kSplitBelow) parts = d->total_q / 32 + d->nseq + 1;
+    if (d->total_q / 128 * d->nheads < ssd::attn_split_below(row_bytes)) parts = d->total_q / 32 + d->nseq + 1;
     w.delta = align16((size_t)d->total_q * (size_t)d->nheads * 4);
     w.part = table ? align16((size_t)parts * (size_t)d->nheads * (size_t)d->num_buckets * 4) : 0;
-    const int n = d->nseq > 0 ? ssd::attn_key_parts(nullptr, d->total_k - d->total_k % d->nseq, d->nseq, d->nkvheads) : 1;
+    const int n = d->nseq > 0 ? ssd::attn_key_parts(nullptr, d->total_k - d->total_k % d->nseq, d->nseq, d->nkvheads, row_bytes) : 1;
     w.dkv = n > 1 ? align16((size_t)(2 * n) * (size_t)d->total_k * (size_t)d->nkvheads * (size_t)d->headdim * 4) : 0;
     w.plan_q = align16((size_t)(d->total_q * (d->nheads / d->nkvheads) / 128 + d->nseq + 1) * 16);
     w.plan_k = align16((size_t)k_slots * 16);

@@ -769,7 +769,7 @@ int launch_dkv(AttnParams p, hipStream_t stream) {
     constexpr int OWN = kOwn<SHARE == kSplit>;
     p.k_slots = (int)attn_slots(p.cu_k, p.total_k, p.nseq, OWN);
     set_each(p, 1, OWN);
-    p.parts = SHARE == kSplit && p.dkv_part ? attn_key_parts(p.cu_k, p.total_k, p.nseq, p.Hk) : 1;
+    p.parts = SHARE == kSplit && p.dkv_part ? attn_key_parts(p.cu_k, p.total_k, p.nseq, p.Hk, Tile<T, D>::RB) : 1;
     const int64_t grid = (int64_t)p.k_slots * p.Hk * p.parts;
     const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (SHARE == kSplit ? p.H / p.Hk : 1);
     if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dkv_kernel<T, D, CAP, BIAS, SHARE>),
@@ -789,8 +789,8 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
     const bool dkv_fits = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, false) * (p.H / p.Hk) <= kSplitBiasLds;
     AttnParams d = p;
     d.pack = query_pack(p, BIAS);
-    const bool dq_split = dq_fits && query_slots(d, kOwn<false>) * (d.H / d.pack) < kSplitBelow;
-    const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < kSplitBelow;
+    const bool dq_split = dq_fits && query_slots(d, kOwn<false>) * (d.H / d.pack) < attn_split_below(Tile<T, D>::RB);
+    const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < attn_split_below(Tile<T, D>::RB);
     d.plan_q = d.plan_k = nullptr;
     AttnParams with_plan = p;
     with_plan.pack = d.pack;

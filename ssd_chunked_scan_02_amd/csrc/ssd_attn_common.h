@@ -68,6 +68,15 @@ template <> struct Op<float> {
     }
 };
 
+// c plus the sum of a bf16 operand's eight elements, in fp32.
+__device__ __forceinline__ float sum_of(bf16x8 f, float c) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) c = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{f[i], f[i + 1]}, one, c, false);
+    return c;
+}
+
 // Row-major tile [rows][D] in LDS, in 16-byte chunks, chunk c of a row stored at c ^ swz(row): the
 // eight rows that one pass of a 16-byte read touches, and the four rows of a transposing read, then
 // lie in different banks without padding.

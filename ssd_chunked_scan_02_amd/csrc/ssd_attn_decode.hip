@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) attn_decode_
     f32x4 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x4{};
+    // (in bf16 the sum of the rounded weights, the divisor that takes out what their rounding has in common)
     float m = kNoMax, l = 0.f;
 
     uint4 kb[2][NT], vb[VL];
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) attn_decode_
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 sv[n][r] = exp2_hw(sv[n][r] - m);
-                l += sv[n][r];
+                if constexpr (sizeof(T) == 4) l += sv[n][r];
             }
         if constexpr (sizeof(T) == 2) {
             // contraction over the 32 keys in the row order of the two stacked tiles: 4 g + j, 16 + 4 g + j - 4
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) attn_decode_
                 pf[j] = (__bf16)sv[0][j];
                 pf[4 + j] = (__bf16)sv[1][j];
             }
+            l = sum_of(pf, l);
             const __bf16* at = reinterpret_cast<const __bf16*>(vt) + (4 * g + col / 4) * VS + 4 * (col % 4);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {

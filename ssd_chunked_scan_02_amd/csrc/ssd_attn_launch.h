@@ -25,16 +25,23 @@ struct AttnBuckets {
     uint8_t of[kMaxDistance + 1];  // a direction's bucket by distance, to max_distance
 };
 
-// Workgroups of 128 rows below which the four waves of one split instead (kOwn in ssd_attn_common.h).
-constexpr int64_t kSplitBelow = 512;
+// Workgroups of 128 rows below which the four waves of one split instead (kOwn in ssd_attn_common.h), by the
+// bytes of a row.  A split workgroup's tiles take most of a CU's LDS from rows of 256 bytes on, so that it
+// stays alone there, and half of it below.  bf16, causal, one sequence, forward / dq / dk and dv in us,
+// split against not:
+//     64 wide, 4096 tokens   256 workgroups 46 / 51 / 64 against 74 / 83 / 111, 512: 83 / 90 / 120 against 79 / 91 / 123
+//     64 wide, 1024 tokens   256: 21 / 24 / 29 against 23 / 26 / 34,            512: 37 / 43 / 53 against 25 / 31 / 38
+//     128 wide, 4096 tokens  128: 51 / 52 / 68 against 82 / 114 / 143,          256: 93 / 97 / 127 against 84 / 119 / 148
+//     128 wide, 1024 tokens  128: 23 / 25 / 29 against 26 / 35 / 43,            256: 44 / 48 / 56 against 28 / 39 / 46
+inline int64_t attn_split_below(int row_bytes) { return row_bytes >= 256 ? 256 : 384; }
 // Tiles of a packed axis, at most: its whole tiles, and one more for each sequence.
 inline int64_t attn_slots(const int64_t* cu, int64_t total, int64_t nseq, int own) {
     if (nseq == 0) return 0;
     return cu ? total / own + nseq : nseq * ((total / nseq + own - 1) / own);
 }
 // Key gradients of a small problem: parts of a tile's queries, so that the workgroups reach the 256 CUs twice.
-inline int attn_key_parts(const int64_t* cu_k, int64_t total_k, int64_t nseq, int64_t Hk) {
-    if (attn_slots(cu_k, total_k, nseq, 128) * Hk >= kSplitBelow) return 1;
+inline int attn_key_parts(const int64_t* cu_k, int64_t total_k, int64_t nseq, int64_t Hk, int row_bytes) {
+    if (attn_slots(cu_k, total_k, nseq, 128) * Hk >= attn_split_below(row_bytes)) return 1;
     const int64_t grid = attn_slots(cu_k, total_k, nseq, 32) * Hk, n = grid > 0 ? 512 / grid : 1;
     return n < 1 ? 1 : n > 8 ? 8 : (int)n;
 }

@@ -255,3 +255,23 @@ def test_gradients_of_no_sequence_stay_as_they_were():
     want = _backward(cut, offsets(lens))
     for n in want:
         assert np.array_equal(got[n][:sum(lens)], want[n]), n
+
+
+@pytest.mark.parametrize("heads", ["few", "many"])
+@pytest.mark.parametrize("cap", [0.0, 50.0, 500.0])
+def test_a_row_of_one_key_is_that_value(cap, heads):
+    """Whatever its score, a lone key's weight is one: y is its value to the bit, and dq and dk nothing (dS is
+    dy.v - dy.y, where a y off by its rounding would be far larger than the rest of a long document's dq):
+    fp32 sums of D products in two orders, times the key and the scale."""
+    H, Hk = HEADS[heads][64]
+    lens = [1] * 40
+    d = make(77, 40, 40, H, Hk, 64, "bf16", grads=True)
+    d["q"] *= 3
+    y, lse = _forward(d, offsets(lens), cap=cap)
+    v = f64(d["v"]).repeat(H // Hk, 1)
+    assert np.array_equal(y, v)
+    got = _backward(d, offsets(lens), cap=cap)
+    worst = 2 * 64 * 2.0 ** -24 * (np.abs(f64(d["dy"])) * np.abs(v)).sum(-1).max() * 0.125 * 1.05
+    assert np.abs(got["dq"]).max() <= worst * np.abs(f64(d["k"])).max()
+    assert np.abs(got["dk"]).max() <= worst * (H // Hk) * np.abs(f64(d["q"])).max()
+    assert np.array_equal(got["dv"], f64(d["dy"])) or H != Hk
