@@ -77,16 +77,21 @@ __device__ __forceinline__ float sum_of(bf16x8 f, float c) {
     return c;
 }
 
-// Row-major tile [rows][D] in LDS, in 16-byte chunks, chunk c of a row stored at c ^ swz(row): the
-// eight rows that one pass of a 16-byte read touches, and the four rows of a transposing read, then
-// lie in different banks without padding.
+// Row-major tile [rows][D] in LDS, in 16-byte chunks, chunk c of a row stored at c ^ swz(row).  LDS serves
+// 256 bytes (16 chunks) at a time: the 16 rows that a pass of 16-byte reads takes at one chunk, and the
+// four rows by four chunks that a pass of transposing reads takes, lie in different banks without padding.
+// (fp32: a pass of 4-byte reads takes eight chunks of two rows four apart.)  swz only moves bits of the
+// row, so that swz(a ^ b) = swz(a) ^ swz(b).
 template <typename T, int D> struct Tile {
     static constexpr int kE = Op<T>::kE;
     static constexpr int CH = D / kE;
     static constexpr int RB = D * (int)sizeof(T);
-    static constexpr int RPB = RB >= 256 ? 1 : 256 / RB;
-    static constexpr int MASK = CH / 2 - 1 < 7 ? CH / 2 - 1 : 7;
-    static __device__ __forceinline__ int swz(int row) { return 2 * ((row / RPB) & MASK); }
+    static __host__ __device__ __forceinline__ constexpr int swz(int r) {
+        if constexpr (sizeof(T) == 2)
+            return CH == 16 ? ((r & 3) << 2) | ((r >> 2) & 3) : CH == 8 ? ((r & 2) << 1) | ((r >> 2) & 3) : (r >> 2) & 3;
+        else
+            return CH >= 16 ? ((r & 4) << 1) | ((r & 3) << 1) | ((r >> 3) & 1) : (r >> 1) & 7;
+    }
     static __device__ __forceinline__ int at(int row, int c) { return (row * CH + (c ^ swz(row))) * kE; }
 
     // A lane's part of the byte addresses of its operands: rows() and cols() add to it what does not depend on
@@ -95,7 +100,7 @@ template <typename T, int D> struct Tile {
         uint32_t row, col;
         __device__ __forceinline__ explicit Lanes(int lane) {
             const int r = lane % 32, h = lane / 32;
-            row = (uint32_t)(r * RB + (h + swz(r)) * 16);
+            row = (uint32_t)(r * RB + (h ^ swz(r)) * 16);
             if constexpr (sizeof(T) == 2) {
                 const int q = lane % 4, kr = 4 * h + (lane % 16) / 4;
                 col = (uint32_t)(kr * RB + ((2 * ((lane / 16) % 2) + q / 2) ^ swz(kr)) * 16 + (q % 2) * 8);
@@ -118,18 +123,18 @@ template <typename T, int D> struct Tile {
         if constexpr (sizeof(T) == 2) {
             // ds_read_b64_tr_b16: a 16-lane group whose lane 4 r + q points at row r, columns 4 q .. 4 q + 3
             // returns column i of those four rows in its lane i
-            static_assert(sizeof(T) != 2 || RPB * (MASK + 1) <= 8, "eight rows on, the swizzle is the same");
-            at += (z.col ^ (uint32_t)(2 * col0)) + (row0 + 16 * kk) * RB;
-            const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)at);
-            const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(at + 8 * RB));
+            const uint32_t low = z.col ^ (uint32_t)(2 * col0);
+            at += (row0 + 16 * kk) * RB;
+            const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(at + low));
+            const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(at + (low ^ (swz(8) * 16u)) + 8 * RB));
             const v8i16 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             return __builtin_bit_cast(bf16x8, v);
         } else {
-            // (row 4 h + i of eight: its swizzle is that of 4 h, in `col`, and of i)
             f32x4 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = *reinterpret_cast<const float*>(at + (z.col ^ (uint32_t)(swz(i) * 16) ^ (uint32_t)(4 * col0)) + (row0 + 8 * kk + i) * RB);
+                v[i] = *reinterpret_cast<const float*>(at + (z.col ^ (uint32_t)(swz(8 * kk + i) * 16) ^ (uint32_t)(4 * col0)) +
+                                                       (row0 + 8 * kk + i) * RB);
             return v;
         }
     }
