@@ -12,6 +12,12 @@
 // common drops out (a row of one key gives that value exactly, as the backward pass needs: it forms
 // dy.y - dy.v), and lse comes from the sum of the unrounded ones.  With too few rows to fill
 // the chip the waves split the keys instead (SPLIT).
+//
+// Measured: 16384 tokens, 32/4 heads of 128, causal, bf16: 2.13 ms, 1.03 PFLOP/s, bound by MFMA (86% of what an
+// 8192^3 matrix product reaches).  8 x 2048 tokens, 24 heads of 64, capped: 187 us, 550 TFLOP/s, bound by VALU: a
+// score costs 11 instructions, one of them an exponential of four issue slots, against 4 MFMA cycles a lane.
+// The tile: 32 queries a wave and 64 keys read LDS at half its rate when MFMA is full and leave registers for two
+// (128-wide heads) or three waves a SIMD; 32 keys at a time measured 2.30 against 2.17 ms at 128 wide.
 #include "ssd_attn_common.h"
 
 namespace ssd {

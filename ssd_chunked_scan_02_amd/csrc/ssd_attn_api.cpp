@@ -3,7 +3,6 @@
 #include "ssd_attn.h"
 
 #include <cmath>
-#include <vector>
 
 #include <hip/hip_runtime.h>
 
@@ -17,25 +16,22 @@ constexpr int64_t kMaxHeads = 1 << 16;
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// A whole number of any size (little-endian 32-bit limbs), so that bucket borders are compared without
-// rounding.
+// A whole number (little-endian 32-bit limbs), so that bucket borders are compared without rounding.  The
+// largest is 1025^32 * 32^32, under 2^481.
 struct Whole {
-    std::vector<uint32_t> limb{1};
-    void times(uint32_t f) {
-        uint64_t carry = 0;
-        for (uint32_t& x : limb) {
-            carry += (uint64_t)x * f;
-            x = (uint32_t)carry;
-            carry >>= 32;
-        }
-        if (carry) limb.push_back((uint32_t)carry);
-    }
+    uint32_t limb[16] = {1};
     void times_power(uint32_t f, int n) {
-        while (n-- > 0) times(f);
+        while (n-- > 0) {
+            uint64_t carry = 0;
+            for (uint32_t& x : limb) {
+                carry += (uint64_t)x * f;
+                x = (uint32_t)carry;
+                carry >>= 32;
+            }
+        }
     }
     bool at_least(const Whole& o) const {
-        if (limb.size() != o.limb.size()) return limb.size() > o.limb.size();
-        for (size_t i = limb.size(); i-- > 0;)
+        for (int i = 15; i >= 0; --i)
             if (limb[i] != o.limb[i]) return limb[i] > o.limb[i];
         return true;
     }

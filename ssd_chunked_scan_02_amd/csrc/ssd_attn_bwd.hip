@@ -16,6 +16,10 @@
 // the sum of a row's dS is what the D that it was formed with is off by, so after the pass over all
 // keys D is exact; far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of
 // their p, and the tiles near the diagonal are visited once more with the exact D, for the table alone.
+//
+// Measured, bf16: 8 x 2048 tokens, 24 heads of 64, capped: dq 260 us (bound by VALU, 81% busy), dk and dv 350 us
+// (VALU 59%, MFMA 29%, in turns); 16385 packed tokens, 16/4 heads of 128, buckets: dq 217 us, dk and dv 243 us
+// (530 us with four waves a workgroup and tiles in the order of the documents), table 8 us, plan 6 us.
 #include "ssd_attn_common.h"
 
 namespace ssd {
@@ -443,7 +447,8 @@ __global__ void __launch_bounds__(kThreads) attn_dtable_kernel(AttnParams p) {
     }
 }
 
-// How a workgroup of the key-gradient kernel shares its work.
+// How a workgroup of the key-gradient kernel shares its work.  (kPaired at 64-wide heads, whose sums leave room for two
+// waves a SIMD anyway: 452 us against 350.)
 enum Share {
     kAlone = 0,   // four waves, 32 keys each
     kSplit = 1,   // four waves on the same 32 keys (see kOwn)
