@@ -29,8 +29,9 @@
  * Layouts: q, y [total_q, H, D], k, v [total_k, Hk, D]; one token's heads are dense, and q, k, v may be
  * views of wider rows (a fused projection's output) with a token stride of their own.  Everything else
  * is dense.  slopes, table and lse are fp32 whatever the dtype.
- * Non-finite inputs propagate to the outputs of their own sequence and head, and of a key/value head's
- * whole group in gradients; inputs outside every sequence reach no output.
+ * Non-finite inputs: y and lse of a query depend on that query and on the keys and values it sees, whatever
+ * the others hold.  Gradients: an infinity or NaN may reach every gradient of its own sequence and key/value
+ * head.  Inputs outside every sequence reach no output.
  */
 #ifndef SSD_ATTN_H
 #define SSD_ATTN_H

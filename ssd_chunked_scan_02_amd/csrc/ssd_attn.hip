@@ -3,8 +3,9 @@
 //     visible j;  y_i = sum_j p_ij v_j;  lse_i = log sum_j exp s_ij.
 //
 // One pass over the keys with a running maximum m and sum l (in log2 units): a workgroup of four waves
-// owns 128 query rows (of one head, or of all heads of a group) of a document, 32 a wave, and streams 64-key tiles (32 in fp32) through
-// LDS, double buffered, the next tile on its way to LDS while the present one is used.  A wave forms
+// owns 128 query rows (of one head, or of all heads of a group) of a document, 32 a wave, and streams
+// 64-key tiles (32 in fp32) through LDS, double buffered, the next tile on its way to LDS while the present
+// one is used.  A wave forms
 // S^T = K Q^T (queries in lanes), so m and l are one number a lane, and P^T in its accumulator layout is
 // the operand of O^T += V^T P^T (ssd_attn_common.h).  O is rescaled only when a row's maximum has grown by
 // more than 2^8: weights are relative to m, so a late m costs no accuracy.  In bf16 a weight is rounded for the
@@ -12,6 +13,11 @@
 // common drops out (a row of one key gives that value exactly, as the backward pass needs: it forms
 // dy.y - dy.v), and lse comes from the sum of the unrounded ones.  With too few rows to fill
 // the chip the waves split the keys instead (SPLIT).
+//
+// A row's y depends on the keys that it sees, whatever lies in the others of its tile: a weight of zero does not keep
+// an infinity or NaN of V out of a product, so where one has come up under a causal mask the workgroup does its tiles
+// again with those values taken out, and rewrites the rows that see none of them (attn_fwd_rows<CAREFUL>; the vote costs 0.3 us of the 11.5 of
+// 256 tokens of one head, and nothing that 2 ms of a long prompt show).
 //
 // Measured: 16384 tokens, 32/4 heads of 128, causal, bf16: 2.13 ms, 1.03 PFLOP/s, bound by MFMA (86% of what an
 // 8192^3 matrix product reaches).  8 x 2048 tokens, 24 heads of 64, capped: 187 us, 550 TFLOP/s, bound by VALU: a
@@ -30,31 +36,39 @@ constexpr float kLazy = 8.f;  // log2 growth of a maximum that is let pass witho
 constexpr float kNoMaxNeeded = 80.f;
 enum Cap { kCapNone = 0, kCapped = 1, kCapBounds = 2 };  // kCapBounds: without a bias, by a cap that needs no maximum
 
-template <typename T, int D, int CAPPED, int BIAS, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_fwd_kernel(AttnParams p) {
+// LDS, in arrays of their own: a load on its way to one is not waited for at another.
+template <typename T, int D, bool SPLIT> struct FwdShared {
+    static constexpr int KT = SPLIT ? 32 : Op<T>::kKT, ELEMS = (SPLIT ? kWaves : 1) * KT * D;
+    static constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;  // (two buffers of split fp32 tiles of 128 would not fit)
+    T *k_a, *v_a, *k_b, *v_b;
+    float* lut;
+    float (*stat)[SPLIT ? kWaves * 32 : 1];  // by row: m, l, weight of a wave's share, sum of rounded weights, spoilt
+    uint32_t (*spoilt)[SPLIT ? kWaves : 1][KT];  // CAREFUL, by buffer: keys with an infinity or NaN in V
+};
+
+// The rows of workgroup `block`; CAREFUL: without what is infinite or NaN in V, and only the rows that see none of it.
+// Returns whether something infinite or NaN came up.
+template <typename T, int D, int CAPPED, int BIAS, bool SPLIT, bool CAREFUL>
+__device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShared<T, D, SPLIT>& lds, uint32_t block, int tid) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
     constexpr int OWN = kOwn<SPLIT>, KT = SPLIT ? 32 : O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
-    constexpr int ELEMS = (SPLIT ? kWaves : 1) * KT * D;
-    constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;  // (two buffers of split fp32 tiles of 128 would not fit)
+    constexpr bool DOUBLE = FwdShared<T, D, SPLIT>::DOUBLE;
     constexpr bool CAP = CAPPED != kCapNone, NO_MAX = CAPPED == kCapBounds;
     constexpr bool RAW = !CAP && BIAS == kBiasNone;  // scores stay raw products until the exponential
-    __shared__ __attribute__((aligned(16))) T k_a[ELEMS];
-    __shared__ __attribute__((aligned(16))) T v_a[ELEMS];
-    __shared__ __attribute__((aligned(16))) T k_b[DOUBLE ? ELEMS : 8];
-    __shared__ __attribute__((aligned(16))) T v_b[DOUBLE ? ELEMS : 8];
-    __shared__ float lut[BIAS == kBiasBuckets ? 2 * kMaxDistance + 1 : 1];
     constexpr bool ROUNDED = sizeof(T) == 2;  // weights lose bits on their way to V
-    __shared__ float stat[SPLIT ? 4 : 1][SPLIT ? kWaves * 32 : 1];  // by row: m, l, weight of a wave's share, sum of rounded weights
+    T *const k_a = lds.k_a, *const v_a = lds.v_a, *const k_b = lds.k_b, *const v_b = lds.v_b;
+    const auto stat = lds.stat;
+    const auto spoilt = lds.spoilt;
 
     int slot, unit;
-    work_item(blockIdx.x, p.q_slots, (uint32_t)p.H / (uint32_t)p.pack, slot, unit);
+    work_item(block, p.q_slots, (uint32_t)p.H / (uint32_t)p.pack, slot, unit);
     const Span sp = find_span(p, slot, OWN, false);
-    if (sp.tile < 0) return;
+    if (sp.tile < 0) return false;
     const int head0 = unit * p.pack, kvh = (int)((uint32_t)head0 / ((uint32_t)p.H / (uint32_t)p.Hk));
-    const int lane = threadIdx.x % kWave, half = lane / 32;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int lane = tid % kWave, half = lane / 32;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int shift = sp.lk - sp.lq;  // position of query 0 on the key axis
     int prefix = 0;
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
@@ -94,22 +108,38 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     sc.init<T>(fabsf(p.scale), p.cap, CAP);
     float slope2 = 0.f;
     if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[head] * kLog2e;
-    if constexpr (BIAS == kBiasBuckets) fill_bias(lut, p, head);
+    if constexpr (BIAS == kBiasBuckets) fill_bias(lds.lut, p, head);
 
     f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
     float m = NO_MAX ? 0.f : kNoMax, l = 0.f, lr = 0.f;  // this lane half's share of the weights, and of the rounded ones
     const int qpos = mine + shift;
+    bool sees_spoilt = false;
 
-    auto settle = [&]() {  // what was on its way to LDS is there, and (SPLIT: this wave's) reads are over
-        __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
+    auto meet = [&]() {
         if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
+    };
+    // what was on its way to LDS (the values: to v) is there, and (SPLIT: this wave's) reads are over
+    auto settle = [&](T* v) {
+        __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
+        meet();
+        if (CAREFUL && v) {
+            uint32_t* keys = spoilt[v == vb][SPLIT ? wave : 0];
+            if (lane < KT) keys[lane] = 0;
+            meet();
+            vf.clean(v, keys);
+            meet();
+        }
     };
     const typename L::Lanes z(lane);
     auto step = [&](const T* kt, const T* vt, T* kn, T* vn, int t) {
         const int k0 = t * KT;
         if (DOUBLE && t + dt < ntiles) fetch(kn, vn, t + dt);
+        if constexpr (CAREFUL) {
+#pragma unroll 1
+            for (int j = 0; j < KT; ++j) sees_spoilt |= spoilt[vt == vb][SPLIT ? wave : 0][j] && k0 + j < my_limit;
+        }
         if (k0 < wave_most) {
             f32x16 s[NS];
 #pragma unroll
@@ -119,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                 for (int i = 0; i < NT; ++i) s[n] = O::mma(L::rows(kt, 32 * n, i, z), qf[i], s[n]);
             }
             if constexpr (CAP) sc.template capped<T>(s);
-            add_bias<BIAS, 1>(s, CAP ? 1.f : sc.a, slope2, lut, p.bk.max_distance, k0 + 4 * half - qpos,
+            add_bias<BIAS, 1>(s, CAP ? 1.f : sc.a, slope2, lds.lut, p.bk.max_distance, k0 + 4 * half - qpos,
                               k0 - (row0 + 31 + shift), k0 + KT - 1 - (row0 + shift));
             if (k0 + KT > wave_least) {
                 const int left = my_limit - k0 - 4 * half;
@@ -164,14 +194,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                     for (int d = 0; d < DT; ++d) o[d] = O::mma(L::cols(vt, 32 * n, kk, 32 * d, z), pf, o[d]);
                 }
         }
-        settle();
+        settle(DOUBLE && t + dt < ntiles ? vn : nullptr);
         if (!DOUBLE && t + dt < ntiles) {
             fetch(kn, vn, t + dt);
-            settle();
+            settle(vn);
         }
     };
-    settle();
     if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();  // (the bias is everybody's)
+    settle(t0 < ntiles ? va : nullptr);
     for (int t = t0; t < ntiles; t += 2 * dt) {
         step(ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
         if (t + dt < ntiles) step(DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);
@@ -184,10 +214,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             stat[0][32 * wave + lane] = m;
             stat[1][32 * wave + lane] = l;
             stat[3][32 * wave + lane] = lr;
+            stat[4][32 * wave + lane] = sees_spoilt ? 1.f : 0.f;
         }
         __syncthreads();  // (nobody reads a tile any more)
         Join<T, D>::keep(k_a, v_a, o, lane, wave);
-        if (threadIdx.x < 32) {
+        if (tid < 32) {
             float top = kNoMax, sum = 0.f, rounded = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[0][32 * w + lane]);
@@ -205,24 +236,51 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                 p.lse[(sp.q0 + mine) * p.H + head] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
+        for (int i = tid; i < 32 * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
             if (row0 + r >= sp.rows) break;
+            if (stat[4][r] + stat[4][32 + r] + stat[4][64 + r] + stat[4][96 + r] > 0.f) continue;
             const f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, stat[2]);
             const int q = query_of(row0 + r);
             store4(static_cast<T*>(p.y) + ((sp.q0 + q) * p.H + head0 + row0 + r - q * p.pack) * D + 4 * d4, v[0], v[1], v[2], v[3]);
         }
-        return;
+    } else if (row < sp.rows && !sees_spoilt) {
+        // (the store exchanges words between a row's two lanes, which are in or out together)
+        const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);  // (an empty row is zero; a NaN stays one)
+        T* yg = static_cast<T*>(p.y) + ((sp.q0 + mine) * p.H + head) * D;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 8) store_rows(yg + 32 * d, o[d], r, half, inv);
+        if (p.lse && half == 0) p.lse[(sp.q0 + mine) * p.H + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
     }
-    // (the store exchanges words between a row's two lanes, which leave or stay together)
-    if (row >= sp.rows) return;
-    const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);  // (an empty row is zero; a NaN stays one)
-    T* yg = static_cast<T*>(p.y) + ((sp.q0 + mine) * p.H + head) * D;
+
+    if constexpr (CAREFUL) return false;
+    float bad = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 8) store_rows(yg + 32 * d, o[d], r, half, inv);
-    if (p.lse && half == 0) p.lse[(sp.q0 + mine) * p.H + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        for (int r = 0; r < 16; ++r) bad = __builtin_fmaf(o[d][r], 0.f, bad);
+    return bad != 0.f;
+}
+
+template <typename T, int D, int CAPPED, int BIAS, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_fwd_kernel(AttnParams p) {
+    using S = FwdShared<T, D, SPLIT>;
+    __shared__ __attribute__((aligned(16))) T k_a[S::ELEMS];
+    __shared__ __attribute__((aligned(16))) T v_a[S::ELEMS];
+    __shared__ __attribute__((aligned(16))) T k_b[S::DOUBLE ? S::ELEMS : 8];
+    __shared__ __attribute__((aligned(16))) T v_b[S::DOUBLE ? S::ELEMS : 8];
+    __shared__ float lut[BIAS == kBiasBuckets ? 2 * kMaxDistance + 1 : 1];
+    __shared__ float stat[SPLIT ? 5 : 1][SPLIT ? kWaves * 32 : 1];
+    __shared__ uint32_t spoilt[2][SPLIT ? kWaves : 1][S::KT];
+    const S lds{k_a, v_a, k_b, v_b, lut, stat, spoilt};
+    const bool bad = attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, false>(p, lds, blockIdx.x, threadIdx.x);
+    if (!p.causal || !__syncthreads_or(bad)) return;
+    uint32_t block = blockIdx.x;
+    int tid = threadIdx.x;
+    asm volatile("" : "+s"(block), "+v"(tid));  // (nothing worked out for the first time is kept for this one)
+    attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, true>(p, lds, block, tid);
 }
 
 template <typename T, int D, int CAPPED, int BIAS>

@@ -133,6 +133,29 @@ def test_documents_do_not_reach_each_other():
         assert np.array_equal(y[s], clean[s])
 
 
+@pytest.mark.parametrize("heads", ["few", "many"])
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("fp32", 32), ("fp32", 128)])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_what_a_row_does_not_see_does_not_reach_it(dtype, D, heads, prefix):
+    """NaN and infinities in later keys and values of the same document (a padded batch's tail) leave the rows
+    that do not see them as they were; the rows that do are not finite."""
+    H, Hk = HEADS[heads][D]
+    lens, bad = [300, 90], {0: [200, 250], 1: [64]}
+    d = make(90 + D, sum(lens), sum(lens), H, Hk, D, dtype)
+    cu = offsets(lens)
+    pre = torch.tensor([100, 70], dtype=torch.int64) if prefix else None
+    clean, lse0 = _forward(d, cu, prefix=pre)
+    d["v"][200], d["v"][250, 0, 3] = float("nan"), float("inf")
+    d["v"][300 + 64], d["k"][300 + 64] = float("-inf"), float("nan")
+    y, lse = _forward(d, cu, prefix=pre)
+    first = {0: 200, 1: 0 if prefix else 64}             # (key 64 of the second is in its prefix of 70)
+    for s, at in ((0, 0), (1, 300)):
+        rows = slice(at, at + first[s])
+        assert np.array_equal(y[rows], clean[rows]) and np.array_equal(lse[rows], lse0[rows])
+        seen = y[at + first[s]:at + lens[s]]
+        assert not np.isfinite(seen.reshape(len(seen), -1)).all(1).any()
+
+
 def test_many_short_documents():
     """More documents than one search step takes, most of them a few tokens long."""
     lens = [(5 * i) % 7 for i in range(4500)] + [200]
