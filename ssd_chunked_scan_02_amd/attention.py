@@ -122,6 +122,15 @@ def _offsets(t, name, device, n=None):
         raise ValueError("%s has %d values, expected %d" % (name, t.numel(), n))
 
 
+def _workspace(t, need, device):
+    """The caller's workspace, or one of ``need`` bytes, and its size."""
+    if t is None:
+        return (None, 0) if need == 0 else (torch.empty(need, dtype=torch.uint8, device=device), need)
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return t, t.numel() * t.element_size()
+
+
 def _bias_args(slopes, table, H, device):
     if slopes is None and table is None:
         return 0
@@ -219,9 +228,7 @@ def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, c
         # (no sequence: no launch writes it)
         out["dtable"] = (torch.empty if dims.nseq else torch.zeros)(table.shape, dtype=torch.float32, device=dev)
     need = ssd_attn_backward_workspace_bytes(dims, want_dtable)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, dev)
     _on_stream(stream, workspace, *out.values())
     _call("ssd_attn_backward", dev, stream, ctypes.byref(dims), _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(prefix),
           _addr(q), _addr(k), _addr(v), _addr(slopes), _addr(table), _addr(y), _addr(lse), _addr(dy), _addr(out["dq"]),
@@ -273,9 +280,7 @@ def ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
         y = torch.empty((nseq, H, D), dtype=q.dtype, device=dev)
     _dense(y, "y", (nseq, H, D), q.dtype, dev)
     need = ssd_attn_decode_workspace_bytes(dims)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, dev)
     _on_stream(stream, y, workspace)
     _call("ssd_attn_decode", dev, stream, ctypes.byref(dims), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table),
           _addr(seq_lens), _addr(slopes), _addr(table), _addr(y), _addr(workspace), ws_bytes)

@@ -11,6 +11,7 @@ import torch
 
 import oracle.attention as oa
 import ssd_chunked_scan_02_amd as ssd
+from ssd_chunked_scan_02_amd import attention
 from ssd_chunked_scan_02_amd.attention import AttnCache, AttnDims
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -163,6 +164,42 @@ def test_append_refusals(lib):
     assert call(inv=P, rot=40) == INVALID and call(inv=P, rot=12) == UNSUPPORTED and call(inv=P, rot=-8) == INVALID
     assert call(inter=2) == INVALID
     assert call(tokens=0, cu=P) == OK and call(d=_cache(nseq=0), tokens=0) == OK
+
+
+def test_an_output_that_is_an_input_is_refused(lib):
+    X = [P + 4096 * i for i in range(12)]
+    q, k, v, y, lse, dy, dq, dk, dv, ws = X[:10]
+    for bad in (q, k, v):
+        assert _forward(lib, _dims(), q=q, k=k, v=v, y=bad) == INVALID
+
+    def backward(dq=dq, dk=dk, dv=dv, ws=ws):
+        return lib.ssd_attn_backward(ctypes.byref(_dims()), None, None, None, q, k, v, None, None, y, lse, dy, dq, dk, dv, None,
+                                     ws, 1 << 30, None)
+
+    for name in ("dq", "dk", "dv", "ws"):
+        for bad in (q, k, v, y, lse, dy):
+            assert backward(**{name: bad}) == INVALID, name
+
+    def decode(y=y, ws=ws):
+        return lib.ssd_attn_decode(ctypes.byref(_cache()), q, k, v, X[10], X[11], None, None, y, ws, 1 << 30, None)
+
+    def append(qo=y, kc=lse, vc=dy):
+        return lib.ssd_kv_append(ctypes.byref(_cache()), 3, None, X[10], X[11], k, v, q, None, 0, 0, kc, vc, qo, None)
+
+    for bad in (q, k, v):
+        assert decode(y=bad) == INVALID and decode(ws=bad) == INVALID
+        assert append(qo=bad) == INVALID and append(kc=bad) == INVALID and append(vc=bad) == INVALID
+
+
+def test_binding_refuses_a_workspace_elsewhere():
+    for bad in (torch.empty(64, dtype=torch.uint8), torch.empty(64, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError):
+            attention._workspace(bad, 64, torch.device("cuda", 0))
+    with pytest.raises(ValueError):
+        attention._workspace(torch.empty(64, 2, dtype=torch.uint8)[:, 0], 64, torch.device("cpu"))
+    t = torch.empty(32, dtype=torch.int32)
+    assert attention._workspace(t, 64, torch.device("cpu")) == (t, 128)
+    assert attention._workspace(None, 0, torch.device("cpu")) == (None, 0)
 
 
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
