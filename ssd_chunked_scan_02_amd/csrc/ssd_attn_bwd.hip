@@ -11,10 +11,11 @@
 // gradients through memory.  Both keep their rows' operands and gradients in registers; the tile layout
 // and operand order are the forward kernel's (ssd_attn_common.h).
 //
-// D is sum_d dy_id y_id, which is as exact as the given y, and a bf16 y is exact enough for dq and dk.  The
-// gradient of the table sums dS over whole diagonals, where that error would be most of the result's.  But
-// the sum of a row's dS is what the D that it was formed with is off by, so after the pass over all
-// keys D is exact; far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of
+// D is sum_d dy_id y_id, which is as exact as the given y.  What a bf16 y leaves in dq and dk, (y's error . dy)
+// sum_j p_ij k_j, falls as 1 / n with the n keys of a row beside a dq that falls as 1 / sqrt(n).  The sum of a row's
+// dS is what the D that it was formed with is off by: rows that see one tile of keys (the first of a document, where
+// that error was most of all dq's) take it from a first visit to their tile.  The gradient of the table sums dS over
+// whole diagonals, where it counts for every row: after the pass over all keys D is exact; far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of
 // their p, and the tiles near the diagonal are visited once more with the exact D, for the table alone.
 //
 // Measured, bf16: 8 x 2048 tokens, 24 heads of 64, capped: dq 260 us (bound by VALU, 81% busy), dk and dv 350 us
@@ -156,10 +157,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
         if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
     };
-    // p and dS of 32 keys from kn on (dS before the cap's derivative, which is returned in `slope`); true: some
-    // are nearer than the table's reach
+    // p and dS of 32 keys from kn on (dS before the cap's derivative, which is returned in `slope`, or with no bias
+    // and `whole` already in dS); true: some are nearer than the table's reach
     typename L::Lanes z(lane);
-    auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope) {
+    auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope, bool whole = true) {
         z.renew();
         f32x16 x[1] = {f32x16{}}, dp;
 #pragma unroll
@@ -187,7 +188,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             s[r] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x[0][r], sc.a, -lse2) : x[0][r] - lse2);
             ds[r] = s[r] * dp[r];
             // (without a bias the capped score is still there to take the derivative from)
-            if constexpr (CAP && BIAS == kBiasNone) ds[r] *= sc.slope(x[0][r]);
+            if constexpr (CAP && BIAS == kBiasNone) {
+                if (whole) ds[r] *= sc.slope(x[0][r]);
+            }
         }
         return near;
     };
@@ -235,6 +238,18 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     };
     settle();
     if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();
+    if (t0 == 0 && wave_most > 0 && wave_most <= KT) {
+        // all that these rows see is there: first the sum of dS, which D is off by
+        float off = 0.f;
+#pragma unroll 1
+        for (int n = 0; n < NS; ++n) {
+            f32x16 s, ds, slope;
+            weights(ka, va, n, 32 * n, s, ds, slope, false);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) off += ds[r];
+        }
+        delta += off + other_half(off);
+    }
     for (int t = t0; t < ntiles; t += 2 * dt) {
         step(ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
         if (t + dt < ntiles) step(DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import ssd_chunked_scan_02_amd as ssd
-from attn_helpers import f64, grad_bounds, lse_bound, make, offsets, reference, some_heads, within, y_bound
+from attn_helpers import U, f64, grad_bounds, lse_bound, make, offsets, reference, some_heads, within, y_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -298,3 +298,38 @@ def test_a_row_of_one_key_is_that_value(cap, heads):
     assert np.abs(got["dq"]).max() <= worst * np.abs(f64(d["k"])).max()
     assert np.abs(got["dk"]).max() <= worst * (H // Hk) * np.abs(f64(d["q"])).max()
     assert np.array_equal(got["dv"], f64(d["dy"])) or H != Hk
+
+
+@pytest.mark.parametrize("heads", ["few", "many"])
+@pytest.mark.parametrize("cap", [0.0, 2.0])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_short_documents_without_the_rounding_of_y(D, cap, heads):
+    """dq of rows that see one tile of keys, in bf16: dS and dq are rounded to bf16 once each, and what the
+    rounding of y leaves in dy.y is not in dS.  With A_ij = sum_d |dy_id v_jd| the fp32 part of dS is off by its
+    weight's error (twice the score's e_s, and the sums') times A_ij + sum_j p_ij A_ij, at dP, at D and at the sum
+    of dS, and the cap's derivative by some steps."""
+    H, Hk = HEADS[heads][D]
+    lens = [1, 2, 3, 5, 17, 31, 32] * (4 if heads == "many" else 1) + ([33, 63, 64] * 60 if heads == "many" else [])
+    n = sum(lens)
+    d = make(55 + D, n, n, H, Hk, D, "bf16", grads=True)
+    cu = offsets(lens)
+    got = _backward(d, cu, cap=cap)["dq"]
+    h = [0, H // 2, H - 1]
+    q, dy = f64(d["q"])[:, h], f64(d["dy"])[:, h]
+    k, v = (f64(d[x])[:, [i // (H // Hk) for i in h]] for x in ("k", "v"))
+    u, scale, at = 2.0 ** -24, D ** -0.5, 0
+    for n in lens:
+        Q, K, V, G = (x[at:at + n].transpose(1, 0, 2) for x in (q, k, v, dy))
+        z = scale * Q @ K.transpose(0, 2, 1)
+        s = cap * np.tanh(z / cap) if cap else z
+        w = np.where(np.tril(np.ones((n, n), bool)), np.exp(s - s.max(-1, keepdims=True)), 0.0)
+        pr = w / w.sum(-1, keepdims=True)
+        dp, A = G @ V.transpose(0, 2, 1), np.abs(G) @ np.abs(V).transpose(0, 2, 1)
+        ds = pr * (dp - (pr * dp).sum(-1, keepdims=True))
+        slope = 1 - (s / cap) ** 2 if cap else np.ones_like(s)
+        es = ((D + 16) * scale * np.abs(Q) @ np.abs(K).transpose(0, 2, 1) + 4 * max(cap, 1.0)).max(-1, keepdims=True) * u
+        fine = pr * (A + (pr * A).sum(-1, keepdims=True)) * 2 * (2 * es + (D + n + 32) * u)
+        want = (ds * slope) @ K * scale
+        bound = 1.1 * (((U["bf16"] * np.abs(ds * slope) + fine) @ np.abs(K)) * scale + U["bf16"] * np.abs(want))
+        within(got[at:at + n][:, h], want.transpose(1, 0, 2), bound.transpose(1, 0, 2) + 1e-30, "D%d cap %g, %d tokens" % (D, cap, n))
+        at += n
