@@ -71,6 +71,8 @@ def _call(name, device, stream, *args):
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     else:
+        if stream.device != device:
+            raise ValueError("stream is of %s, the tensors are on %s" % (stream.device, device))
         handle = stream.cuda_stream
     function = getattr(load_library(), name)
     if torch._C._cuda_getDevice() == index:
@@ -122,10 +124,21 @@ def _offsets(t, name, device, n=None):
         raise ValueError("%s has %d values, expected %d" % (name, t.numel(), n))
 
 
-def _workspace(t, need, device):
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on ``stream`` (None: the current one), taken from that stream's own pool: a block that was
+    just freed on another stream may still be in use by what is queued there, which the call would not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError("stream is of %s, the tensors are on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(t, need, device, stream=None):
     """The caller's workspace, or one of ``need`` bytes, and its size."""
     if t is None:
-        return (None, 0) if need == 0 else (torch.empty(need, dtype=torch.uint8, device=device), need)
+        return (None, 0) if need == 0 else (_empty(need, torch.uint8, device, stream), need)
     if t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     return t, t.numel() * t.element_size()
@@ -188,10 +201,10 @@ def ssd_attn_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal: bool =
                  prefix)
     dev = q.device
     if y is None:
-        y = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        y = _empty(q.shape, q.dtype, dev, stream)
     _dense(y, "y", q.shape, q.dtype, dev)
     if lse is True:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        lse = _empty(q.shape[:-1], torch.float32, dev, stream)
     elif lse is False:
         lse = None
     _dense(lse, "lse", q.shape[:-1], torch.float32, dev)
@@ -222,13 +235,14 @@ def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, c
         want_dtable = table is not None
     if want_dtable and table is None:
         raise ValueError("dtable needs a table")
-    out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev), dk=torch.empty(k.shape, dtype=q.dtype, device=dev),
-               dv=torch.empty(v.shape, dtype=q.dtype, device=dev))
+    out = {"d" + n: _empty(t.shape, q.dtype, dev, stream) for n, t in (("q", q), ("k", k), ("v", v))}
     if want_dtable:
-        # (no sequence: no launch writes it)
-        out["dtable"] = (torch.empty if dims.nseq else torch.zeros)(table.shape, dtype=torch.float32, device=dev)
+        out["dtable"] = _empty(table.shape, torch.float32, dev, stream)
+        if dims.nseq == 0:  # (no launch writes it)
+            with torch.cuda.stream(stream):
+                out["dtable"].zero_()
     need = ssd_attn_backward_workspace_bytes(dims, want_dtable)
-    workspace, ws_bytes = _workspace(workspace, need, dev)
+    workspace, ws_bytes = _workspace(workspace, need, dev, stream)
     _on_stream(stream, workspace, *out.values())
     _call("ssd_attn_backward", dev, stream, ctypes.byref(dims), _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(prefix),
           _addr(q), _addr(k), _addr(v), _addr(slopes), _addr(table), _addr(y), _addr(lse), _addr(dy), _addr(out["dq"]),
@@ -277,10 +291,10 @@ def ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
     if dims.nseq != nseq or dims.headdim != D:
         raise ValueError("q %s does not fit %d sequences of head dim %d" % (tuple(q.shape), dims.nseq, dims.headdim))
     if y is None:
-        y = torch.empty((nseq, H, D), dtype=q.dtype, device=dev)
+        y = _empty((nseq, H, D), q.dtype, dev, stream)
     _dense(y, "y", (nseq, H, D), q.dtype, dev)
     need = ssd_attn_decode_workspace_bytes(dims)
-    workspace, ws_bytes = _workspace(workspace, need, dev)
+    workspace, ws_bytes = _workspace(workspace, need, dev, stream)
     _on_stream(stream, y, workspace)
     _call("ssd_attn_decode", dev, stream, ctypes.byref(dims), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table),
           _addr(seq_lens), _addr(slopes), _addr(table), _addr(y), _addr(workspace), ws_bytes)
@@ -315,7 +329,7 @@ def ssd_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None
             raise ValueError("q_out needs q")
     else:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _empty(q.shape, q.dtype, dev, stream)
         _dense(q_out, "q_out", q.shape, q.dtype, dev)
     _on_stream(stream, q_out)
     _call("ssd_kv_append", dev, stream, ctypes.byref(dims), tokens, _addr(cu_seqlens), _addr(seq_lens), _addr(block_table),
