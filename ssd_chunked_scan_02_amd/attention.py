@@ -208,7 +208,7 @@ def ssd_attn_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal: bool =
     elif lse is False:
         lse = None
     _dense(lse, "lse", q.shape[:-1], torch.float32, dev)
-    _on_stream(stream, y, lse)
+    _on_stream(stream, q, k, v, cu_seqlens, cu_seqlens_k, prefix, slopes, table, y, lse)
     _call("ssd_attn_forward", dev, stream, ctypes.byref(dims), _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(prefix),
           _addr(q), _addr(k), _addr(v), _addr(slopes), _addr(table), _addr(y), _addr(lse))
     return y, lse
@@ -243,7 +243,7 @@ def ssd_attn_backward(q, k, v, y, lse, dy, cu_seqlens=None, cu_seqlens_k=None, c
                 out["dtable"].zero_()
     need = ssd_attn_backward_workspace_bytes(dims, want_dtable)
     workspace, ws_bytes = _workspace(workspace, need, dev, stream)
-    _on_stream(stream, workspace, *out.values())
+    _on_stream(stream, q, k, v, cu_seqlens, cu_seqlens_k, prefix, slopes, table, y, lse, dy, workspace, *out.values())
     _call("ssd_attn_backward", dev, stream, ctypes.byref(dims), _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(prefix),
           _addr(q), _addr(k), _addr(v), _addr(slopes), _addr(table), _addr(y), _addr(lse), _addr(dy), _addr(out["dq"]),
           _addr(out["dk"]), _addr(out["dv"]), _addr(out.get("dtable")), _addr(workspace), ws_bytes)
@@ -295,7 +295,7 @@ def ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
     _dense(y, "y", (nseq, H, D), q.dtype, dev)
     need = ssd_attn_decode_workspace_bytes(dims)
     workspace, ws_bytes = _workspace(workspace, need, dev, stream)
-    _on_stream(stream, y, workspace)
+    _on_stream(stream, q, k_cache, v_cache, block_table, seq_lens, slopes, table, y, workspace)
     _call("ssd_attn_decode", dev, stream, ctypes.byref(dims), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table),
           _addr(seq_lens), _addr(slopes), _addr(table), _addr(y), _addr(workspace), ws_bytes)
     return y
@@ -331,7 +331,7 @@ def ssd_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None
         if q_out is None:
             q_out = _empty(q.shape, q.dtype, dev, stream)
         _dense(q_out, "q_out", q.shape, q.dtype, dev)
-    _on_stream(stream, q_out)
+    _on_stream(stream, k, v, q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, inv_freq, q_out)
     _call("ssd_kv_append", dev, stream, ctypes.byref(dims), tokens, _addr(cu_seqlens), _addr(seq_lens), _addr(block_table),
           _addr(k), _addr(v), _addr(q), _addr(inv_freq), 0 if inv_freq is None else inv_freq.numel(), int(bool(interleaved)),
           _addr(k_cache), _addr(v_cache), _addr(q_out))

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import ssd_chunked_scan_02_amd as ssd
+from ssd_chunked_scan_02_amd import attention
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,34 @@ def test_outputs_of_a_call_on_a_stream_are_that_streams_memory():
     y, _ = ssd.ssd_attn_forward(q, q, q, cu, stream=s)
     torch.cuda.synchronize()
     assert y.data_ptr() == place and torch.equal(y, want)
+
+
+def test_inputs_of_a_call_on_a_stream_are_known_to_the_allocator(monkeypatch):
+    """Every tensor that a call on a given stream reads or writes is recorded there, so that a caller who drops an
+    input right after the call does not get its memory back while the kernels still read it."""
+    seen = []
+    monkeypatch.setattr(attention, "_on_stream", lambda s, *t: seen.extend((s, x.data_ptr()) for x in t if x is not None))
+    n, H, Hk, D, s = 40, 4, 2, 64, torch.cuda.Stream()
+    r = lambda *shape: torch.randn(shape, device="cuda")  # noqa: E731
+    i64 = lambda *x: torch.tensor(x, dtype=torch.int64, device="cuda")  # noqa: E731
+    q, k, v, dy, slopes, table = r(n, H, D), r(n, Hk, D), r(n, Hk, D), r(n, H, D), r(H), r(16, H)
+    cu, cu_k, prefix, cu_new = i64(0, 15, n), i64(0, 20, n), i64(3, 0), i64(0, 3, 5)
+    kc, vc, inv, lens = r(4, 16, Hk, D), r(4, 16, Hk, D), r(16), i64(30, 9)
+    pages = torch.tensor([[0, 1], [2, -1]], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+
+    def check(*tensors):
+        torch.cuda.synchronize()
+        assert {(s, t.data_ptr()) for t in tensors} <= set(seen)
+        seen.clear()
+
+    y, lse = ssd.ssd_attn_forward(q, k, v, cu, cu_k, slopes=slopes, prefix=prefix, lse=True, stream=s)
+    check(q, k, v, cu, cu_k, slopes, prefix, y, lse)
+    y, lse = ssd.ssd_attn_forward(q, k, v, cu, cu_k, table=table, prefix=prefix, lse=True, stream=s)
+    check(q, k, v, cu, cu_k, table, prefix, y, lse)
+    got = ssd.ssd_attn_backward(q, k, v, y, lse, dy, cu, cu_k, table=table, prefix=prefix, stream=s)
+    check(q, k, v, y, lse, dy, cu, cu_k, table, prefix, *got.values())
+    q_out = ssd.ssd_kv_append(k[:5], v[:5], kc, vc, pages, lens, cu_new, inv, q=q[:5], stream=s)
+    check(k, v, q, kc, vc, pages, lens, cu_new, inv, q_out)
+    y = ssd.ssd_attn_decode(q[:2], kc, vc, pages, lens, table=table, stream=s)
+    check(q, kc, vc, pages, lens, table, y)
