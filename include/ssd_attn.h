@@ -29,8 +29,8 @@
  * Layouts: q, y [total_q, H, D], k, v [total_k, Hk, D]; one token's heads are dense, and q, k, v may be
  * views of wider rows (a fused projection's output) with a token stride of their own.  Everything else
  * is dense.  slopes, table and lse are fp32 whatever the dtype.
- * Outputs must not overlap inputs; a call whose output or workspace is an input's very pointer is refused
- * (SSD_ERR_INVALID).
+ * Outputs and the workspace must not overlap inputs or each other; a call where one of them is the very pointer of
+ * an input (offsets, lengths and tables among them) or of another output is refused (SSD_ERR_INVALID).
  * Non-finite inputs: y and lse of a query depend on that query and on the keys and values it sees, whatever
  * the others hold.  Gradients: an infinity or NaN may reach every gradient of its own sequence and key/value
  * head.  Inputs outside every sequence reach no output.

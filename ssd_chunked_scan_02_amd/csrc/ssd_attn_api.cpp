@@ -145,11 +145,15 @@ int fill(const ssd_attn_dims* d, const int64_t* cu_q, const int64_t* cu_k, const
     return SSD_OK;
 }
 
-// Whether an output is one of the inputs (kernels read inputs after their first stores to outputs).
+// Whether an output is one of the inputs (kernels read inputs after their first stores to outputs) or another output.
 template <size_t N, size_t M> bool shared(const void* const (&outputs)[N], const void* const (&inputs)[M]) {
-    for (const void* o : outputs)
+    for (size_t o = 0; o < N; ++o) {
+        if (!outputs[o]) continue;
         for (const void* i : inputs)
-            if (o && o == i) return true;
+            if (outputs[o] == i) return true;
+        for (size_t i = 0; i < o; ++i)
+            if (outputs[o] == outputs[i]) return true;
+    }
     return false;
 }
 
@@ -241,7 +245,7 @@ int ssd_attn_forward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, con
     if (work && !y) return SSD_ERR_INVALID;
     if ((y && !aligned(y, 16)) || (lse && !aligned(lse, 16))) return SSD_ERR_ALIGN;
     if (!work) return SSD_OK;
-    if (shared({y, lse}, {q, k, v})) return SSD_ERR_INVALID;
+    if (shared({y, lse}, {q, k, v, slopes, table, cu_seqlens_q, cu_seqlens_k, prefix})) return SSD_ERR_INVALID;
     p.y = y;
     p.lse = lse;
     return code(ssd::launch_attn_forward(p, dims->dtype, (int)dims->headdim, bias, static_cast<hipStream_t>(stream)));
@@ -272,7 +276,8 @@ int ssd_attn_backward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q, co
     const BackwardWorkspace w = backward_workspace(dims, dtable != nullptr);
     if (p.nseq > 0 && w.total > 0 && (!workspace || workspace_bytes < w.total)) return SSD_ERR_INVALID;
     if (!queries && !keys && !dtable) return SSD_OK;
-    if (shared({dq, dk, dv, workspace}, {q, k, v, y, lse, dy})) return SSD_ERR_INVALID;
+    if (shared({dq, dk, dv, dtable, workspace}, {q, k, v, y, lse, dy, slopes, table, cu_seqlens_q, cu_seqlens_k, prefix}))
+        return SSD_ERR_INVALID;
     p.y = const_cast<void*>(y);
     p.lse = const_cast<float*>(lse);
     p.dy = dy;
@@ -318,7 +323,7 @@ int ssd_attn_decode(const ssd_attn_cache* d, const void* q, const void* k_cache,
     const DecodeWorkspace w = decode_workspace(d);
     if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return SSD_ERR_INVALID;
     if (d->nseq == 0) return SSD_OK;
-    if (shared({y, workspace}, {q, k_cache, v_cache})) return SSD_ERR_INVALID;
+    if (shared({y, workspace}, {q, k_cache, v_cache, block_table, seq_lens, slopes, table})) return SSD_ERR_INVALID;
     p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
@@ -366,7 +371,7 @@ int ssd_kv_append(const ssd_attn_cache* d, int64_t tokens, const int64_t* cu_seq
     if ((block_table && !aligned(block_table, 4)) || (seq_lens && !aligned(seq_lens, 8)) || (cu_seqlens && !aligned(cu_seqlens, 8)))
         return SSD_ERR_ALIGN;
     if (tokens == 0 || d->nseq == 0) return SSD_OK;
-    if (shared({k_cache, v_cache, q_out}, {k, v, q})) return SSD_ERR_INVALID;
+    if (shared({k_cache, v_cache, q_out}, {k, v, q, cu_seqlens, seq_lens, block_table, inv_freq})) return SSD_ERR_INVALID;
     p.q = q;
     p.k = k;
     p.v = v;

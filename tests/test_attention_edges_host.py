@@ -1,11 +1,75 @@
 """The attention layer at its edges, on a machine without a GPU: what the binding and the C entry points refuse, and
 where a call's memory comes from."""
 import contextlib
+import ctypes
+import os
 
 import pytest
 import torch
 
+import ssd_chunked_scan_02_amd as ssd
 from ssd_chunked_scan_02_amd import attention
+from ssd_chunked_scan_02_amd.attention import AttnCache, AttnDims
+
+INVALID, UNSUPPORTED = -1, -2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ssd.library_path()):
+        from ssd_chunked_scan_02_amd.build import build
+        build()
+    return ssd.load_library()
+
+
+def _dims(**kw):
+    d = dict(nseq=2, total_q=100, total_k=100, nheads=4, nkvheads=2, headdim=64, q_stride=0, k_stride=0, v_stride=0, scale=0.125,
+             softcap=0.0, dtype=1, causal=1, num_buckets=32, max_distance=128, bidirectional=0)
+    d.update(kw)
+    return AttnDims(**d)
+
+
+def _cache(**kw):
+    d = dict(nseq=3, nheads=8, nkvheads=2, headdim=64, num_pages=10, page_size=16, max_pages=4, q_stride=0, k_stride=0, v_stride=0,
+             scale=0.125, softcap=0.0, dtype=1, num_buckets=32, max_distance=128, bidirectional=0)
+    d.update(kw)
+    return AttnCache(**d)
+
+
+# The four entry points: arguments in the call's order, those that are inputs, and those that are written.
+ENTRIES = {
+    "ssd_attn_forward": ("cu_q cu_k prefix q k v slopes table y lse", "y lse"),
+    "ssd_attn_backward": ("cu_q cu_k prefix q k v slopes table y lse dy dq dk dv dtable ws", "dq dk dv dtable ws"),
+    "ssd_attn_decode": ("q kc vc bt sl slopes table y ws", "y ws"),
+    "ssd_kv_append": ("cu sl bt k v q inv kc vc qo", "kc vc qo"),
+}
+
+
+def _entry(lib, name, at, dims=None):
+    """The entry point's status, its pointers taken from ``at`` by name."""
+    a = [at.get(n) for n in ENTRIES[name][0].split()]
+    if name == "ssd_attn_backward" or name == "ssd_attn_decode":
+        a.append(1 << 40)
+    if name == "ssd_kv_append":
+        a = [3] + a[:7] + [8, 0] + a[7:]
+    d = dims if dims is not None else _dims() if name in ("ssd_attn_forward", "ssd_attn_backward") else _cache()
+    return getattr(lib, name)(ctypes.byref(d), *a, None)
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+@pytest.mark.parametrize("bias", ["slopes", "table"])
+def test_outputs_and_workspace_are_nobody_elses(lib, name, bias):
+    """Every output and workspace that is the pointer of any input, or of another output, is refused.  (Addresses that
+    nothing follows: no call of this test may pass its checks.)"""
+    every, written = (x.split() for x in ENTRIES[name])
+    at = {n: (1 << 20) + 4096 * i for i, n in enumerate(every)}
+    at[{"slopes": "table", "table": "slopes"}[bias]] = None
+    if bias == "slopes":
+        at["dtable"] = None
+    pairs = [(o, x) for o in written for x in every if x != o and at.get(o) and at.get(x)]
+    assert len(pairs) >= len(written)
+    for o, x in pairs:
+        assert _entry(lib, name, dict(at, **{o: at[x]})) == INVALID, (o, x)
 
 
 class _Stream:
