@@ -31,6 +31,9 @@
  * is dense.  slopes, table and lse are fp32 whatever the dtype.
  * Outputs and the workspace must not overlap inputs or each other; a call where one of them is the very pointer of
  * an input (offsets, lengths and tables among them) or of another output is refused (SSD_ERR_INVALID).
+ * Sizes: a launch holds under 2^24 workgroups (2^23 in the backward pass of 128-wide bf16 heads), one for each sequence
+ * and each further 128 of its queries or keys, of each head (in forward and decode of each group of heads, where they share
+ * keys); calls past that are SSD_ERR_UNSUPPORTED.  Tokens to append are not limited by it.
  * Non-finite inputs: y and lse of a query depend on that query and on the keys and values it sees, whatever
  * the others hold.  Gradients: an infinity or NaN may reach every gradient of its own sequence and key/value
  * head.  Inputs outside every sequence reach no output.

@@ -292,6 +292,7 @@ int launch_fwd(AttnParams p, hipStream_t stream) {
     set_each(p, split ? kOwn<true> : kOwn<false>, 1);
     const int64_t grid = (int64_t)p.q_slots * units;
     if (grid == 0) return 0;
+    if (!launchable(grid, kThreads)) return -2;
     if (split) hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAPPED, BIAS, true>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
     else hipLaunchKernelGGL((attn_fwd_kernel<T, D, CAPPED, BIAS, false>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;

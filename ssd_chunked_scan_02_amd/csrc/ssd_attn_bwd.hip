@@ -811,6 +811,11 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
     d.pack = query_pack(p, BIAS);
     const bool dq_split = dq_fits && query_slots(d, kOwn<false>) * (d.H / d.pack) < attn_split_below(Tile<T, D>::RB);
     const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < attn_split_below(Tile<T, D>::RB);
+    constexpr int WHOLE = sizeof(T) == 2 && D == 128 ? kPaired : kAlone;
+    // (a split kernel has few workgroups)
+    if ((!dq_split && !launchable(query_slots(d, kOwn<false>) * (d.H / d.pack), kThreads)) ||
+        (!dkv_split && !launchable(attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk, WHOLE == kPaired ? 2 * kThreads : kThreads)))
+        return -2;
     d.plan_q = d.plan_k = nullptr;
     AttnParams with_plan = p;
     with_plan.pack = d.pack;
@@ -820,7 +825,6 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
         if (!dq_split) d.plan_q = p.plan_q;
         if (!dkv_split) d.plan_k = p.plan_k;
     }
-    constexpr int WHOLE = sizeof(T) == 2 && D == 128 ? kPaired : kAlone;
     int rc = dq_split ? launch_dq<T, D, CAP, BIAS, true>(d, stream) : launch_dq<T, D, CAP, BIAS, false>(d, stream);
     if (rc == 0) rc = dkv_split ? launch_dkv<T, D, CAP, BIAS, kSplit>(d, stream) : launch_dkv<T, D, CAP, BIAS, WHOLE>(d, stream);
     return rc;

@@ -34,6 +34,8 @@ struct AttnBuckets {
 //     128 wide, 4096 tokens  128: 51 / 52 / 68 against 82 / 114 / 143,          256: 93 / 97 / 127 against 84 / 119 / 148
 //     128 wide, 1024 tokens  128: 23 / 25 / 29 against 26 / 35 / 43,            256: 44 / 48 / 56 against 28 / 39 / 46
 inline int64_t attn_split_below(int row_bytes) { return row_bytes >= 256 ? 256 : 384; }
+// HIP counts the threads of a launch in 32 bits; calls past that are refused before their first launch.
+inline bool launchable(int64_t groups, int threads) { return groups * threads < ((int64_t)1 << 32); }
 // Tiles of a packed axis, at most: its whole tiles, and one more for each sequence.
 inline int64_t attn_slots(const int64_t* cu, int64_t total, int64_t nseq, int own) {
     if (nseq == 0) return 0;

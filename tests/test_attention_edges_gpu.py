@@ -62,3 +62,26 @@ def test_inputs_of_a_call_on_a_stream_are_known_to_the_allocator(monkeypatch):
     check(k, v, q, kc, vc, pages, lens, cu_new, inv, q_out)
     y = ssd.ssd_attn_decode(q[:2], kc, vc, pages, lens, table=table, stream=s)
     check(q, kc, vc, pages, lens, table, y)
+
+
+def test_append_more_tokens_than_a_launch_has_workgroups():
+    """2^24 tokens and some: each in its place, and its first pair rotated by its own position."""
+    n, page, D = (1 << 24) + 37, 16, 32
+    pages = -(-n // page)
+    k = torch.randn((n, 1, D), device="cuda").bfloat16()
+    table = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    kc, vc = (torch.zeros((pages, page, 1, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    seq, cu = (torch.tensor(x, dtype=torch.int64, device="cuda") for x in ([n], [0, n]))
+    inv = torch.zeros(8, device="cuda")
+    inv[0] = 1.0
+    ssd.ssd_kv_append(k, k, kc, vc, table, seq, cu, inv)
+    torch.cuda.synchronize()
+    assert torch.equal(vc.flip(0).flatten(0, 1)[:n], k)
+    got = kc.flip(0).flatten(0, 1)[:n, 0]
+    keep = [i for i in range(D) if i not in (0, 8)]
+    assert torch.equal(got[:, keep], k[:, 0, keep])
+    angle = torch.arange(n, device="cuda").double()
+    a, b = k[:, 0, 0].double(), k[:, 0, 8].double()
+    for have, want in ((got[:, 0], a * angle.cos() - b * angle.sin()), (got[:, 8], b * angle.cos() + a * angle.sin())):
+        # one rounding to bf16, and in fp32 the sine and cosine and two products: 12 u (|a| + |b|)
+        assert torch.all((have.double() - want).abs() <= 1.05 * 2.0 ** -8 * want.abs() + 12 * 2.0 ** -24 * (a.abs() + b.abs()))

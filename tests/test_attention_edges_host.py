@@ -105,3 +105,21 @@ def test_a_stream_of_another_device_is_refused():
         attention._empty((2,), torch.float32, torch.device("cuda", 0), _Stream("cuda:1"))
     with pytest.raises(ValueError, match="stream"):
         attention._call("ssd_attn_forward", torch.device("cuda", 0), _Stream("cuda:1"))
+
+
+SENTENCES = dict(nseq=1 << 20, total_q=1 << 20, total_k=1 << 20, nheads=16, nkvheads=16)  # one token each: 2^24 workgroups and more
+
+
+def test_more_workgroups_than_a_launch_holds(lib):
+    """Refused before the first launch, the backward pass's second kernel included."""
+    def at(name):
+        a = {n: (1 << 20) + 4096 * i for i, n in enumerate(ENTRIES[name][0].split())}
+        return dict(a, slopes=None, table=None, dtable=None, prefix=None)
+
+    assert _entry(lib, "ssd_attn_forward", at("ssd_attn_forward"), _dims(**SENTENCES)) == UNSUPPORTED
+    assert _entry(lib, "ssd_attn_backward", at("ssd_attn_backward"), _dims(**SENTENCES)) == UNSUPPORTED
+    # eight waves a workgroup: half as many
+    half = _dims(**dict(SENTENCES, nseq=1 << 19, headdim=128))
+    assert _entry(lib, "ssd_attn_backward", at("ssd_attn_backward"), half) == UNSUPPORTED
+    cache = _cache(nseq=1 << 20, nheads=16, nkvheads=16)
+    assert _entry(lib, "ssd_attn_decode", at("ssd_attn_decode"), cache) == UNSUPPORTED
