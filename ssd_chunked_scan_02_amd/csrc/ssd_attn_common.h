@@ -374,42 +374,52 @@ struct Score {
         none = raw && capped ? -1e15f : raw && s < 0.f ? INFINITY : -INFINITY;
         small = capped ? 0.0625f / (u * u) : 0.f;
     }
-    // The capped scores of N products, in place.  bf16: the series of tanh where all of the wave's arguments
-    // are within 1/4 (its next term, 62/2835 u^9, is under 1e-7 there): 5 full-rate operations a score;
-    // otherwise tanh u = 1 - 2 / (1 + e^2u) from the hardware's exp2 and reciprocal (off by some 1e-7),
-    // which the unit for them takes 8 times as long for.  fp32: the math library's.
-    template <typename T, int N> __device__ __forceinline__ void capped(f32x16 (&s)[N]) const {
+    // tanh by its series, for arguments within 1/4 (the next term, 62/2835 u^9, is under 4e-7 of u there): 5 full-rate
+    // operations.
+    __device__ __forceinline__ float series(float x) const {
+#pragma clang fp contract(off)
+        const float q = x * x;
+        return x * __builtin_fmaf(q, __builtin_fmaf(q, __builtin_fmaf(q, k[3], k[2]), k[1]), k[0]);
+    }
+    // tanh u = 1 - 2 / (1 + e^2u) from the hardware's exp2 and reciprocal, which the unit for them takes 8 times as long
+    // for.  It is off by some 1e-7 of the cap, whatever u: for arguments past 1/4 only.
+    __device__ __forceinline__ float saturating(float x) const {
+#pragma clang fp contract(off)
+        return __builtin_fmaf(-2.f * c2, __builtin_amdgcn_rcpf(1.f + exp2_hw(x * a)), c2);
+    }
+    // The capped scores of N vectors of products, in place.  bf16: each by the form for its own argument, so that a score
+    // does not depend on the others; a wave whose arguments are all small leaves the other form out.  fp32: the math
+    // library's tanh.
+    template <typename T, typename V, int N> __device__ __forceinline__ void capped(V (&s)[N]) const {
+        constexpr int L = sizeof(V) / 4;
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[n][r] = c2 * tanhf(s[n][r] * a);
+                for (int r = 0; r < L; ++r) s[n][r] = c2 * tanhf(s[n][r] * a);
         } else {
             float most = 0.f;
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(s[n][r]));
+                for (int r = 0; r < L; ++r) most = fmaxf(most, fabsf(s[n][r]));
             if (__all(most * most <= small)) {
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float x = s[n][r], q = x * x;
-                        s[n][r] = x * (k[0] + q * (k[1] + q * (k[2] + q * k[3])));
-                    }
+                    for (int r = 0; r < L; ++r) s[n][r] = series(s[n][r]);
             } else {
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[n][r] = c2 - 2.f * c2 * __builtin_amdgcn_rcpf(1.f + exp2_hw(s[n][r] * a));
+                    for (int r = 0; r < L; ++r) {
+                        float x = s[n][r];
+                        x = x * x <= small ? series(x) : saturating(x);
+                        asm volatile("" : "+v"(x));  // (one after the other: side by side they cost the tile loop a wave a SIMD)
+                        s[n][r] = x;
+                    }
             }
         }
-    }
-    template <typename T> __device__ __forceinline__ float capped(float x) const {
-        if constexpr (sizeof(T) == 4) return c2 * tanhf(x * a);
-        else return c2 - 2.f * c2 * __builtin_amdgcn_rcpf(1.f + exp2_hw(x * a));
     }
     // derivative of the cap at a capped score
     __device__ __forceinline__ float slope(float s) const {

@@ -153,13 +153,13 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) attn_decode_
         const int key0 = b * kBlock + 4 * g;
         const bool all_far = len - 1 - (b * kBlock + kBlock - 1) >= md;
         float mx = -INFINITY;
+        if constexpr (CAP) sc.template capped<T>(sv);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int key = key0 + 16 * n + r;
-                float x = sv[n][r];
-                x = CAP ? sc.template capped<T>(x) : x * sc.a;
+                float x = CAP ? sv[n][r] : sv[n][r] * sc.a;
                 if constexpr (BIAS == kBiasSlopes) x -= slope2 * (float)(len - 1 - key);
                 if constexpr (BIAS == kBiasBuckets) x += all_far ? far : bias[bucket[min(max(len - 1 - key, 0), md)] + col];
                 x = key < len && (here >> n & 1) ? x : -INFINITY;

@@ -1,11 +1,16 @@
 """The attention layer at its edges, on the GPU: calls that the documentation allows and an ordinary run does not make."""
+import numpy as np
 import pytest
 import torch
 
 import ssd_chunked_scan_02_amd as ssd
+from attn_helpers import U, f64, make, offsets, reference, within
 from ssd_chunked_scan_02_amd import attention
 
 pytestmark = pytest.mark.gpu
+
+# few heads: the waves of a workgroup share rows; many: each has its own
+HEADS = {"few": (4, 2), "many": (44, 44)}
 
 
 def test_outputs_of_a_call_on_a_stream_are_that_streams_memory():
@@ -85,3 +90,67 @@ def test_append_more_tokens_than_a_launch_has_workgroups():
     for have, want in ((got[:, 0], a * angle.cos() - b * angle.sin()), (got[:, 8], b * angle.cos() + a * angle.sin())):
         # one rounding to bf16, and in fp32 the sine and cosine and two products: 12 u (|a| + |b|)
         assert torch.all((have.double() - want).abs() <= 1.05 * 2.0 ** -8 * want.abs() + 12 * 2.0 ** -24 * (a.abs() + b.abs()))
+
+
+def _capped_bound(ref, dtype, D, n):
+    """y_bound of attn_helpers with a score's error that does not grow with the cap.  bf16: tanh's series (arguments
+    within 1/4) is off by 3.3e-7 = 5.6 u of its argument and some roundings, the other form by 1.3e-7 (exp2, reciprocal
+    and the subtraction, half a step of 1 each and one more) of a tanh over 0.24, 9 u of the score: 16 u of |z|, which
+    is at most the sum of its terms' magnitudes.  fp32: the math library's tanh, a few u."""
+    es = ((D + 32) * ref["s_abs"] * 2.0 ** -24)[..., None]
+    soft = U[dtype] * ((ref["y_abs"] if dtype == "bf16" else 0) + np.abs(ref["y"]))
+    return 1.1 * (soft + (2 * es + (n + 16) * 2.0 ** -24) * ref["y_abs"]) + 1e-30
+
+
+CAPS = [0.5, 30.0, 500.0, 1e4, 1e6, 1e9]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cap", CAPS)
+def test_caps_of_any_size_in_a_decode_step(cap, dtype):
+    """A cap far above the scores is no cap; the sequences are long enough for their weights to tell."""
+    H, Hk, D, page, lens = 8, 2, 64, 16, [900, 17, 1]
+    total, n = [-(-x // page) for x in lens], len(lens)
+    d = make(21, n, sum(total) * page, H, Hk, D, dtype, spread=1.5)
+    table = torch.full((n, max(total)), -1, dtype=torch.int32)
+    rows, at = [], 0
+    for i, (pages, length) in enumerate(zip(total, lens)):
+        table[i, :pages] = torch.arange(at, at + pages)
+        rows.append(torch.arange(at * page, at * page + length))
+        at += pages
+    kc, vc = (d[x].unflatten(0, (at, page)).contiguous().cuda() for x in "kv")
+    y = ssd.ssd_attn_decode(d["q"].cuda(), kc, vc, table.cuda(), torch.tensor(lens, dtype=torch.int64).cuda(), softcap=cap)
+    torch.cuda.synchronize()
+    d["k"], d["v"] = d["k"][torch.cat(rows)], d["v"][torch.cat(rows)]
+    ref = reference(d, cu=list(range(n + 1)), cu_k=offsets(lens).numpy(), cap=cap)
+    within(f64(y), ref["y"], _capped_bound(ref, dtype, D, max(lens)), "decode cap %g %s" % (cap, dtype))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cap", CAPS)
+def test_caps_of_any_size_in_a_prompt(cap, dtype, heads):
+    H, Hk = HEADS[heads]
+    d = make(22, 300, 300, H, Hk, 64, dtype, spread=1.5)
+    cu = offsets([300])
+    y, _ = ssd.ssd_attn_forward(*(d[x].cuda() for x in "qkv"), cu.cuda(), softcap=cap)
+    torch.cuda.synchronize()
+    keep = slice(0, 4)
+    one = dict(d, q=d["q"][:, keep], k=d["k"][:, :4 * Hk // H], v=d["v"][:, :4 * Hk // H])
+    ref = reference(one, cu=cu.numpy(), cap=cap)
+    within(f64(y)[:, keep], ref["y"], _capped_bound(ref, dtype, 64, 300), "prompt cap %g %s" % (cap, dtype))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("cap", [5.0, 50.0])
+def test_hidden_keys_do_not_choose_the_form_of_the_cap(cap, heads):
+    """Keys that a row does not see, however large, leave its capped scores' bits as they were."""
+    H, Hk = HEADS[heads]
+    d = make(23, 300, 300, H, Hk, 64, "bf16")
+    q, k, v, cu = (x.cuda() for x in (d["q"], d["k"], d["v"], offsets([300])))
+    y, lse = ssd.ssd_attn_forward(q, k, v, cu, softcap=cap, lse=True)
+    k[200:] *= 1000
+    k[250] = float("inf")
+    y2, lse2 = ssd.ssd_attn_forward(q, k, v, cu, softcap=cap, lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:200], y2[:200]) and torch.equal(lse[:200], lse2[:200])
