@@ -167,7 +167,8 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
                 mx = fmaxf(mx, other_half(mx));
                 if constexpr (RAW) mx *= sc.a;
                 if (__any(mx > m + kLazy)) {
-                    const float next = fmaxf(m, mx), keep = exp2_hw(m - next);
+                    // (each row by its own growth, so that its weights' rounding does not depend on the others)
+                    const float next = mx > m + kLazy ? mx : m, keep = exp2_hw(m - next);
                     m = next;
                     l *= keep;
                     lr *= keep;

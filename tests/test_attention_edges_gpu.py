@@ -154,3 +154,19 @@ def test_hidden_keys_do_not_choose_the_form_of_the_cap(cap, heads):
     y2, lse2 = ssd.ssd_attn_forward(q, k, v, cu, softcap=cap, lse=True)
     torch.cuda.synchronize()
     assert torch.equal(y[:200], y2[:200]) and torch.equal(lse[:200], lse2[:200])
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_a_row_does_not_depend_on_its_neighbours(dtype, D, heads):
+    """Queries of the same tile whose maxima grow along the keys leave the other rows' bits as they were."""
+    H, Hk = HEADS[heads]
+    d = make(24, 300, 300, H, Hk, D, dtype)
+    q, k, v, cu = (x.cuda() for x in (d["q"], d["k"], d["v"], offsets([300])))
+    y, lse = ssd.ssd_attn_forward(q, k, v, cu, lse=True)
+    loud = torch.arange(300, device="cuda") % 7 == 3
+    q[loud] *= 40
+    y2, lse2 = ssd.ssd_attn_forward(q, k, v, cu, lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y[~loud], y2[~loud]) and torch.equal(lse[~loud], lse2[~loud])
+    assert not torch.equal(y[loud], y2[loud])
