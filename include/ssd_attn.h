@@ -58,7 +58,7 @@ typedef struct {
     int64_t k_stride;      /* 16 bytes, at least the token's own elements, under 2^24.  Likewise k, v */
     int64_t v_stride;      /* (dense: Hk D).  H D itself is under 2^24 */
     float scale;           /* of q . k: finite */
-    float softcap;         /* 0: none; else positive and finite */
+    float softcap;         /* 0: none; else positive and finite (taken as 2^-56 below that, as 2^96 above) */
     int32_t dtype;         /* ssd_dtype of q, k, v, y and their gradients */
     int32_t causal;        /* 0 or 1 */
     int32_t num_buckets;   /* with a table: 2 .. 64 (bidirectional: 4 .. 128, even), otherwise ignored */

@@ -85,6 +85,12 @@ int check_shape(int64_t H, int64_t Hk, int64_t D, int32_t dtype) {
     return SSD_OK;
 }
 
+// The cap as the kernels take it, within [2^-56, 2^96], where their 1 / cap^2 and cap log2 e are finite.  Scores under a
+// cap of 2^-56 are zero to the last bit of an fp32 weight, and 2^96 caps none that fp32 products of use reach.
+float take_cap(float cap) {
+    return cap > 0.f ? std::fmin(std::fmax(cap, 0x1p-56f), 0x1p96f) : 0.f;
+}
+
 int check_stride(int64_t given, int64_t dense, int64_t elem, int64_t& out) {
     if (given == 0) {
         out = dense;
@@ -141,7 +147,7 @@ int fill(const ssd_attn_dims* d, const int64_t* cu_q, const int64_t* cu_k, const
     p.Hk = (int)d->nkvheads;
     p.causal = d->causal;
     p.scale = d->scale;
-    p.cap = d->softcap;
+    p.cap = take_cap(d->softcap);
     return SSD_OK;
 }
 
@@ -341,7 +347,7 @@ int ssd_attn_decode(const ssd_attn_cache* d, const void* q, const void* k_cache,
     p.page_size = (int)d->page_size;
     p.max_pages = (int)d->max_pages;
     p.scale = d->scale;
-    p.cap = d->softcap;
+    p.cap = take_cap(d->softcap);
     const int bias = table ? ssd::kBiasBuckets : slopes ? ssd::kBiasSlopes : ssd::kBiasNone;
     return code(ssd::launch_attn_decode(p, d->dtype, (int)d->headdim, bias, static_cast<hipStream_t>(stream)));
 }

@@ -366,13 +366,17 @@ struct Score {
         const float s = fabsf(scale) < 1e-30f ? 1e-30f : scale, u = capped ? s / cap : 0.f;
         c2 = cap * kLog2e;
         rc2 = capped ? 1.f / c2 : 0.f;
-        a = !capped ? s * kLog2e : sizeof(T) == 4 ? u : 2.f * u * kLog2e;
-        k[0] = c2 * u;
+        // (finite, so that a product of zero is a score of zero)
+        a = !capped ? s * kLog2e : fminf(fmaxf(sizeof(T) == 4 ? u : 2.f * u * kLog2e, -3e38f), 3e38f);
+        k[0] = s * kLog2e;
         k[1] = k[0] * u * u * (-1.f / 3.f);
         k[2] = k[0] * (u * u) * (u * u) * (2.f / 15.f);
         k[3] = k[0] * (u * u) * (u * u) * (u * u) * (-17.f / 315.f);
-        none = raw && capped ? -1e15f : raw && s < 0.f ? INFINITY : -INFINITY;
-        small = capped ? 0.0625f / (u * u) : 0.f;
+        // (capped: lse is at least -c2, so that its weight, under 2^-160, is zero; and (160 / c2)^2 is finite from caps
+        // of 2^-56 on)
+        none = raw && capped ? -2.f * c2 - 160.f : raw && s < 0.f ? INFINITY : -INFINITY;
+        // (a cap so far below the scale that the series' factors overflow: the other form, off by 1e-7 of that cap)
+        small = capped && fabsf(k[3]) < 1e38f ? 0.0625f / (u * u) : -1.f;
     }
     // tanh by its series, for arguments within 1/4 (the next term, 62/2835 u^9, is under 4e-7 of u there): 5 full-rate
     // operations.

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import ssd_chunked_scan_02_amd as ssd
-from attn_helpers import U, f64, make, offsets, reference, within
+from attn_helpers import U, f64, grad_bounds, make, offsets, reference, within
 from ssd_chunked_scan_02_amd import attention
 
 pytestmark = pytest.mark.gpu
@@ -170,3 +170,60 @@ def test_a_row_does_not_depend_on_its_neighbours(dtype, D, heads):
     torch.cuda.synchronize()
     assert torch.equal(y[~loud], y2[~loud]) and torch.equal(lse[~loud], lse2[~loud])
     assert not torch.equal(y[loud], y2[loud])
+
+
+def _slope_error(d, cap, D):
+    """What errors of the cap's derivative c1 = 1 - tanh^2(z / cap) leave in dq and dk of one causal document.
+    z is off by (D + 32) u sum_d |q_d k_d| scale: c1, which falls with |z|, by its change over that, which is all of it
+    where the cap is under z's error.  Formed from a t off by 6 u (the capped score 4 u, 1 / cap and the product one
+    each), c1 is off by 12 u more: 16 u.  It multiplies dS with its own error (y's rounding and fp32's, all that dS is
+    in a row of one key): within p (A + sum p A), A = |dy| . |v|."""
+    q, k, v, dy = (f64(d[x]).transpose(1, 0, 2) for x in ("q", "k", "v", "dy"))
+    group, n, u, scale = len(q) // len(k), q.shape[1], 2.0 ** -24, D ** -0.5
+    dq, dk = np.zeros_like(q), np.zeros_like(k)
+    for h in range(len(q)):
+        K, V = k[h // group], v[h // group]
+        z, off = scale * q[h] @ K.T, (D + 32) * u * scale * np.abs(q[h]) @ np.abs(K).T
+
+        def c1(x):
+            return 1 - np.tanh(np.maximum(x, 0) / cap) ** 2
+
+        e = np.maximum(c1(np.abs(z) - off) - c1(np.abs(z)), c1(np.abs(z)) - c1(np.abs(z) + off)) + 16 * u
+        p = np.where(np.tril(np.ones((n, n), bool)), np.exp(cap * np.tanh(z / cap)), 0.0)
+        p /= p.sum(-1, keepdims=True)
+        A = np.abs(dy[h]) @ np.abs(V).T
+        w = e * p * (A + (p * A).sum(-1, keepdims=True)) * scale
+        dq[h] = w @ np.abs(K)
+        dk[h // group] += w.T @ np.abs(q[h])
+    return dq.transpose(1, 0, 2), dk.transpose(1, 0, 2)
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("cap", [1e-38, 1e-20, 1e-9, 1e-6, 1e-3, 1e6, 1e16, 3e38])
+def test_gradients_under_caps_of_any_size(cap, dtype, D, heads):
+    """Forward and backward, rows of zero scores among them (a padded batch's).  A score's error does not grow with the
+    cap (_capped_bound); for the sum of its magnitudes (D + 32) u instead of grad_bounds' (D + 16) u.
+    What the cap's derivative is off by is added (_slope_error)."""
+    H, Hk = HEADS[heads]
+    n = 130
+    d = make(25, n, n, H, Hk, D, dtype, grads=True)
+    d["q"][40:75] = 0
+    d["k"][:20] = 0
+    cu = offsets([n])
+    g = {x: d[x].cuda() for x in ("q", "k", "v", "dy")}
+    y, lse = ssd.ssd_attn_forward(g["q"], g["k"], g["v"], cu.cuda(), softcap=cap, lse=True)
+    got = ssd.ssd_attn_backward(g["q"], g["k"], g["v"], y, lse, g["dy"], cu.cuda(), softcap=cap)
+    torch.cuda.synchronize()
+    hk, hq = slice(0, 2), slice(0, 2 * H // Hk)
+    d = dict(d, q=d["q"][:, hq], dy=d["dy"][:, hq], k=d["k"][:, hk], v=d["v"][:, hk])
+    label = "cap %g %s D%d " % (cap, dtype, D)
+    first = reference(d, cu=cu.numpy(), cap=cap)
+    bound = _capped_bound(first, dtype, D, n)
+    within(f64(y)[:, hq], first["y"], bound, label + "y")
+    ref = reference(d, cu=cu.numpy(), cap=cap, dy=d["dy"], y_err=bound)
+    bounds = grad_bounds(dict(ref, s_abs=ref["s_abs"] * (D + 32) / (D + 16)), dtype, D, n, 2 * H // Hk, 2, 1.0)
+    for x, more in zip(("dq", "dk"), _slope_error(d, cap, D)):
+        bounds[x] = bounds[x] + 1.1 * more
+    for x, heads_of in (("dq", hq), ("dk", hk), ("dv", hk)):
+        within(f64(got[x])[:, heads_of], ref[x], bounds[x], label + x)
