@@ -16,8 +16,9 @@
 //
 // A row's y depends on the keys that it sees, whatever lies in the others of its tile: a weight of zero does not keep
 // an infinity or NaN of V out of a product, so where one has come up under a causal mask the workgroup does its tiles
-// again with those values taken out, and rewrites the rows that see none of them (attn_fwd_rows<CAREFUL>; the vote costs 0.3 us of the 11.5 of
-// 256 tokens of one head, and nothing that 2 ms of a long prompt show).
+// again with those values taken out (attn_fwd_rows<CAREFUL>).  A row sees the keys before its limit, so that the first key
+// with a NaN, an infinity and a negative infinity in a column say what that column of the row is.  (The vote costs 0.3 us
+// of the 11.5 of 256 tokens of one head, and nothing that 2 ms of a long prompt show.)
 //
 // Measured: 16384 tokens, 32/4 heads of 128, causal, bf16: 2.13 ms, 1.03 PFLOP/s, bound by MFMA (86% of what an
 // 8192^3 matrix product reaches).  8 x 2048 tokens, 24 heads of 64, capped: 187 us, 550 TFLOP/s, bound by VALU: a
@@ -42,11 +43,11 @@ template <typename T, int D, bool SPLIT> struct FwdShared {
     static constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;  // (two buffers of split fp32 tiles of 128 would not fit)
     T *k_a, *v_a, *k_b, *v_b;
     float* lut;
-    float (*stat)[SPLIT ? kWaves * 32 : 1];  // by row: m, l, weight of a wave's share, sum of rounded weights, spoilt
-    uint32_t (*spoilt)[SPLIT ? kWaves : 1][KT];  // CAREFUL, by buffer: keys with an infinity or NaN in V
+    float (*stat)[SPLIT ? kWaves * 32 : 1];  // by row: m, l, weight of a wave's share, sum of rounded weights
+    int (*first)[D];                         // CAREFUL, by column of V: first key with a NaN, an infinity, a negative one
 };
 
-// The rows of workgroup `block`; CAREFUL: without what is infinite or NaN in V, and only the rows that see none of it.
+// The rows of workgroup `block`; CAREFUL: what is infinite or NaN in V counts for the rows that see it, and for no others.
 // Returns whether something infinite or NaN came up.
 template <typename T, int D, int CAPPED, int BIAS, bool SPLIT, bool CAREFUL>
 __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShared<T, D, SPLIT>& lds, uint32_t block, int tid) {
@@ -60,7 +61,7 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
     constexpr bool ROUNDED = sizeof(T) == 2;  // weights lose bits on their way to V
     T *const k_a = lds.k_a, *const v_a = lds.v_a, *const k_b = lds.k_b, *const v_b = lds.v_b;
     const auto stat = lds.stat;
-    const auto spoilt = lds.spoilt;
+    const auto first = lds.first;
 
     int slot, unit;
     work_item(block, p.q_slots, (uint32_t)p.H / (uint32_t)p.pack, slot, unit);
@@ -115,20 +116,26 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
     float m = NO_MAX ? 0.f : kNoMax, l = 0.f, lr = 0.f;  // this lane half's share of the weights, and of the rounded ones
     const int qpos = mine + shift;
-    bool sees_spoilt = false;
+    if constexpr (CAREFUL) {
+        for (int i = tid; i < 3 * D; i += kThreads) first[0][i] = INT_MAX;
+        __syncthreads();
+    }
+    // a column of y from its sum over what is finite in V
+    auto with_rest = [&](float x, int column, int see) {
+        const bool nan = first[0][column] < see, up = first[1][column] < see, down = first[2][column] < see;
+        return nan || (up && down) ? NAN : x != x ? x : up ? INFINITY : down ? -INFINITY : x;
+    };
 
     auto meet = [&]() {
         if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
     };
-    // what was on its way to LDS (the values: to v) is there, and (SPLIT: this wave's) reads are over
-    auto settle = [&](T* v) {
+    // what was on its way to LDS (the values of tile t: to v) is there, and (SPLIT: this wave's) reads are over
+    auto settle = [&](T* v, int t) {
         __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
         meet();
         if (CAREFUL && v) {
-            uint32_t* keys = spoilt[v == vb][SPLIT ? wave : 0];
-            if (lane < KT) keys[lane] = 0;
-            meet();
-            vf.clean(v, keys);
+            vf.clean(v, t * KT, first);
+            __builtin_amdgcn_s_waitcnt(kAllDone);
             meet();
         }
     };
@@ -136,10 +143,6 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
     auto step = [&](const T* kt, const T* vt, T* kn, T* vn, int t) {
         const int k0 = t * KT;
         if (DOUBLE && t + dt < ntiles) fetch(kn, vn, t + dt);
-        if constexpr (CAREFUL) {
-#pragma unroll 1
-            for (int j = 0; j < KT; ++j) sees_spoilt |= spoilt[vt == vb][SPLIT ? wave : 0][j] && k0 + j < my_limit;
-        }
         if (k0 < wave_most) {
             f32x16 s[NS];
 #pragma unroll
@@ -195,14 +198,14 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
                     for (int d = 0; d < DT; ++d) o[d] = O::mma(L::cols(vt, 32 * n, kk, 32 * d, z), pf, o[d]);
                 }
         }
-        settle(DOUBLE && t + dt < ntiles ? vn : nullptr);
+        settle(DOUBLE && t + dt < ntiles ? vn : nullptr, t + dt);
         if (!DOUBLE && t + dt < ntiles) {
             fetch(kn, vn, t + dt);
-            settle(vn);
+            settle(vn, t + dt);
         }
     };
     if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();  // (the bias is everybody's)
-    settle(t0 < ntiles ? va : nullptr);
+    settle(t0 < ntiles ? va : nullptr, t0);
     for (int t = t0; t < ntiles; t += 2 * dt) {
         step(ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
         if (t + dt < ntiles) step(DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);
@@ -215,7 +218,6 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
             stat[0][32 * wave + lane] = m;
             stat[1][32 * wave + lane] = l;
             stat[3][32 * wave + lane] = lr;
-            stat[4][32 * wave + lane] = sees_spoilt ? 1.f : 0.f;
         }
         __syncthreads();  // (nobody reads a tile any more)
         Join<T, D>::keep(k_a, v_a, o, lane, wave);
@@ -240,14 +242,24 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
         for (int i = tid; i < 32 * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
             if (row0 + r >= sp.rows) break;
-            if (stat[4][r] + stat[4][32 + r] + stat[4][64 + r] + stat[4][96 + r] > 0.f) continue;
-            const f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, stat[2]);
+            f32x4 v = Join<T, D>::sum(k_a, v_a, r, d4, stat[2]);
             const int q = query_of(row0 + r);
+            if constexpr (CAREFUL) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = with_rest(v[e], 4 * d4 + e, limit(q));
+            }
             store4(static_cast<T*>(p.y) + ((sp.q0 + q) * p.H + head0 + row0 + r - q * p.pack) * D + 4 * d4, v[0], v[1], v[2], v[3]);
         }
-    } else if (row < sp.rows && !sees_spoilt) {
+    } else if (row < sp.rows) {
         // (the store exchanges words between a row's two lanes, which are in or out together)
-        const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);  // (an empty row is zero; a NaN stays one)
+        float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);  // (an empty row is zero; a NaN stays one)
+        if constexpr (CAREFUL) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] = with_rest(o[d][r] * inv, 32 * d + acc_row(r) + 4 * half, my_limit);
+            inv = 1.f;
+        }
         T* yg = static_cast<T*>(p.y) + ((sp.q0 + mine) * p.H + head) * D;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -273,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     __shared__ __attribute__((aligned(16))) T k_b[S::DOUBLE ? S::ELEMS : 8];
     __shared__ __attribute__((aligned(16))) T v_b[S::DOUBLE ? S::ELEMS : 8];
     __shared__ float lut[BIAS == kBiasBuckets ? 2 * kMaxDistance + 1 : 1];
-    __shared__ float stat[SPLIT ? 5 : 1][SPLIT ? kWaves * 32 : 1];
-    __shared__ uint32_t spoilt[2][SPLIT ? kWaves : 1][S::KT];
-    const S lds{k_a, v_a, k_b, v_b, lut, stat, spoilt};
+    __shared__ float stat[SPLIT ? 4 : 1][SPLIT ? kWaves * 32 : 1];
+    __shared__ int first[3][D];
+    const S lds{k_a, v_a, k_b, v_b, lut, stat, first};
     const bool bad = attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, false>(p, lds, blockIdx.x, threadIdx.x);
     if (!p.causal || !__syncthreads_or(bad)) return;
     uint32_t block = blockIdx.x;

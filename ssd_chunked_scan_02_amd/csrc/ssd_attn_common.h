@@ -169,18 +169,20 @@ template <typename T, int D, int ROWS, int THREADS> struct Feed {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)row(i) * pitch + col(i);
     }
-    // Takes the infinities and NaN out of what this thread has loaded, and notes their rows.
-    static __device__ __forceinline__ void clean(T* s, uint32_t* rows_with) {
+    // Takes the infinities and NaN out of what this thread has loaded, rows `at` .. of the sequence, and notes for their
+    // columns the first row with a NaN, an infinity and a negative infinity.
+    static __device__ __forceinline__ void clean(T* s, int at, int (*first)[D]) {
         const int wave = (int)threadIdx.x % THREADS / kWave, lane = threadIdx.x % kWave;
 #pragma unroll 1
         for (int i = 0; i < kLoads; ++i) {
-            T* at = s + (wave * kWave + THREADS * i + lane) * L::kE;
+            T* chunk = s + (wave * kWave + THREADS * i + lane) * L::kE;
 #pragma unroll 1
-            for (int e = 0; e < L::kE; ++e)
-                if (!(fabsf((float)at[e]) < INFINITY)) {
-                    at[e] = (T)0.f;
-                    rows_with[row(i)] = 1;
-                }
+            for (int e = 0; e < L::kE; ++e) {
+                const float x = (float)chunk[e];
+                if (fabsf(x) < INFINITY) continue;
+                chunk[e] = (T)0.f;
+                atomicMin(&first[x != x ? 0 : x > 0.f ? 1 : 2][col(i) / (int)sizeof(T) + e], at + row(i));
+            }
         }
     }
     // rows 0 .. of `g`, the tensor's row `first`; `left` >= 1 rows are there

@@ -227,3 +227,47 @@ def test_gradients_under_caps_of_any_size(cap, dtype, D, heads):
         bounds[x] = bounds[x] + 1.1 * more
     for x, heads_of in (("dq", hq), ("dk", hk), ("dv", hk)):
         within(f64(got[x])[:, heads_of], ref[x], bounds[x], label + x)
+
+
+def _not_finite(v, at):
+    """v with +inf, -inf and NaN in single columns of some keys, and the same with zeros there; [(key, head, column, value)]."""
+    inf, nan = float("inf"), float("nan")
+    places = [(120, 0, 3, inf), (150, 0, 3, -inf), (64, 0, 9, -inf), (200, 0, 5, nan), (130, 0, 7, inf), (260, 0, 7, nan),
+              (0, 1, 0, inf), (299, 1, 31, -inf), (256, 1, 30, nan), (255, 1, 29, inf)]
+    with_them, without = v.clone(), v.clone()
+    for key, head, column, x in places:
+        with_them[at + key, head, column], without[at + key, head, column] = x, 0
+    return with_them, without, places
+
+
+def _with_rest(y, places, at, n, seen, group):
+    """What becomes of y (of the values without them) by the formula: a seen infinity is the column's, a seen NaN or two
+    infinities make it NaN.  seen(key): first row that sees it."""
+    y = y.clone()
+    for key, head, column, x in places:
+        rows = slice(at + seen(key), at + n)
+        y[rows, head * group:(head + 1) * group, column] += x
+    return y
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("fp32", 32), ("fp32", 64), ("fp32", 128)])
+@pytest.mark.parametrize("how", [{}, dict(prefix=140), dict(cap=50.0), dict(bias="buckets")], ids=str)
+def test_columns_of_seen_and_hidden_values_are_told_apart(dtype, D, heads, how):
+    """Infinities and NaN of V in single columns: a row has those that it sees, in their columns, and its other columns,
+    and every column of rows that see none, are as they are without them, to the bit."""
+    H, Hk = HEADS[heads]
+    lens, at, n = [33, 300, 20], 33, 300
+    d = make(26 + D, sum(lens), sum(lens), H, Hk, D, dtype, bias=how.get("bias", "none"))
+    pre = how.get("prefix", 0)
+    args = dict(softcap=how.get("cap", 0.0), table=None if d["table"] is None else d["table"].cuda(),
+                prefix=torch.tensor([0, pre, 0], dtype=torch.int64).cuda() if pre else None)
+    bad, good, places = _not_finite(d["v"], at)
+    q, k, cu = d["q"].cuda(), d["k"].cuda(), offsets(lens).cuda()
+    y0, lse0 = ssd.ssd_attn_forward(q, k, good.cuda(), cu, lse=True, **args)
+    y, lse = ssd.ssd_attn_forward(q, k, bad.cuda(), cu, lse=True, **args)
+    torch.cuda.synchronize()
+    want = _with_rest(y0, places, at, n, lambda key: 0 if key < pre else key, H // Hk)
+    assert torch.equal(lse, lse0)
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(y, 7.0, 1e30, -1e30), torch.nan_to_num(want, 7.0, 1e30, -1e30))
