@@ -15,10 +15,11 @@
 // the chip the waves split the keys instead (SPLIT).
 //
 // A row's y depends on the keys that it sees, whatever lies in the others of its tile: a weight of zero does not keep
-// an infinity or NaN of V out of a product, so where one has come up under a causal mask the workgroup does its tiles
-// again with those values taken out (attn_fwd_rows<CAREFUL>).  A row sees the keys before its limit, so that the first key
-// with a NaN, an infinity and a negative infinity in a column say what that column of the row is.  (The vote costs 0.3 us
-// of the 11.5 of 256 tokens of one head, and nothing that 2 ms of a long prompt show.)
+// an infinity or NaN of V out of a product (the copies of the last key that fill its tile have that weight, too), so
+// where one has come up the workgroup does its tiles again with those values taken out (attn_fwd_rows<CAREFUL>).  A row
+// sees the keys before its limit, so that the first key with a NaN, an infinity and a negative infinity in a column say
+// what that column of the row is.  (The vote costs 0.3 us of the 11.5 of 256 tokens of one head, and nothing that 2 ms of
+// a long prompt show.)
 //
 // Measured: 16384 tokens, 32/4 heads of 128, causal, bf16: 2.13 ms, 1.03 PFLOP/s, bound by MFMA (86% of what an
 // 8192^3 matrix product reaches).  8 x 2048 tokens, 24 heads of 64, capped: 187 us, 550 TFLOP/s, bound by VALU: a
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     __shared__ int first[3][D];
     const S lds{k_a, v_a, k_b, v_b, lut, stat, first};
     const bool bad = attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, false>(p, lds, blockIdx.x, threadIdx.x);
-    if (!p.causal || !__syncthreads_or(bad)) return;
+    if (!__syncthreads_or(bad)) return;
     uint32_t block = blockIdx.x;
     int tid = threadIdx.x;
     asm volatile("" : "+s"(block), "+v"(tid));  // (nothing worked out for the first time is kept for this one)
