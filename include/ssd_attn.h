@@ -35,8 +35,10 @@
  * and each further 128 of its queries or keys, of each head (in forward and decode of each group of heads, where they share
  * keys); calls past that are SSD_ERR_UNSUPPORTED.  Tokens to append are not limited by it.
  * Non-finite inputs: y and lse of a query depend on that query and on the keys and values it sees, whatever
- * the others hold.  Gradients: an infinity or NaN may reach every gradient of its own sequence and key/value
- * head.  Inputs outside every sequence reach no output.
+ * the others hold, to the bit.  An infinity in a value that a query of ssd_attn_forward sees is that column of its y
+ * (NaN beside one of the other sign or a NaN).  Gradients: an infinity or NaN may reach every gradient of its own sequence
+ * and key/value head.  Inputs outside every sequence reach no output.  Sums over the keys are fp32 and divided at the
+ * end: 2^8 |v| times the number of keys has to stay under 2^127.
  */
 #ifndef SSD_ATTN_H
 #define SSD_ATTN_H

@@ -33,9 +33,10 @@ namespace attn {
 namespace {
 
 constexpr float kLazy = 8.f;  // log2 growth of a maximum that is let pass without a rescale
-// Scores capped to at most 2^80 need no maximum at all: weights in [2^-80, 2^80] times 2^24 keys and any
-// sensible value stay inside fp32 (and bf16, which has its range).
-constexpr float kNoMaxNeeded = 80.f;
+// Scores capped to at most 2^80 need no maximum at all: weights in [2^-80, 2^80] and their sums stay inside fp32 (and
+// bf16, which has its range).  Where their products with V may not (a sum is infinite, or a row's weights come to less
+// than 2^-32), the workgroup does its tiles again, with a maximum for those rows (attn_fwd_rows<CAREFUL>, `track`).
+constexpr float kNoMaxNeeded = 80.f, kFewWeights = 0x1p-32f;
 enum Cap { kCapNone = 0, kCapped = 1, kCapBounds = 2 };  // kCapBounds: without a bias, by a cap that needs no maximum
 
 // LDS, in arrays of their own: a load on its way to one is not waited for at another.
@@ -49,9 +50,10 @@ template <typename T, int D, bool SPLIT> struct FwdShared {
 };
 
 // The rows of workgroup `block`; CAREFUL: what is infinite or NaN in V counts for the rows that see it, and for no others.
-// Returns whether something infinite or NaN came up.
+// Returns whether something infinite or NaN came up, or a row needs the maximum that it was done without;
+// CAREFUL: the latter, of this lane's row (SPLIT: this wave's share of it).
 template <typename T, int D, int CAPPED, int BIAS, bool SPLIT, bool CAREFUL>
-__device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShared<T, D, SPLIT>& lds, uint32_t block, int tid) {
+__device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShared<T, D, SPLIT>& lds, uint32_t block, int tid, bool track) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
@@ -115,7 +117,7 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
     f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16{};
-    float m = NO_MAX ? 0.f : kNoMax, l = 0.f, lr = 0.f;  // this lane half's share of the weights, and of the rounded ones
+    float m = NO_MAX && !(CAREFUL && track) ? 0.f : kNoMax, l = 0.f, lr = 0.f;  // this lane half's share of the weights, and of the rounded ones
     const int qpos = mine + shift;
     if constexpr (CAREFUL) {
         for (int i = tid; i < 3 * D; i += kThreads) first[0][i] = INT_MAX;
@@ -162,7 +164,7 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[n][r] = 32 * n + acc_row(r) < left ? s[n][r] : -INFINITY;
             }
-            if constexpr (!NO_MAX) {
+            if constexpr (!NO_MAX || CAREFUL) {
                 float mx = s[0][0];
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
@@ -170,9 +172,10 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
                     for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
                 mx = fmaxf(mx, other_half(mx));
                 if constexpr (RAW) mx *= sc.a;
-                if (__any(mx > m + kLazy)) {
+                const bool grown = mx > m + kLazy && (!NO_MAX || track);
+                if (__any(grown)) {
                     // (each row by its own growth, so that its weights' rounding does not depend on the others)
-                    const float next = mx > m + kLazy ? mx : m, keep = exp2_hw(m - next);
+                    const float next = grown ? mx : m, keep = exp2_hw(m - next);
                     m = next;
                     l *= keep;
                     lr *= keep;
@@ -185,7 +188,7 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[n][r] = exp2_hw(RAW ? __builtin_fmaf(s[n][r], sc.a, -m) : NO_MAX ? s[n][r] : s[n][r] - m);
+                    s[n][r] = exp2_hw(RAW ? __builtin_fmaf(s[n][r], sc.a, -m) : NO_MAX && !CAREFUL ? s[n][r] : s[n][r] - m);
                     add += s[n][r];
                 }
             l += add;
@@ -214,6 +217,15 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
 
     l += other_half(l);
     if constexpr (ROUNDED) lr += other_half(lr); else lr = l;
+    float bad = 0.f;
+    if constexpr (!CAREFUL || NO_MAX) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) bad = __builtin_fmaf(o[d][r], 0.f, bad);
+        if (NO_MAX && l > 0.f && l < kFewWeights) bad = 1.f;
+        if constexpr (CAREFUL) bad += other_half(bad);  // (a row's two lanes keep one maximum)
+    }
     if constexpr (SPLIT) {
         if (half == 0) {
             stat[0][32 * wave + lane] = m;
@@ -269,17 +281,18 @@ __device__ __forceinline__ bool attn_fwd_rows(const AttnParams& p, const FwdShar
         if (p.lse && half == 0) p.lse[(sp.q0 + mine) * p.H + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
     }
 
-    if constexpr (CAREFUL) return false;
-    float bad = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) bad = __builtin_fmaf(o[d][r], 0.f, bad);
-    return bad != 0.f;
+    return bad != 0.f && !(CAREFUL && track);
 }
 
+// Waves a SIMD.  Capped scores without a maximum: as many as the first pass's registers leave room for; the second pass,
+// with a maximum, has to do with those (left to itself it takes a wave from the first at 32- and 64-wide heads).
+template <int ROW, int D, int CAPPED, bool SPLIT>
+constexpr int kForwardWaves = CAPPED != kCapBounds ? (SPLIT || ROW >= 512 ? 1 : 2)
+                              : SPLIT              ? (ROW <= 64 ? 3 : ROW <= 128 ? 2 : 1)
+                                                   : (D == 32 ? 4 : D == 64 ? 3 : ROW <= 256 ? 2 : 1);
+
 template <typename T, int D, int CAPPED, int BIAS, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 2) attn_fwd_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kThreads, (kForwardWaves<(int)sizeof(T) * D, D, CAPPED, SPLIT>)) attn_fwd_kernel(AttnParams p) {
     using S = FwdShared<T, D, SPLIT>;
     __shared__ __attribute__((aligned(16))) T k_a[S::ELEMS];
     __shared__ __attribute__((aligned(16))) T v_a[S::ELEMS];
@@ -289,12 +302,17 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     __shared__ float stat[SPLIT ? 4 : 1][SPLIT ? kWaves * 32 : 1];
     __shared__ int first[3][D];
     const S lds{k_a, v_a, k_b, v_b, lut, stat, first};
-    const bool bad = attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, false>(p, lds, blockIdx.x, threadIdx.x);
-    if (!__syncthreads_or(bad)) return;
+    bool again = attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, false>(p, lds, blockIdx.x, threadIdx.x, false), track = false;
+    if (!__syncthreads_or(again)) return;
     uint32_t block = blockIdx.x;
     int tid = threadIdx.x;
-    asm volatile("" : "+s"(block), "+v"(tid));  // (nothing worked out for the first time is kept for this one)
-    attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, true>(p, lds, block, tid);
+#pragma unroll 1
+    for (int pass = 0; pass < (CAPPED == kCapBounds ? 2 : 1); ++pass) {
+        asm volatile("" : "+s"(block), "+v"(tid));  // (nothing worked out for the first time is kept for this one)
+        again = attn_fwd_rows<T, D, CAPPED, BIAS, SPLIT, true>(p, lds, block, tid, track);
+        if (CAPPED != kCapBounds || !__syncthreads_or(again)) return;
+        track = again;
+    }
 }
 
 template <typename T, int D, int CAPPED, int BIAS>

@@ -271,3 +271,32 @@ def test_columns_of_seen_and_hidden_values_are_told_apart(dtype, D, heads, how):
     assert torch.equal(lse, lse0)
     assert torch.equal(torch.isnan(y), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(y, 7.0, 1e30, -1e30), torch.nan_to_num(want, 7.0, 1e30, -1e30))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cap", [50.0, 55.0, 60.0])
+@pytest.mark.parametrize("sign,size", [(1, 1e18), (-1, 1e-18), (1, 1e-18), (-1, 1e18)])
+def test_scores_at_the_cap_with_values_of_any_size(sign, size, cap, dtype, heads):
+    """Rows all of whose scores are at the cap or at its negative, where weights are e^cap or e^-cap before they are
+    divided by their sum; other rows of the same tiles keep the bits that they have without them."""
+    H, Hk = HEADS[heads]
+    n, D = 200, 64
+    d = make(27, n, n, H, Hk, D, dtype)
+    d["v"] *= size
+    d["k"][:, :, 0] = 8.0
+    d["q"][:, :, 0] = 0.0
+    cu = offsets([n])
+    q, k, v = (d[x].cuda() for x in "qkv")
+    plain, _ = ssd.ssd_attn_forward(q, k, v, cu.cuda(), softcap=cap)
+    loud = torch.arange(n) % 5 == 2
+    d["q"][loud, :, 0] = sign * 1000.0
+    y, _ = ssd.ssd_attn_forward(d["q"].cuda(), k, v, cu.cuda(), softcap=cap)
+    torch.cuda.synchronize()
+    assert torch.equal(y.cpu()[~loud], plain.cpu()[~loud])
+    hk, hq = slice(0, 2), slice(0, 2 * H // Hk)
+    d = dict(d, q=d["q"][:, hq], k=d["k"][:, hk], v=d["v"][:, hk])
+    ref = reference(d, cu=cu.numpy(), cap=cap)
+    # at the cap a score is off by the 4 u of its tanh times the cap, whatever its terms' magnitudes
+    keep = np.where(loud.numpy()[:, None], 2 * cap / (D + 32), ref["s_abs"])
+    within(f64(y)[:, hq], ref["y"], _capped_bound(dict(ref, s_abs=keep), dtype, D, n), "at the cap %g %s" % (cap, dtype))
