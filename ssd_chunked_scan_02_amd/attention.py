@@ -151,8 +151,8 @@ def _bias_args(slopes, table, H, device):
         raise ValueError("slopes and table are two forms of the bias: give at most one")
     _dense(slopes, "slopes", (H,), torch.float32, device)
     if table is not None:
-        if table.dim() != 2:
-            raise ValueError("table must be [num_buckets, H]")
+        if table.dim() != 2 or table.shape[0] < 2:
+            raise ValueError("table must be [num_buckets, H], of two buckets or more")
         _dense(table, "table", (table.shape[0], H), torch.float32, device)
     return 0 if table is None else table.shape[0]
 

@@ -123,3 +123,11 @@ def test_more_workgroups_than_a_launch_holds(lib):
     assert _entry(lib, "ssd_attn_backward", at("ssd_attn_backward"), half) == UNSUPPORTED
     cache = _cache(nseq=1 << 20, nheads=16, nkvheads=16)
     assert _entry(lib, "ssd_attn_decode", at("ssd_attn_decode"), cache) == UNSUPPORTED
+
+
+def test_a_table_without_rows_is_refused():
+    """Its address is null, which the library takes for no table."""
+    cpu = torch.device("cpu")
+    for table in (torch.zeros(0, 4), torch.zeros(1, 4), torch.zeros(4)):
+        with pytest.raises(ValueError, match="buckets"):
+            attention._bias_args(None, table, 4, cpu)
