@@ -1,4 +1,6 @@
 """The attention layer at its edges, on the GPU: calls that the documentation allows and an ordinary run does not make."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -9,8 +11,9 @@ from ssd_chunked_scan_02_amd import attention
 
 pytestmark = pytest.mark.gpu
 
-# few heads: the waves of a workgroup share rows; many: each has its own
-HEADS = {"few": (4, 2), "many": (44, 44)}
+# few heads: the waves of a workgroup share rows; many: each has its own, which takes 384 workgroups (two and more to
+# each of 192 key heads of 130 tokens or more)
+HEADS = {"few": (4, 2), "many": (384, 192)}
 
 
 def test_outputs_of_a_call_on_a_stream_are_that_streams_memory():
@@ -300,3 +303,73 @@ def test_scores_at_the_cap_with_values_of_any_size(sign, size, cap, dtype, heads
     # at the cap a score is off by the 4 u of its tanh times the cap, whatever its terms' magnitudes
     keep = np.where(loud.numpy()[:, None], 2 * cap / (D + 32), ref["s_abs"])
     within(f64(y)[:, hq], ref["y"], _capped_bound(dict(ref, s_abs=keep), dtype, D, n), "at the cap %g %s" % (cap, dtype))
+
+
+GUARD = 64  # rows
+
+
+class _Guarded:
+    """Outputs and a workspace with a pattern in them and behind them, and the C entry points called on them."""
+
+    def __init__(self, g, cu, table):
+        self.g, self.cu, self.table, q, k = g, cu, table, g["q"], g["k"]
+        self.dims = attention._dims(q, k, g["v"], cu, None, True, None, 0.0, None, table, 128, False, None)
+        need = ssd.ssd_attn_backward_workspace_bytes(self.dims, table is not None)
+        self.ws, self.need = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda"), need
+        self.out = {n: torch.full((len(t) + GUARD, *t.shape[1:]), 7.0, dtype=t.dtype, device="cuda")
+                    for n, t in (("y", q), ("dq", q), ("dk", k), ("dv", k))}
+        self.out["lse"] = torch.full((len(q) + GUARD, q.shape[1]), 7.0, device="cuda")
+        if table is not None:
+            self.out["dtable"] = torch.full((len(table) + GUARD, q.shape[1]), 7.0, device="cuda")
+
+    def run(self):
+        a, o, g = attention._addr, {n: attention._addr(t) for n, t in self.out.items()}, self.g
+        ins = [ctypes.byref(self.dims), a(self.cu), None, None, a(g["q"]), a(g["k"]), a(g["v"]), None, a(self.table)]
+        dev = g["q"].device
+        attention._call("ssd_attn_forward", dev, None, *ins, o["y"], o["lse"])
+        attention._call("ssd_attn_backward", dev, None, *ins, o["y"], o["lse"], a(g["dy"]), o["dq"], o["dk"], o["dv"],
+                        o.get("dtable"), a(self.ws), self.need)
+        torch.cuda.synchronize()
+
+    def check_untouched(self, first):
+        """Rows from ``first`` on (of a table: behind its last) and what is behind the workspace are as they were."""
+        for n, t in self.out.items():
+            assert torch.all(t[len(self.table) if n == "dtable" else first:] == 7.0), n
+        assert torch.all(self.ws[self.need:] == 0x5A)
+
+
+def _guarded(heads, dtype, total, table):
+    H, Hk = HEADS[heads]
+    d = make(28, total, total, H, Hk, 64, dtype, bias="buckets" if table else "none", grads=True)
+    return {n: d[n].cuda() for n in ("q", "k", "v", "dy")}, d["table"].cuda() if table else None
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("table", [False, True])
+def test_backward_writes_no_row_of_no_sequence(table, dtype, heads):
+    """Tokens behind the last sequence (NaN themselves) keep what their rows of every output held, and nothing is
+    written behind the outputs and the workspace; the sequences' rows have nothing of that pattern."""
+    lens, extra = [70, 0, 133], 45
+    n = sum(lens)
+    g, table = _guarded(heads, dtype, n + extra, table)
+    for t in g.values():
+        t[n:] = float("nan")
+    case = _Guarded(g, offsets(lens).cuda(), table)
+    case.run()
+    case.check_untouched(n)
+    for name, t in case.out.items():
+        rows = t[:len(table)] if name == "dtable" else t[:n]
+        assert torch.all(torch.isfinite(rows)) and not torch.any(torch.all(rows.flatten(1) == 7.0, 1)), name
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [[0, 500, -7, 300], [200, 100, 300, 250], [-1, -1, 10 ** 12, 5], [300, 300, 300, 300],
+                                 [290, 10, 290, 10]], ids=str)
+def test_malformed_offsets_write_inside_the_outputs(bad, dtype, heads):
+    """Offsets that fall, repeat or lie outside the axis: some gradients, and nothing behind any output."""
+    g, table = _guarded(heads, dtype, 300, True)
+    case = _Guarded(g, torch.tensor(bad, dtype=torch.int64, device="cuda"), table)
+    case.run()
+    case.check_untouched(300)
