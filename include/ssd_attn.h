@@ -94,8 +94,8 @@ int ssd_attn_forward(const ssd_attn_dims* dims, const int64_t* cu_seqlens_q,
  *   dtable        [num_buckets, H] fp32, or NULL to skip it; needs table.
  *   workspace     device scratch of at least ssd_attn_backward_workspace_bytes(dims, dtable wanted)
  *                 bytes, 16-byte aligned; its contents are undefined afterwards.
- * Rows of no sequence are never written; a key that no query sees has zero gradients.  No atomics: equal
- * calls give equal bits.  Two to five launches.
+ * Rows of no sequence are never written; a key that no query sees has zero gradients.  No sum is made
+ * by atomics: equal calls give equal bits.  Two to five launches.
  */
 size_t ssd_attn_backward_workspace_bytes(const ssd_attn_dims* dims, int want_dtable);
 

@@ -4,23 +4,29 @@
 //     dq_i = scale sum_j dz_ij k_j,  dk_j = scale sum_i dz_ij q_i,  dv_j = sum_i p_ij dy_i,
 //     dtable[b] = sum of dS over the cells of bucket b.
 //
-// Two kernels, each owning what it sums, so that nothing is added by atomics and every run gives the
+// Two kernels, each owning what it sums, so that no sum is made by atomics and every run gives the
 // same bits: attn_dq_kernel owns 128 query rows and streams keys (S^T, dP^T, dq^T), and leaves D for
 // attn_dkv_kernel, which owns 128 keys of a key head and streams the queries of every head of its group
 // (S, dP, dv^T, dk^T).  That is 7 products where sharing S and dP would need 5, and no partial
 // gradients through memory.  Both keep their rows' operands and gradients in registers; the tile layout
 // and operand order are the forward kernel's (ssd_attn_common.h).
 //
-// D is sum_d dy_id y_id, which is as exact as the given y.  What a bf16 y leaves in dq and dk, (y's error . dy)
-// sum_j p_ij k_j, falls as 1 / n with the n keys of a row beside a dq that falls as 1 / sqrt(n).  The sum of a row's
-// dS is what the D that it was formed with is off by: rows that see one tile of keys (the first of a document, where
-// that error was most of all dq's) take it from a first visit to their tile.  The gradient of the table sums dS over
-// whole diagonals, where it counts for every row: after the pass over all keys D is exact; far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of
-// their p, and the tiles near the diagonal are visited once more with the exact D, for the table alone.
+// D is sum_d dy_id y_id to begin with, which is as exact as the given y: a bf16 y leaves it off by some e_i, and dq_i by
+// scale e_i sum_j p_ij k_j.  That is little for weights spread over keys and values without a mean, but whole where a row
+// has one dominating key, or keys and values a common part: dq off by 6e-2 at a mean of 2, or at a weight of 0.99 on one
+// key of 2048.  The sum of a row's dS is e_i (with a bf16 dS, its own roundings' sum beside it), known after the pass, and
+// with the sum of p k beside that of dS k dq is put right at the end, for one product more and registers (MEAN): 1.7e-3 to
+// 2.3e-3 in all those cases.  The gradient of the table sums dS over whole diagonals, where e_i counts for every row: with D
+// exact after the pass far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of their p,
+// and the tiles near the diagonal are visited once more, for the table alone.  For 128-wide heads with a table the sum of
+// p k would take a wave's room on each SIMD, and a pass over S and dP comes before instead (PASS), after which the
+// diagonals are summed as dS comes up, as in fp32, whose y needs none of this.
 //
-// Measured, bf16: 8 x 2048 tokens, 24 heads of 64, capped: dq 260 us (bound by VALU, 81% busy), dk and dv 350 us
-// (VALU 59%, MFMA 29%, in turns); 16385 packed tokens, 16/4 heads of 128, buckets: dq 217 us, dk and dv 243 us
-// (530 us with four waves a workgroup and tiles in the order of the documents), table 8 us, plan 6 us.
+// Measured in profiled runs, bf16: 8 x 2048 tokens, 24 heads of 64, capped: dq 335 us, dk and dv 365 us;
+// 16385 packed tokens, 16/4 heads of 128, buckets: dq 265 us, dk and dv 244 us (530 us with four waves a workgroup and
+// tiles in the order of the documents), table 8 us, plan 7 us.
+#include <type_traits>
+
 #include "ssd_attn_common.h"
 
 namespace ssd {
@@ -53,19 +59,73 @@ __device__ __forceinline__ float fold_bucket(const AttnBuckets& b, const float* 
     return v;
 }
 
-template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : sizeof(T) * D >= 256 ? 2 : 3) attn_dq_kernel(AttnParams p) {
+// How a workgroup shares its work.  (Paired key gradients at 64-wide heads, whose sums leave room for two waves a SIMD
+// anyway: 452 us against 350.)
+enum Share {
+    kAlone = 0,   // four waves, 32 rows (keys) each
+    kSplit = 1,   // four waves on the same 32 (see kOwn)
+    kPaired = 2,  // eight waves, two on the same 32, each with half of a streamed tile, and the operands of the workgroup's
+                  // own rows in LDS: the sums of 128-wide heads alone fill half a SIMD's registers, and so two waves
+                  // still fit on each
+};
+
+// Adds the sums of a pair's second wave to its first's, through a buffer of the pair's own.
+template <int DT> __device__ __forceinline__ void add_second(f32x16 (&acc)[DT], float* over, int second, int lane) {
+    f32x4* at = reinterpret_cast<f32x4*>(over) + lane;
+    if (second) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                at[(4 * d + r / 4) * kWave] = f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
+    }
+    __syncthreads();
+    if (!second) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const f32x4 x = at[(4 * d + r / 4) * kWave];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[d][r + e] += x[e];
+            }
+    }
+    __syncthreads();
+}
+
+// How dq gets rid of what a bf16 y leaves in D: with the sum of p k beside the sum of dS k (MEAN), or with a pass of its own
+// for D before (PASS).  dq with the sum, with the pass and with neither, us, bf16, 16385 tokens in 32 documents, 16/4 heads
+// (4 x 2048 tokens, 8 heads):
+//     64 wide  80 (n/a), 106, 63                          with buckets and their gradient  184 (144), 165 (211), 126 (128)
+//     128 wide 230 (131), 209 (231), 139 (135)            with buckets and their gradient  359, 269, 221
+template <typename T, int D, int BIAS> constexpr bool kTakesPass = sizeof(T) == 2 && D == 128 && BIAS == kBiasBuckets;
+template <typename T, int D, int BIAS> constexpr bool kTakesMean = sizeof(T) == 2 && !kTakesPass<T, D, BIAS>;
+
+// Waves a SIMD that the sums and operands in registers leave room for.
+template <int ROW, int D, bool MEAN, int SHARE>
+constexpr int kQueryWaves = SHARE != kAlone || ROW >= 512 ? 1 : ROW == 256 || (MEAN && D == 64) ? 2 : 3;
+
+template <typename T, int D, bool CAP, int BIAS, int SHARE>
+__global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads,
+                                  (kQueryWaves<(int)sizeof(T) * D, D, kTakesMean<T, D, BIAS>, SHARE>))
+    attn_dq_kernel(AttnParams p) {
     using O = Op<T>;
     using L = Tile<T, D>;
     using Frag = typename O::Frag;
-    constexpr int OWN = kOwn<SPLIT>, KT = SPLIT ? 32 : O::kKT, NS = KT / 32, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
+    constexpr bool SPLIT = SHARE == kSplit, PAIRED = SHARE == kPaired, MEAN = kTakesMean<T, D, BIAS>;
+    static_assert(!PAIRED || BIAS != kBiasBuckets, "the sums by distance are those of four waves");
+    constexpr int OWN = kOwn<SPLIT>, KT = SPLIT ? 32 : O::kKT, NT = D / O::kK, DT = D / 32, PK = 32 / O::kK;
+    constexpr int NS = PAIRED ? 1 : KT / 32;  // 32-key blocks of a tile that are this wave's
+    constexpr int BLOCK = PAIRED ? 2 * kThreads : kThreads;
     constexpr int ELEMS = (SPLIT ? kWaves : 1) * KT * D;
     constexpr bool DOUBLE = !SPLIT || ELEMS * sizeof(T) <= 32768;
     __shared__ __attribute__((aligned(16))) T k_a[ELEMS];
     __shared__ __attribute__((aligned(16))) T v_a[ELEMS];
     __shared__ __attribute__((aligned(16))) T k_b[DOUBLE ? ELEMS : 8];
     __shared__ __attribute__((aligned(16))) T v_b[DOUBLE ? ELEMS : 8];
-    __shared__ float off_by[SPLIT ? kWaves * 32 : 1];
+    __shared__ __attribute__((aligned(16))) T q_own[PAIRED ? OWN * D : 8];
+    __shared__ __attribute__((aligned(16))) T g_own[PAIRED ? OWN * D : 8];
+    __shared__ float off_by[SPLIT || PAIRED ? BLOCK / 2 : 1];
     extern __shared__ float extra[];
 
     int slot, unit;
@@ -81,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     }
     const int kvh = (int)((uint32_t)head0 / ((uint32_t)p.H / (uint32_t)p.Hk));
     const int lane = threadIdx.x % kWave, half = lane / 32;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int all_waves = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int wave = all_waves % kWaves, n_own = all_waves / kWaves;  // (PAIRED: which 32 keys of a tile)
     const int shift = sp.lk - sp.lq;
     int prefix = 0;
     if (p.prefix) prefix = (int)clamp64(p.prefix[sp.seq], 0, sp.lk);
@@ -97,12 +158,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 
     const T* kg = static_cast<const T*>(p.k) + sp.k0 * p.k_stride + (int64_t)kvh * D;
     const T* vg = static_cast<const T*>(p.v) + sp.k0 * p.v_stride + (int64_t)kvh * D;
-    Feed<T, D, KT, SPLIT ? kWave : kThreads> kf, vf;
+    Feed<T, D, KT, SPLIT ? kWave : BLOCK> kf, vf;
     kf.init(p.k_stride);
     vf.init(p.v_stride);
     const int at = SPLIT ? wave * KT * D : 0;
     T *ka = k_a + at, *va = v_a + at, *kb = k_b + (DOUBLE ? at : 0), *vb = v_b + (DOUBLE ? at : 0);
-    auto fetch = [&](T* ks, T* vs, int t) {
+    auto fetch = [&](T* ks, T* vs, int t) __attribute__((always_inline)) {
         kf.load(ks, kg, t * KT, sp.lk - t * KT);
         vf.load(vs, vg, t * KT, sp.lk - t * KT);
     };
@@ -110,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
     if (t0 < ntiles) fetch(ka, va, t0);
 
     const int64_t mine = (sp.q0 + query) * p.H + head;  // this lane's (query, head)
-    Frag qf[NT], gf[NT];
+    Frag qf[PAIRED ? 1 : NT], gf[PAIRED ? 1 : NT];
     float delta = 0.f;
     {
         const T* qg = static_cast<const T*>(p.q) + (sp.q0 + query) * p.q_stride + (int64_t)head * D;
@@ -119,11 +180,17 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int e0 = (2 * t + half) * O::kE;
-            qf[t] = __builtin_bit_cast(Frag, ld16(qg + e0));
-            gf[t] = __builtin_bit_cast(Frag, ld16(gg + e0));
-            const Frag yf = __builtin_bit_cast(Frag, ld16(yg + e0));
+            const Frag g = __builtin_bit_cast(Frag, ld16(gg + e0)), yf = __builtin_bit_cast(Frag, ld16(yg + e0));
+            if constexpr (PAIRED) {  // (a pair's first wave keeps the queries, its second dy)
+                const int own = L::at(32 * wave + lane % 32, 2 * t + half);
+                if (n_own == 0) st16(q_own + own, ld16(qg + e0));
+                else st16(g_own + own, __builtin_bit_cast(uint4, g));
+            } else {
+                qf[t] = __builtin_bit_cast(Frag, ld16(qg + e0));
+                gf[t] = g;
+            }
 #pragma unroll
-            for (int e = 0; e < O::kE; ++e) delta += (float)gf[t][e] * (float)yf[e];
+            for (int e = 0; e < O::kE; ++e) delta += (float)g[e] * (float)yf[e];
         }
     }
     delta += other_half(delta);
@@ -145,30 +212,36 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
         if (grad)
             for (int i = lane; i < reach; i += kWave) sums[i] = 0.f;
     }
-    // far cells' dS and p, below (first) and above the reach, and the row's sum of dS
-    float far_ds[2] = {0.f, 0.f}, far_p[2] = {0.f, 0.f}, row_ds = 0.f;
+    // the row's sum of dS (before the cap's derivative), and that of far cells below and above the reach
+    float row_ds = 0.f, far_lo = 0.f, far_hi = 0.f, far_lo_p = 0.f, far_hi_p = 0.f;  // (and of their p)
     const int qpos = query + shift;
 
-    f32x16 acc[DT];
+    f32x16 acc[DT], mean[MEAN ? DT : 1];  // sums of dS k and of p k
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
+#pragma unroll
+    for (int d = 0; d < (MEAN ? DT : 1); ++d) mean[d] = f32x16{};
 
-    auto settle = [&]() {
+    auto settle = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_s_waitcnt(SPLIT ? kAllDone : kLoadsDone);
         if constexpr (SPLIT) __builtin_amdgcn_wave_barrier(); else lds_barrier();
     };
-    // p and dS of 32 keys from kn on (dS before the cap's derivative, which is returned in `slope`, or with no bias
-    // and `whole` already in dS); true: some are nearer than the table's reach
+    // p and dS of 32 keys from kn on, before the cap's derivative, which is returned in `slope`, or with no bias and
+    // `whole` already in both (dS before it is then in row_ds); true: some are nearer than the table's reach
     typename L::Lanes z(lane);
-    auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope, bool whole = true) {
+    auto q_frag = [&](int i) { return PAIRED ? L::rows(q_own, 32 * wave, i, z) : qf[PAIRED ? 0 : i]; };
+    auto g_frag = [&](int i) { return PAIRED ? L::rows(g_own, 32 * wave, i, z) : gf[PAIRED ? 0 : i]; };
+    auto weights = [&](const T* kt, const T* vt, int n, int kn, f32x16& s, f32x16& ds, f32x16& slope, bool whole) __attribute__((always_inline)) {
         z.renew();
         f32x16 x[1] = {f32x16{}}, dp;
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] = -delta;  // the accumulator starts at -D: dP - D at no cost
 #pragma unroll
-        for (int i = 0; i < NT; ++i) x[0] = O::mma(L::rows(kt, 32 * n, i, z), qf[i], x[0]);
+        for (int i = 0; i < NT; ++i) x[0] = O::mma(L::rows(kt, 32 * n, i, z), q_frag(i), x[0]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, z), gf[i], dp);
+        for (int i = 0; i < NT; ++i) dp = O::mma(L::rows(vt, 32 * n, i, z), g_frag(i), dp);
+        // (left to itself the schedule holds more than there are registers for)
+        if constexpr (PAIRED) __builtin_amdgcn_sched_barrier(0);
         if constexpr (CAP) {
             sc.template capped<T>(x);
             if constexpr (BIAS != kBiasNone) {
@@ -186,27 +259,74 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             s[r] = exp2_hw(!CAP && BIAS == kBiasNone ? __builtin_fmaf(x[0][r], sc.a, -lse2) : x[0][r] - lse2);
-            ds[r] = s[r] * dp[r];
             // (without a bias the capped score is still there to take the derivative from)
             if constexpr (CAP && BIAS == kBiasNone) {
-                if (whole) ds[r] *= sc.slope(x[0][r]);
+                if (whole) {
+                    if constexpr (MEAN) row_ds = __builtin_fmaf(s[r], dp[r], row_ds);
+                    s[r] *= sc.slope(x[0][r]);
+                }
             }
+            ds[r] = s[r] * dp[r];
         }
         return near;
     };
-    auto step = [&](const T* kt, const T* vt, T* kn_, T* vn_, int t) {
+    // Sums of dS along the diagonals of 16 keys x 32 queries at a time: lane j takes relative position base + j, from the
+    // corner key 0, query 31 on.
+    auto by_distance = [&](const f32x16& ds, int kn) __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) block[(acc_row(r) + 4 * half) * kDiagStride + lane % 32] = ds[8 * b + r];
+            __builtin_amdgcn_wave_barrier();
+            const int off = lane - 31, rel = kn + 16 * b - (row0 + shift) + off;
+            float add = 0.f;
+#pragma unroll
+            for (int key = 0; key < kDiagRows; ++key) {
+                const int q = key - off;
+                const float x = block[key * kDiagStride + min(max(q, 0), 31)];
+                add += q >= 0 && q < 32 ? x : 0.f;
+            }
+            if (lane < 31 + kDiagRows) {
+                if (rel <= -md) far_lo += add;
+                else if (rel >= md) far_hi += add;
+                else sums[rel + md] += add;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
+    // (ONLY_D: the first of two passes, for the sum of dS alone)
+    auto step = [&](auto only_d, const T* kt, const T* vt, T* kn_, T* vn_, int t) __attribute__((always_inline)) {
+        constexpr bool ONLY_D = decltype(only_d)::value;
         const int k0 = t * KT;
         if (DOUBLE && t + dt < ntiles) fetch(kn_, vn_, t + dt);
         if (k0 < wave_most) {
-            // (one half of a tile after the other: both at once take the registers of one more wave a SIMD, which is
-            // worth more: 282 -> 263 us at 8 x 2048 tokens, 24 heads of 64, capped; 332 -> 282 us on packed 128-wide heads)
+            // (one half of a tile after the other: both at once take the registers of one more wave a SIMD)
 #pragma unroll 1
-            for (int n = 0; n < NS; ++n) {
-                const int kn = k0 + 32 * n;
+            for (int j = 0; j < NS; ++j) {
+                const int n = PAIRED ? n_own : j, kn = k0 + 32 * n;
                 f32x16 s, ds, slope;
-                const bool near = weights(kt, vt, n, kn, s, ds, slope);
-                if constexpr (BIAS == kBiasBuckets) {
+                const bool near = weights(kt, vt, n, kn, s, ds, slope, !ONLY_D);
+                if constexpr (ONLY_D || (MEAN && CAP && BIAS == kBiasSlopes)) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) row_ds += ds[r];
+                }
+                if constexpr (ONLY_D) continue;
+                if constexpr (BIAS == kBiasBuckets && !MEAN) {
                     if (grad) {
+                        if (near) {
+                            by_distance(ds, kn);
+                        } else {
+                            float a = 0.f;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) a += ds[r];
+                            const bool above = kn >= row0 + shift;
+                            far_lo += above ? 0.f : a;
+                            far_hi += above ? a : 0.f;
+                        }
+                    }
+                }
+                if constexpr (BIAS == kBiasBuckets && MEAN) {
+                    if (grad || CAP) {
                         float a = 0.f, b = 0.f;
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
@@ -215,18 +335,28 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                         }
                         row_ds += a;
                         const bool above = kn >= row0 + shift;
-                        far_ds[0] += near || above ? 0.f : a;
-                        far_p[0] += near || above ? 0.f : b;
-                        far_ds[1] += near || !above ? 0.f : a;
-                        far_p[1] += near || !above ? 0.f : b;
+                        far_lo += near || above ? 0.f : a;
+                        far_lo_p += near || above ? 0.f : b;
+                        far_hi += near || !above ? 0.f : a;
+                        far_hi_p += near || !above ? 0.f : b;
                     }
                 }
-                if constexpr (CAP && BIAS != kBiasNone) ds *= slope;
+                if constexpr (CAP && BIAS != kBiasNone) {
+                    ds *= slope;
+                    if constexpr (MEAN) s *= slope;
+                }
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk) {
-                    const Frag sf = O::pack(ds, kk);
+                    const Frag sf = O::pack(ds, kk), pf = O::pack(s, kk);
+                    if constexpr (MEAN && !CAP) {
+                        if (!grad) row_ds = sum_of(sf, row_ds);
+                    }
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) acc[d] = O::mma(L::cols(kt, 32 * n, kk, 32 * d, z), sf, acc[d]);
+                    for (int d = 0; d < DT; ++d) {
+                        const Frag kf = L::cols(kt, 32 * n, kk, 32 * d, z);
+                        acc[d] = O::mma(kf, sf, acc[d]);
+                        if constexpr (MEAN) mean[d] = O::mma(kf, pf, mean[d]);
+                    }
                 }
             }
         }
@@ -236,30 +366,41 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             settle();
         }
     };
-    settle();
-    if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();
-    if (t0 == 0 && wave_most > 0 && wave_most <= KT) {
-        // all that these rows see is there: first the sum of dS, which D is off by
-        float off = 0.f;
-#pragma unroll 1
-        for (int n = 0; n < NS; ++n) {
-            f32x16 s, ds, slope;
-            weights(ka, va, n, 32 * n, s, ds, slope, false);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) off += ds[r];
+    auto pass = [&](auto only_d) __attribute__((always_inline)) {
+        settle();
+        for (int t = t0; t < ntiles; t += 2 * dt) {
+            step(only_d, ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
+            if (t + dt < ntiles) step(only_d, DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);
         }
-        delta += off + other_half(off);
+    };
+    // the sum of a row's dS over all its keys, which its D is off by
+    auto row_sum = [&]() __attribute__((always_inline)) {
+        row_ds += other_half(row_ds);
+        if constexpr (SPLIT || PAIRED) {
+            if (half == 0) off_by[32 * all_waves + lane] = row_ds;
+            __syncthreads();
+            row_ds = 0.f;
+#pragma unroll
+            for (int w = 0; w < BLOCK / kWave; ++w) row_ds += SPLIT || w % kWaves == wave ? off_by[32 * w + lane % 32] : 0.f;
+        }
+        delta += row_ds;
+    };
+    if constexpr (SPLIT && BIAS == kBiasBuckets) __syncthreads();
+    if constexpr (kTakesPass<T, D, BIAS>) {
+        pass(std::true_type{});
+        row_sum();
+        if (t0 < ntiles) fetch(ka, va, t0);
     }
-    for (int t = t0; t < ntiles; t += 2 * dt) {
-        step(ka, va, DOUBLE ? kb : ka, DOUBLE ? vb : va, t);
-        if (t + dt < ntiles) step(DOUBLE ? kb : ka, DOUBLE ? vb : va, ka, va, t + dt);
+    pass(std::false_type{});
+    if constexpr (MEAN) {
+        row_sum();
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] -= row_ds * mean[d];
     }
 
     if constexpr (SPLIT) {
         __syncthreads();
         Join<T, D>::keep(k_a, v_a, acc, lane, wave);
-        row_ds += other_half(row_ds);
-        if (half == 0) off_by[32 * wave + lane] = row_ds;
         __syncthreads();
         for (int i = threadIdx.x; i < 32 * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
@@ -268,13 +409,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
             const int q = query_of(row0 + r);
             store4(static_cast<T*>(p.dq) + ((sp.q0 + q) * p.H + head0 + row0 + r - q * p.pack) * D + 4 * d4, v[0], v[1], v[2], v[3]);
         }
-        row_ds = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) row_ds += off_by[32 * w + lane % 32];
-        __syncthreads();  // (the tiles are free again)
     } else {
-        row_ds += other_half(row_ds);
-        if (row < sp.rows) {
+        if constexpr (PAIRED) {
+            static_assert(!PAIRED || ELEMS * sizeof(T) == 32 * D * 4, "a tile's buffer holds one wave's sums");
+            add_second(acc, reinterpret_cast<float*>(wave == 0 ? k_a : wave == 1 ? v_a : wave == 2 ? k_b : v_b), n_own, lane);
+        }
+        if (row < sp.rows && n_own == 0) {
             T* out = static_cast<T*>(p.dq) + mine * D;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -282,50 +422,33 @@ __global__ void __launch_bounds__(kThreads, SPLIT || sizeof(T) * D >= 512 ? 1 : 
                 for (int r = 0; r < 16; r += 8) store_rows(out + 32 * d, acc[d], r, half, p.scale);
         }
     }
-    if (grad) delta += row_ds;
-    if (row < sp.rows && half == 0 && (!SPLIT || wave == 0)) p.delta[mine] = delta;
+    if (row < sp.rows && half == 0 && (SPLIT ? wave : n_own) == 0) p.delta[mine] = delta;
     if constexpr (BIAS == kBiasBuckets) {
         if (!grad) return;
-        float far_lo = far_ds[0] - row_ds * far_p[0], far_hi = far_ds[1] - row_ds * far_p[1];
-        // tiles with a relative position inside the reach of any of the workgroup's queries
-        const int q_first = sp.tile * OWN + shift, q_last = q_first + OWN - 1;
-        const int n0 = max(q_first - md, 0) / KT, n1 = min(ntiles, q_last + md < 0 ? 0 : (q_last + md) / KT + 1);
-        for (int t = n0 + t0; t < n1; t += dt) {
-            const int k0 = t * KT;
-            fetch(ka, va, t);
-            settle();
-            if (k0 < wave_most) {
+        if constexpr (MEAN) {
+            // D is exact now: far cells are put right by the sums of their p, and the tiles with a relative position inside
+            // the reach of any of the workgroup's queries are visited again
+            far_lo -= row_ds * far_lo_p;
+            far_hi -= row_ds * far_hi_p;
+            const int q_first = sp.tile * OWN + shift, q_last = q_first + OWN - 1;
+            const int n0 = max(q_first - md, 0) / KT, n1 = min(ntiles, q_last + md < 0 ? 0 : (q_last + md) / KT + 1);
+            if constexpr (SPLIT) __syncthreads();  // (the tiles are free again)
+            for (int t = n0 + t0; t < n1; t += dt) {
+                const int k0 = t * KT;
+                fetch(ka, va, t);
+                settle();
+                if (k0 < wave_most) {
 #pragma unroll 1
-                for (int n = 0; n < NS; ++n) {
-                    const int kn = k0 + 32 * n;
-                    if (kn + 31 - (row0 + shift) <= -md || kn - (row0 + 31 + shift) >= md) continue;
-                    f32x16 s, ds, slope;
-                    weights(ka, va, n, kn, s, ds, slope);
-                    // sums along the diagonals of 16 keys x 32 queries: lane j takes relative position
-                    // base + j, from the corner key 0, query 31 on
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) block[(acc_row(r) + 4 * half) * kDiagStride + lane % 32] = ds[8 * b + r];
-                        __builtin_amdgcn_wave_barrier();
-                        const int off = lane - 31, rel = kn + 16 * b - (row0 + shift) + off;
-                        float add = 0.f;
-#pragma unroll
-                        for (int key = 0; key < kDiagRows; ++key) {
-                            const int q = key - off;
-                            const float x = block[key * kDiagStride + min(max(q, 0), 31)];
-                            add += q >= 0 && q < 32 ? x : 0.f;
-                        }
-                        if (lane < 31 + kDiagRows) {
-                            if (rel <= -md) far_lo += add;
-                            else if (rel >= md) far_hi += add;
-                            else sums[rel + md] += add;
-                        }
-                        __builtin_amdgcn_wave_barrier();
+                    for (int n = 0; n < NS; ++n) {
+                        const int kn = k0 + 32 * n;
+                        if (kn + 31 - (row0 + shift) <= -md || kn - (row0 + 31 + shift) >= md) continue;
+                        f32x16 s, ds, slope;
+                        weights(ka, va, n, kn, s, ds, slope, false);
+                        by_distance(ds, kn);
                     }
                 }
+                settle();
             }
-            settle();
         }
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1) {
@@ -461,16 +584,6 @@ __global__ void __launch_bounds__(kThreads) attn_dtable_kernel(AttnParams p) {
         p.dtable[(int64_t)b * p.H + head] = (float)v;
     }
 }
-
-// How a workgroup of the key-gradient kernel shares its work.  (kPaired at 64-wide heads, whose sums leave room for two
-// waves a SIMD anyway: 452 us against 350.)
-enum Share {
-    kAlone = 0,   // four waves, 32 keys each
-    kSplit = 1,   // four waves on the same 32 keys (see kOwn)
-    kPaired = 2,  // eight waves, two on the same 32 keys, each with half of a tile's queries, and the keys and
-                  // values in LDS: the gradients of 128-wide heads alone fill half a SIMD's registers, and so two
-                  // waves still fit on each
-};
 
 template <typename T, int D, bool CAP, int BIAS, int SHARE>
 __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SHARE != kAlone || sizeof(T) * D >= 256 ? 1 : 2)
@@ -704,35 +817,16 @@ __global__ void __launch_bounds__(SHARE == kPaired ? 2 * kThreads : kThreads, SH
     T* dkg = static_cast<T*>(p.dk) + ((sp.k0 + key) * p.Hk + kvh) * D;
     T* dvg = static_cast<T*>(p.dv) + ((sp.k0 + key) * p.Hk + kvh) * D;
     if constexpr (PAIRED) {
-        // the second wave of a pair hands its sums over, a tile's buffer for each pair
-        static_assert(!PAIRED || ELEMS * sizeof(T) == 32 * D * 4, "one buffer holds one wave's sums");
+        static_assert(!PAIRED || ELEMS * sizeof(T) == 32 * D * 4, "a tile's buffer holds one wave's sums");
         float* over = reinterpret_cast<float*>(wave == 0 ? q_a : wave == 1 ? g_a : wave == 2 ? q_b : g_b);
         auto merge = [&](f32x16(&acc)[DT], T* out, float f) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    f32x4* at = reinterpret_cast<f32x4*>(over + ((4 * d + r / 4) * kWave + lane) * 4);
-                    if (n_own == 1) *at = f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
-                }
-            __syncthreads();
-            if (n_own == 0) {
+            add_second(acc, over, n_own, lane);
+            if (n_own == 0 && key < sp.lk) {
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        const f32x4 x = *reinterpret_cast<const f32x4*>(over + ((4 * d + r / 4) * kWave + lane) * 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[d][r + e] += x[e];
-                    }
-                if (key < sp.lk) {
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int r = 0; r < 16; r += 8) store_rows(out + 32 * d, acc[d], r, half, f);
-                }
+                    for (int r = 0; r < 16; r += 8) store_rows(out + 32 * d, acc[d], r, half, f);
             }
-            __syncthreads();
         };
         merge(dk, dkg, p.scale);
         merge(dv, dvg, 1.f);
@@ -771,16 +865,19 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) attn_pa
 // Bytes of LDS that a workgroup may have (160 KB), less the largest fixed part of a split kernel.
 constexpr size_t kSplitBiasLds = 163840 - 139264;
 
-template <typename T, int D, bool CAP, int BIAS, bool SPLIT>
+template <typename T, int D, bool CAP, int BIAS, int SHARE>
 int launch_dq(AttnParams p, hipStream_t stream) {
-    p.q_slots = (int)query_slots(p, kOwn<SPLIT>);
-    set_each(p, kOwn<SPLIT>, 1);
+    constexpr int OWN = kOwn<SHARE == kSplit>;
+    p.q_slots = (int)query_slots(p, OWN);
+    set_each(p, OWN, 1);
     const int64_t grid = (int64_t)p.q_slots * (p.H / p.pack);
     const size_t lds = 4 * (size_t)bias_floats(BIAS, p.bk.max_distance, p.dtable != nullptr);
-    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dq_kernel<T, D, CAP, BIAS, SPLIT>),
+    if (BIAS == kBiasBuckets && hipFuncSetAttribute(reinterpret_cast<const void*>(&attn_dq_kernel<T, D, CAP, BIAS, SHARE>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return -1;
-    if (grid > 0) hipLaunchKernelGGL((attn_dq_kernel<T, D, CAP, BIAS, SPLIT>), dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
+    if (grid > 0)
+        hipLaunchKernelGGL((attn_dq_kernel<T, D, CAP, BIAS, SHARE>), dim3((unsigned)grid),
+                           dim3(SHARE == kPaired ? 2 * kThreads : kThreads), lds, stream, p);
     if (p.dtable) hipLaunchKernelGGL(attn_dtable_kernel, dim3((unsigned)p.H), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
@@ -811,9 +908,9 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
     d.pack = query_pack(p, BIAS);
     const bool dq_split = dq_fits && query_slots(d, kOwn<false>) * (d.H / d.pack) < attn_split_below(Tile<T, D>::RB);
     const bool dkv_split = dkv_fits && attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk < attn_split_below(Tile<T, D>::RB);
-    constexpr int WHOLE = sizeof(T) == 2 && D == 128 ? kPaired : kAlone;
+    constexpr int WHOLE = sizeof(T) == 2 && D == 128 ? kPaired : kAlone, WHOLE_DQ = BIAS != kBiasBuckets ? WHOLE : kAlone;
     // (a split kernel has few workgroups)
-    if ((!dq_split && !launchable(query_slots(d, kOwn<false>) * (d.H / d.pack), kThreads)) ||
+    if ((!dq_split && !launchable(query_slots(d, kOwn<false>) * (d.H / d.pack), WHOLE_DQ == kPaired ? 2 * kThreads : kThreads)) ||
         (!dkv_split && !launchable(attn_slots(p.cu_k, p.total_k, p.nseq, kOwn<false>) * p.Hk, WHOLE == kPaired ? 2 * kThreads : kThreads)))
         return -2;
     d.plan_q = d.plan_k = nullptr;
@@ -825,7 +922,7 @@ int launch_bwd(const AttnParams& p, hipStream_t stream) {
         if (!dq_split) d.plan_q = p.plan_q;
         if (!dkv_split) d.plan_k = p.plan_k;
     }
-    int rc = dq_split ? launch_dq<T, D, CAP, BIAS, true>(d, stream) : launch_dq<T, D, CAP, BIAS, false>(d, stream);
+    int rc = dq_split ? launch_dq<T, D, CAP, BIAS, kSplit>(d, stream) : launch_dq<T, D, CAP, BIAS, WHOLE_DQ>(d, stream);
     if (rc == 0) rc = dkv_split ? launch_dkv<T, D, CAP, BIAS, kSplit>(d, stream) : launch_dkv<T, D, CAP, BIAS, WHOLE>(d, stream);
     return rc;
 }
