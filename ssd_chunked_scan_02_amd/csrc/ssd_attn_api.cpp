@@ -205,16 +205,21 @@ int check_cache(const ssd_attn_cache* d) {
 // Splits of a sequence's keys: enough workgroups for four on each of the 256 CUs, so that short and long
 // sequences even out, of at least 128 keys (a block for each wave) at the longest length, and few
 // enough that joining them stays small.  A short cache with a workgroup for every other CU or more is not
-// split but gets eight waves a workgroup (bf16, 32/8 heads of 128, 1000 keys: 32 sequences 19.5 us against
-// 20.0 and 4.3 for the join; one sequence 15.2 us against 6.8 and 4.0, so few workgroups are split).
+// split but gets eight waves a workgroup, which saves the join.  Split (with its join) against eight waves, us, 1000 keys, 32/8
+// heads, 16 and 32 and 62 sequences (128, 256 and 496 workgroups):
+//     bf16  32 wide 11.4/10.2  17.1/14.2  26.4/21.6      64 wide 14.6/11.8  18.9/14.6  28.5/23.5    128 wide 21.7/18.0  28.9/23.1  44.9/42.3
+//     fp32  32 wide 15.4/14.1  20.6/16.6  31.8/25.6      64 wide 23.6/21.6  32.5/25.2  50.1/45.7    128 wide 39.1/46.6  64.9/55.8  139/126
+// and more at 256 and 512 keys (6 to 40%).  In fp32 at 128 wide eight waves' tiles fill a CU's LDS: there below 256
+// workgroups only up to 256 keys (15.4/15.3; 23.3/26.5 at 512).  One sequence: 10.8 split, 15.2 (bf16, 128 wide).
 struct DecodeShape {
     int splits, wide;
 };
-constexpr int64_t kWideKeys = 1024;
+constexpr int64_t kWideKeys = 1024, kWideKeysFullLds = 256;
 DecodeShape decode_shape(const ssd_attn_cache* d) {
     const int64_t group = d->nheads / d->nkvheads, units = d->nseq * d->nkvheads * ((group + 15) / 16);
     const int64_t keys = d->max_pages * d->page_size;
-    if (keys <= kWideKeys && units >= 128 && units < 512) return {1, 1};
+    const bool full_lds = d->headdim * (d->dtype == SSD_BF16 ? 2 : 4) >= 512;
+    if (keys <= (full_lds && units < 256 ? kWideKeysFullLds : kWideKeys) && units >= 128 && units < 512) return {1, 1};
     int64_t n = units > 0 ? (1024 + units - 1) / units : 1;
     const int64_t most = (keys + 127) / 128;
     if (n > most) n = most;

@@ -131,3 +131,13 @@ def test_a_table_without_rows_is_refused():
     for table in (torch.zeros(0, 4), torch.zeros(1, 4), torch.zeros(4)):
         with pytest.raises(ValueError, match="buckets"):
             attention._bias_args(None, table, 4, cpu)
+
+
+def test_short_caches_are_split_where_eight_waves_fill_a_cu(lib):
+    """Eight waves a workgroup need no workspace; in fp32 at 128 wide only where that is faster than splitting."""
+    def need(**kw):
+        return ssd.ssd_attn_decode_workspace_bytes(_cache(**dict(dict(nseq=16, nheads=32, nkvheads=8, headdim=128, page_size=64), **kw)))
+
+    assert need(dtype=1, max_pages=16) == 0 and need(dtype=0, headdim=64, max_pages=16) == 0
+    assert need(dtype=0, max_pages=16) > 0 and need(dtype=0, max_pages=4) == 0
+    assert need(dtype=0, max_pages=16, nseq=32) == 0 and need(dtype=0, max_pages=17, nseq=32) > 0
