@@ -29,10 +29,11 @@ struct AttnBuckets {
 // bytes of a row.  A split workgroup's tiles take most of a CU's LDS from rows of 256 bytes on, so that it
 // stays alone there, and half of it below.  bf16, causal, one sequence, forward / dq / dk and dv in us,
 // split against not:
-//     64 wide, 4096 tokens   256 workgroups 46 / 51 / 64 against 74 / 83 / 111, 512: 83 / 90 / 120 against 79 / 91 / 123
-//     64 wide, 1024 tokens   256: 21 / 24 / 29 against 23 / 26 / 34,            512: 37 / 43 / 53 against 25 / 31 / 38
-//     128 wide, 4096 tokens  128: 51 / 52 / 68 against 82 / 114 / 143,          256: 93 / 97 / 127 against 84 / 119 / 148
-//     128 wide, 1024 tokens  128: 23 / 25 / 29 against 26 / 35 / 43,            256: 44 / 48 / 56 against 28 / 39 / 46
+//     64 wide, 4096 tokens   256 workgroups 48 / 57 / 64 against 68 / 96 / 112, 512: 88 / 101 / 123 against 73 / 105 / 120
+//     64 wide, 1024 tokens   256: 22 / 25 / 29 against 22 / 30 / 34, 512: 39 / 46 / 53 against 24 / 35 / 39
+//     128 wide, 4096 tokens  128: 52 / 58 / 68 against 85 / 113 / 129, 256: 99 / 110 / 129 against 87 / 120 / 136
+//     128 wide, 1024 tokens  128: 23 / 27 / 29 against 26 / 37 / 38, 256: 45 / 52 / 57 against 28 / 42 / 42
+// (In fp32 both widths would gain from splitting at 256 still: 64 wide, 1024 tokens, 68 / 90 / 112 against 83 / 115 / 157.)
 inline int64_t attn_split_below(int row_bytes) { return row_bytes >= 256 ? 256 : 384; }
 // HIP counts the threads of a launch in 32 bits; calls past that are refused before their first launch.
 inline bool launchable(int64_t groups, int threads) { return groups * threads < ((int64_t)1 << 32); }
