@@ -21,9 +21,10 @@
 // what that column of the row is.  (The vote costs 0.3 us of the 11.5 of 256 tokens of one head, and nothing that 2 ms of
 // a long prompt show.)
 //
-// Measured: 16384 tokens, 32/4 heads of 128, causal, bf16: 2.13 ms, 1.03 PFLOP/s, bound by MFMA (86% of what an
-// 8192^3 matrix product reaches).  8 x 2048 tokens, 24 heads of 64, capped: 187 us, 550 TFLOP/s, bound by VALU: a
-// score costs 11 instructions, one of them an exponential of four issue slots, against 4 MFMA cycles a lane.
+// Measured: 16384 tokens, 32/4 heads of 128, causal, bf16: 2.10 to 2.25 ms from box to box, 0.98 to 1.04 PFLOP/s, 81 to 86% of
+// what an 8192^3 matrix product reaches; MFMA is busy for 52% of its cycles and VALU for 53%, in turns.  8 x 2048 tokens,
+// 24 heads of 64, capped: 182 to 200 us, 530 TFLOP/s, bound by VALU (84% of the cycles in which a CU has a wave, which are
+// 82%): a score costs 11 instructions, one of them an exponential of four issue slots, against 4 MFMA cycles a lane.
 // The tile: 32 queries a wave and 64 keys read LDS at half its rate when MFMA is full and leave registers for two
 // (128-wide heads) or three waves a SIMD; 32 keys at a time measured 2.30 against 2.17 ms at 128 wide.
 #include "ssd_attn_common.h"

@@ -16,15 +16,16 @@
 // has one dominating key, or keys and values a common part: dq off by 6e-2 at a mean of 2, or at a weight of 0.99 on one
 // key of 2048.  The sum of a row's dS is e_i (with a bf16 dS, its own roundings' sum beside it), known after the pass, and
 // with the sum of p k beside that of dS k dq is put right at the end, for one product more and registers (MEAN): 1.7e-3 to
-// 2.3e-3 in all those cases.  The gradient of the table sums dS over whole diagonals, where e_i counts for every row: with D
+// 2.3e-3 in all those cases (capped, where the unrounded dS is summed, 4e-3 at that mean).  The gradient of the table sums dS over whole diagonals, where e_i counts for every row: with D
 // exact after the pass far cells (which share a bucket: |distance| >= max_distance) are corrected by the sum of their p,
 // and the tiles near the diagonal are visited once more, for the table alone.  For 128-wide heads with a table the sum of
 // p k would take a wave's room on each SIMD, and a pass over S and dP comes before instead (PASS), after which the
 // diagonals are summed as dS comes up, as in fp32, whose y needs none of this.
 //
-// Measured in profiled runs, bf16: 8 x 2048 tokens, 24 heads of 64, capped: dq 335 us, dk and dv 365 us;
-// 16385 packed tokens, 16/4 heads of 128, buckets: dq 265 us, dk and dv 244 us (530 us with four waves a workgroup and
-// tiles in the order of the documents), table 8 us, plan 7 us.
+// Measured in profiled runs, bf16: 8 x 2048 tokens, 24 heads of 64, capped: dq 300 to 390 us, dk and dv 322 to 428 us (the
+// first passes are the long ones); 16385 packed tokens, 16/4 heads of 128, buckets: dq 266 us, dk and dv 244 us at best (530 us
+// with four waves a workgroup and tiles in the order of the documents), table 9 us, plan 7 us.  dk and dv of small fp32 problems at 128 wide spill 33 to 92
+// registers, and are faster than the kernel that does not (1024 tokens, 16 heads: 139 us with the join against 266).
 #include <type_traits>
 
 #include "ssd_attn_common.h"

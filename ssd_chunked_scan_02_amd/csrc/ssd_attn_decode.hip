@@ -11,7 +11,9 @@
 // device, so a captured graph stays balanced as the cache grows.
 //
 // Measured: 64 sequences of up to 8192 keys, 64/8 heads of 128, bf16: 246 us and 4 for the join, 4.8 TB/s
-// (a large copy reaches 5.1); 17 sequences of up to 4001 keys, 24 heads of 64, fp32: 111 us, 4.6 TB/s.
+// (a large copy reaches 5.1); 17 sequences of up to 4001 keys, 24 heads of 64, fp32: 111 us, 4.6 TB/s.  In fp32 at 128 wide
+// the two blocks that a wave holds are 15 to 21 registers too many, which it spills: 62 sequences of 1000 keys, 8 key heads:
+// 126 us, 4.0 TB/s.
 //
 // kv_append_kernel copies one token's keys and values into its page, rotated: bound by memory (16385 tokens, 32/8 heads
 // of 128: 81 us, 5.0 TB/s), and for a decode step by its launch (64 tokens: 6 us).
