@@ -256,7 +256,8 @@ def _with_rest(y, places, at, n, seen, group):
 
 @pytest.mark.parametrize("heads", HEADS)
 @pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("fp32", 32), ("fp32", 64), ("fp32", 128)])
-@pytest.mark.parametrize("how", [{}, dict(prefix=140), dict(cap=50.0), dict(bias="buckets"), dict(causal=False)], ids=str)
+@pytest.mark.parametrize("how", [{}, dict(prefix=140), dict(cap=50.0), dict(bias="buckets"), dict(causal=False), dict(cap=60.0),
+                                 dict(bias="slopes"), dict(bias="slopes", cap=5.0), dict(bias="buckets", cap=5.0)], ids=str)
 def test_columns_of_seen_and_hidden_values_are_told_apart(dtype, D, heads, how):
     """Infinities and NaN of V in single columns: a row has those that it sees, in their columns, and its other columns,
     and every column of rows that see none, are as they are without them, to the bit."""
@@ -264,7 +265,8 @@ def test_columns_of_seen_and_hidden_values_are_told_apart(dtype, D, heads, how):
     lens, at, n = [33, 300, 20], 33, 300
     d = make(26 + D, sum(lens), sum(lens), H, Hk, D, dtype, bias=how.get("bias", "none"))
     pre = how.get("prefix", 0 if how.get("causal", True) else n)
-    args = dict(causal=how.get("causal", True), softcap=how.get("cap", 0.0), table=None if d["table"] is None else d["table"].cuda(),
+    args = dict(causal=how.get("causal", True), softcap=how.get("cap", 0.0),
+                **{x: None if d[x] is None else d[x].cuda() for x in ("slopes", "table")},
                 prefix=torch.tensor([0, pre, 0], dtype=torch.int64).cuda() if "prefix" in how else None)
     bad, good, places = _not_finite(d["v"], at)
     q, k, cu = d["q"].cuda(), d["k"].cuda(), offsets(lens).cuda()
