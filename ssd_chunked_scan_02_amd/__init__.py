@@ -34,6 +34,8 @@ and, from ``include/ssd_attn.h`` (``attention.py``), the attention layer of a hy
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -203,9 +205,27 @@ def _on_stream(stream, *tensors):
             t.record_stream(stream)
 
 
+def _in_stream(function):
+    """With ``stream`` given, ``function`` runs with it as torch's current stream: what it allocates comes from that
+    stream's pool.  A block that was just freed on another stream may still be in use by what is queued there, which
+    the call would not wait for."""
+    at = list(inspect.signature(function).parameters).index("stream")
+
+    @functools.wraps(function)
+    def call(*args, **kwargs):
+        stream = kwargs.get("stream") if len(args) <= at else args[at]
+        if stream is None:
+            return function(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return function(*args, **kwargs)
+
+    return call
+
+
 SSD_MAX_LAUNCHES = 4
 
 
+@_in_stream
 def ssd_forward(x, log_a, B, C, D=None, chunk: int = 64, init_state=None, y=None,
                 final_state=None, workspace=None, stream=None):
     """Run ``ssd_forward`` on the GPU.
@@ -216,6 +236,7 @@ def ssd_forward(x, log_a, B, C, D=None, chunk: int = 64, init_state=None, y=None
     return _forward(x, log_a, B, C, D, chunk, init_state, y, final_state, workspace, stream)[:2]
 
 
+@_in_stream
 def ssd_forward_profiled(x, log_a, B, C, D=None, chunk: int = 64, init_state=None, y=None,
                          final_state=None, workspace=None, stream=None, events=()):
     """``ssd_forward_profiled``: as ssd_forward; launch k stamps the hipEvent_t handles
@@ -273,6 +294,7 @@ def ssd_noalloc_scratch_bytes() -> int:
     return int(load_library().ssd_noalloc_scratch_bytes())
 
 
+@_in_stream
 def ssd_forward_noalloc(x, log_a, B, C, D=None, chunk: int = 64, init_state=None, y=None, final_state=None,
                         stream=None):
     """Run ``ssd_forward_noalloc``: ssd_forward with its workspace in the library's fixed per-GPU
@@ -325,6 +347,7 @@ def ssd_forward_varlen_workspace_bytes(dims: Dims, chunk: int) -> int:
     return int(load_library().ssd_forward_varlen_workspace_bytes(ctypes.byref(dims), int(chunk)))
 
 
+@_in_stream
 def ssd_forward_varlen(x, log_a, B, C, cu_seqlens, max_seqlen: int, D=None, chunk: int = 64, init_state=None,
                        y=None, final_state=None, workspace=None, stream=None, events=None):
     """Run ``ssd_forward_varlen``: a packed batch of len(cu_seqlens) - 1 sequences, sequence i
@@ -378,6 +401,7 @@ def ssd_forward_dt_varlen_workspace_bytes(dims: Dims, chunk: int, scale_input: b
                                                                     1 if scale_input else 0))
 
 
+@_in_stream
 def ssd_forward_dt_varlen(x, dt, A_log, B, C, cu_seqlens, max_seqlen: int, D=None, dt_bias=None,
                           scale_input: bool = True, chunk: int = 64, init_state=None, y=None, final_state=None,
                           workspace=None, stream=None, events=None):
@@ -435,6 +459,7 @@ def ssd_forward_dt_workspace_bytes(dims: Dims, chunk: int, scale_input: bool = T
                                                              1 if scale_input else 0))
 
 
+@_in_stream
 def ssd_forward_dt(x, dt, A_log, B, C, D=None, dt_bias=None, scale_input: bool = True,
                    chunk: int = 64, init_state=None, y=None, final_state=None, workspace=None,
                    stream=None):
@@ -446,6 +471,7 @@ def ssd_forward_dt(x, dt, A_log, B, C, D=None, dt_bias=None, scale_input: bool =
                        final_state, workspace, stream)[:2]
 
 
+@_in_stream
 def ssd_forward_dt_profiled(x, dt, A_log, B, C, D=None, dt_bias=None, scale_input: bool = True,
                             chunk: int = 64, init_state=None, y=None, final_state=None,
                             workspace=None, stream=None, events=()):
@@ -506,6 +532,7 @@ def _forward_dt(x, dt, A_log, B, C, D, dt_bias, scale_input, chunk, init_state, 
     return y, final_state, launches
 
 
+@_in_stream
 def ssd_step_dt(state, x_t, dt_t, A_log, B_t, C_t, D=None, dt_bias=None, scale_input: bool = True,
                 y_t=None, stream=None):
     """Run ``ssd_step_dt``: one token with the discretisation front-end, ``state`` updated in
@@ -542,6 +569,7 @@ def ssd_backward_workspace_bytes(dims: Dims) -> int:
     return int(load_library().ssd_backward_workspace_bytes(ctypes.byref(dims)))
 
 
+@_in_stream
 def ssd_backward_profiled(x, log_a, B, C, dy, D=None, init_state=None, dfinal=None, want_dD=True,
                           want_dinit=True, workspace=None, stream=None, events=()):
     """``ssd_backward_profiled``: as ssd_backward, launch k stamping events[2k] and events[2k+1].
@@ -550,6 +578,7 @@ def ssd_backward_profiled(x, log_a, B, C, dy, D=None, init_state=None, dfinal=No
                         stream, _events=list(events))
 
 
+@_in_stream
 def ssd_backward(x, log_a, B, C, dy, D=None, init_state=None, dfinal=None, want_dD=True,
                  want_dinit=True, workspace=None, stream=None, _events=None):
     """Run ``ssd_backward``: gradients of <dy, y> + <dfinal, final_state> for the forward pass
@@ -595,6 +624,7 @@ def ssd_backward(x, log_a, B, C, dy, D=None, init_state=None, dfinal=None, want_
     return out if _events is None else (out, count.value)
 
 
+@_in_stream
 def ssd_backward_varlen(x, log_a, B, C, dy, cu_seqlens, max_seqlen: int, D=None, init_state=None, dfinal=None,
                         want_dD=True, want_dinit=True, workspace=None, stream=None, events=None):
     """Run ``ssd_backward_varlen``: gradients of <dy, y> + <dfinal, final_states> for
@@ -640,6 +670,7 @@ def ssd_backward_varlen(x, log_a, B, C, dy, cu_seqlens, max_seqlen: int, D=None,
     return out
 
 
+@_in_stream
 def ssd_backward_dt(x, dt, A_log, B, C, dy, D=None, dt_bias=None, scale_input: bool = True,
                     init_state=None, dfinal=None, want_dD=True, want_dinit=True, workspace=None,
                     stream=None):
@@ -687,6 +718,7 @@ def ssd_backward_dt(x, dt, A_log, B, C, dy, D=None, dt_bias=None, scale_input: b
     return out
 
 
+@_in_stream
 def ssd_backward_dt_varlen(x, dt, A_log, B, C, dy, cu_seqlens, max_seqlen: int, D=None, dt_bias=None,
                            scale_input: bool = True, init_state=None, dfinal=None, want_dD=True, want_dinit=True,
                            workspace=None, stream=None):
@@ -736,6 +768,7 @@ def ssd_backward_dt_varlen(x, dt, A_log, B, C, dy, cu_seqlens, max_seqlen: int, 
     return out
 
 
+@_in_stream
 def ssd_step(state, x_t, log_a_t, B_t, C_t, D=None, y_t=None, stream=None):
     """Run ``ssd_step``: one token for every (batch, head), ``state`` updated in place.
     state [B,H,N,P] fp32; x_t [B,H,P]; log_a_t [B,H] or [B,H,N]; B_t, C_t [B,G,N]."""
