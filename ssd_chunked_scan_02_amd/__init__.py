@@ -670,6 +670,10 @@ def ssd_backward_varlen(x, log_a, B, C, dy, cu_seqlens, max_seqlen: int, D=None,
     return out
 
 
+def ssd_backward_dt_workspace_bytes(dims: Dims, scale_input: bool = True) -> int:
+    return int(load_library().ssd_backward_dt_workspace_bytes(ctypes.byref(dims), int(bool(scale_input))))
+
+
 @_in_stream
 def ssd_backward_dt(x, dt, A_log, B, C, dy, D=None, dt_bias=None, scale_input: bool = True,
                     init_state=None, dfinal=None, want_dD=True, want_dinit=True, workspace=None,

@@ -1,4 +1,4 @@
-"""Where the binding's own tensors come from when a call is given a stream."""
+"""The binding as a whole: its names, and where its own tensors come from when a call is given a stream."""
 import contextlib
 import inspect
 
@@ -35,9 +35,13 @@ def test_a_given_stream_is_the_current_one_during_a_call(monkeypatch):
 def test_every_function_with_a_stream_allocates_from_it():
     """The scan's functions by the decorator, the attention layer's by their own allocation."""
     for name in ssd.__all__:
-        f = getattr(ssd, name, None)
+        f = getattr(ssd, name)
         if callable(f) and not inspect.isclass(f) and "stream" in inspect.signature(f).parameters and "attn" not in name and name != "ssd_kv_append":
             assert hasattr(f, "__wrapped__"), name
+
+
+def test_every_name_of_the_package_is_there():
+    assert [n for n in ssd.__all__ if not hasattr(ssd, n)] == []
 
 
 @pytest.mark.gpu
