@@ -30,6 +30,12 @@ and, from ``include/ssd_attn.h`` (``attention.py``), the attention layer of a hy
   ssd_attn_decode_workspace_bytes(dims) -> int
   ssd_attn_decode(q, k_cache, v_cache, block_table, seq_lens, ...) -> y
   ssd_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, ...) -> rotated q or None
+and, from ``include/ssd_delta.h`` (``delta.py``), the gated delta rule:
+  ssd_delta_forward_workspace_bytes(dims) -> int
+  ssd_delta_forward(q, k, v, log_a, beta, cu_seqlens=None, ..., final_state=None) -> (y, final_state)
+  ssd_delta_backward_workspace_bytes(dims) -> int
+  ssd_delta_backward(q, k, v, log_a, beta, dy, cu_seqlens=None, ...) -> dict of gradients
+  ssd_delta_step(state, q_t, k_t, v_t, log_a_t, beta_t, ...) -> y_t
 """
 from __future__ import annotations
 
@@ -48,6 +54,8 @@ __all__ = ["SSDError", "Dims", "library_path", "load_library", "dims_for",
            "ssd_forward_noalloc", "ssd_noalloc_scratch_bytes", "ssd_strerror",
            "ssd_attn_forward", "ssd_attn_backward", "ssd_attn_backward_workspace_bytes",
            "ssd_attn_decode", "ssd_attn_decode_workspace_bytes", "ssd_kv_append",
+           "ssd_delta_forward", "ssd_delta_forward_workspace_bytes", "ssd_delta_backward",
+           "ssd_delta_backward_workspace_bytes", "ssd_delta_step",
            "SSD_F32", "SSD_BF16", "SSD_DECAY_SCALAR", "SSD_DECAY_DIAG"]
 
 SSD_F32, SSD_BF16 = 0, 1
@@ -145,6 +153,7 @@ def load_library():
         lib.ssd_strerror.argtypes = [i32]
         lib.ssd_strerror.restype = ctypes.c_char_p
         attention.declare(lib)
+        delta.declare(lib)
         _LIB = lib
     return _LIB
 
@@ -806,3 +815,7 @@ from . import attention  # noqa: E402  (its functions use the helpers above)
 from .attention import (  # noqa: E402
     ssd_attn_backward, ssd_attn_backward_workspace_bytes, ssd_attn_decode,
     ssd_attn_decode_workspace_bytes, ssd_attn_forward, ssd_kv_append)
+from . import delta  # noqa: E402
+from .delta import (  # noqa: E402
+    ssd_delta_backward, ssd_delta_backward_workspace_bytes, ssd_delta_forward,
+    ssd_delta_forward_workspace_bytes, ssd_delta_step)
