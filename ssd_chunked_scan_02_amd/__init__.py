@@ -36,6 +36,14 @@ and, from ``include/ssd_delta.h`` (``delta.py``), the gated delta rule:
   ssd_delta_backward_workspace_bytes(dims) -> int
   ssd_delta_backward(q, k, v, log_a, beta, dy, cu_seqlens=None, ...) -> dict of gradients
   ssd_delta_step(state, q_t, k_t, v_t, log_a_t, beta_t, ...) -> y_t
+and, from ``include/ssd_kv8.h`` (``kv8.py``), the attention layer's paged cache in 8 bits:
+  ssd_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, ...) -> rotated q or None
+  ssd_kv8_decode_workspace_bytes(dims) -> int
+  ssd_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, ...) -> y
+  ssd_kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, tokens, ...) -> (k, v)
+and, from ``include/ssd_rotary.h`` (``rotary.py``), rotary positions:
+  ssd_rotate(q, inv_freq, cu_seqlens=None, start=None, k=None, ..., inverse=False) -> (q, k)
+  ssd_rotary_frequencies(dim, base=..., factor=..., how=...) -> (inv_freq, magnitude)
 """
 from __future__ import annotations
 
@@ -56,6 +64,8 @@ __all__ = ["SSDError", "Dims", "library_path", "load_library", "dims_for",
            "ssd_attn_decode", "ssd_attn_decode_workspace_bytes", "ssd_kv_append",
            "ssd_delta_forward", "ssd_delta_forward_workspace_bytes", "ssd_delta_backward",
            "ssd_delta_backward_workspace_bytes", "ssd_delta_step",
+           "ssd_kv8_append", "ssd_kv8_decode", "ssd_kv8_decode_workspace_bytes", "ssd_kv8_read",
+           "ssd_rotate", "ssd_rotary_frequencies",
            "SSD_F32", "SSD_BF16", "SSD_DECAY_SCALAR", "SSD_DECAY_DIAG"]
 
 SSD_F32, SSD_BF16 = 0, 1
@@ -154,6 +164,8 @@ def load_library():
         lib.ssd_strerror.restype = ctypes.c_char_p
         attention.declare(lib)
         delta.declare(lib)
+        kv8.declare(lib)
+        rotary.declare(lib)
         _LIB = lib
     return _LIB
 
@@ -819,3 +831,8 @@ from . import delta  # noqa: E402
 from .delta import (  # noqa: E402
     ssd_delta_backward, ssd_delta_backward_workspace_bytes, ssd_delta_forward,
     ssd_delta_forward_workspace_bytes, ssd_delta_step)
+from . import kv8  # noqa: E402
+from .kv8 import (  # noqa: E402
+    ssd_kv8_append, ssd_kv8_decode, ssd_kv8_decode_workspace_bytes, ssd_kv8_read)
+from . import rotary  # noqa: E402
+from .rotary import ssd_rotary_frequencies, ssd_rotate  # noqa: E402

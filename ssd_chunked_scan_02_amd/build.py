@@ -21,8 +21,9 @@ DEVICE_FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
                 "-Wall", "-Wno-unused-result"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall"]
 DEVICE_SOURCES = ["ssd_kernels.hip", "ssd_fast.hip", "ssd_diag.hip", "ssd_bwd.hip", "ssd_noalloc.hip",
-                  "ssd_attn.hip", "ssd_attn_bwd.hip", "ssd_attn_decode.hip", "ssd_delta.hip", "ssd_delta_bwd.hip"]
-HOST_SOURCES = ["ssd_api.cpp", "ssd_attn_api.cpp", "ssd_delta_api.cpp"]
+                  "ssd_attn.hip", "ssd_attn_bwd.hip", "ssd_attn_decode.hip", "ssd_delta.hip", "ssd_delta_bwd.hip",
+                  "ssd_kv8.hip", "ssd_rotary.hip"]
+HOST_SOURCES = ["ssd_api.cpp", "ssd_attn_api.cpp", "ssd_delta_api.cpp", "ssd_kv8_api.cpp"]
 
 
 def _run(cmd):

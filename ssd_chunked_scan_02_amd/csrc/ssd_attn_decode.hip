@@ -18,6 +18,7 @@
 // kv_append_kernel copies one token's keys and values into its page, rotated: bound by memory (16385 tokens, 32/8 heads
 // of 128: 81 us, 5.0 TB/s), and for a decode step by its launch (64 tokens: 6 us).
 #include "ssd_attn_common.h"
+#include "ssd_attn_join.h"
 
 namespace ssd {
 namespace attn {
@@ -251,27 +252,6 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) attn_decode_
     }
 }
 
-// y of one (sequence, head) from its splits; a workgroup takes kThreads / (D / 4) of them.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(DecodeParams p, int64_t units) {
-    constexpr int PER = D / 4;
-    const int64_t at = (int64_t)blockIdx.x * (kThreads / PER) + threadIdx.x / PER;
-    if (at >= units) return;
-    const int d = 4 * (int)(threadIdx.x % PER);
-    const float* ml = p.part_ml + at * p.splits * 2;
-    float top = kNoMax;
-    for (int i = 0; i < p.splits; ++i) top = fmaxf(top, ml[2 * i]);
-    float sum = 0.f;
-    f32x4 v{};
-    for (int i = 0; i < p.splits; ++i) {
-        const float f = exp2_hw(ml[2 * i] - top);
-        sum += f * ml[2 * i + 1];
-        v += f * as_f32x4(ld16(p.part_o + (at * p.splits + i) * D + d));
-    }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    store4(static_cast<T*>(p.y) + at * D + d, v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-}
-
 template <typename T, int D, bool CAP, int BIAS, int NW>
 int launch_decode(const DecodeParams& p, hipStream_t stream) {
     const int64_t group = p.H / p.Hk, grid = p.nseq * p.Hk * ((group + kG - 1) / kG) * p.splits;
@@ -282,13 +262,7 @@ int launch_decode(const DecodeParams& p, hipStream_t stream) {
         return -1;
     hipLaunchKernelGGL((attn_decode_kernel<T, D, CAP, BIAS, NW>), dim3((unsigned)grid), dim3(NW * kWave), lds, stream, p);
     if (hipGetLastError() != hipSuccess) return -1;
-    if (p.splits > 1) {
-        const int64_t units = p.nseq * p.H;
-        const int per = kThreads / (D / 4);
-        hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((units + per - 1) / per)), dim3(kThreads), 0, stream, p, units);
-        if (hipGetLastError() != hipSuccess) return -1;
-    }
-    return 0;
+    return p.splits > 1 ? launch_join<T, D>(p, stream) : 0;
 }
 template <typename T, int D, bool CAP, int BIAS>
 int launch_decode(const DecodeParams& p, hipStream_t stream) {

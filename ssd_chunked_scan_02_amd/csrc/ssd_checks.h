@@ -1,4 +1,4 @@
-// Argument checks that the C entry points of the delta rule, the 8-bit cache and the rotation share (host only).
+// Argument checks that the C entry points of the attention layer, the delta rule, the 8-bit cache and the rotation share (host only).
 #pragma once
 
 #include <stddef.h>
@@ -37,7 +37,8 @@ template <size_t N, size_t M> bool shared(const void* const (&outputs)[N], const
     return false;
 }
 
-// Elements from one token to the next, as given or dense.
+// Elements from one token to the next, as given or dense (a tile's byte offsets are 32-bit: 64 rows of up to 2^24
+// four-byte elements).
 inline int stride(int64_t given, int64_t dense, int64_t elem, int64_t& out) {
     if (given == 0) {
         out = dense;
