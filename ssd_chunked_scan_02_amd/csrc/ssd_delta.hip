@@ -15,12 +15,12 @@ template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepParams p) {
     constexpr int R = N / 32;
     __shared__ float part[kWaves][8][9];
-    const int blocks = p.P / kCols, cb = (int)(blockIdx.x % blocks);
+    const int blocks = p.P / kDeltaCols, cb = (int)(blockIdx.x % blocks);
     const int64_t sh = blockIdx.x / blocks, s = sh / p.H;
     const int h = (int)(sh % p.H), grp = h / (p.H / p.G), c4 = threadIdx.x % 8, rg = threadIdx.x / 8;
     const T* kp = static_cast<const T*>(p.k) + s * p.k_stride + grp * N;
     const T* qp = static_cast<const T*>(p.q) + s * p.q_stride + grp * N;
-    float* state = p.state + (sh * N) * p.P + cb * kCols + 4 * c4;
+    float* state = p.state + (sh * N) * p.P + cb * kDeltaCols + 4 * c4;
     const float a = expf(p.log_a[sh]), beta = p.beta[sh];
     f32x4 x[R];
     float k[R];
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepParams p)
         }
         kq += part[w][c4][8];
     }
-    const int64_t col = (int64_t)h * p.P + cb * kCols + 4 * c4;
+    const int64_t col = (int64_t)h * p.P + cb * kDeltaCols + 4 * c4;
     const T* vp = static_cast<const T*>(p.v) + s * p.v_stride + col;
     f32x4 u;
 #pragma unroll
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepParams p)
 
 template <typename T, int N>
 int launch_step(const DeltaStepParams& p, hipStream_t stream) {
-    hipLaunchKernelGGL((delta_step_kernel<T, N>), dim3((unsigned)(p.nseq * p.H * (p.P / kCols))), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((delta_step_kernel<T, N>), dim3((unsigned)(p.nseq * p.H * (p.P / kDeltaCols))), dim3(kThreads), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

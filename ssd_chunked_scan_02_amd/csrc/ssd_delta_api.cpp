@@ -23,9 +23,9 @@ int check_dims(const ssd_delta_dims* d, bool step) {
     if ((d->keydim != 32 && d->keydim != 64 && d->keydim != 128) || d->valuedim % ssd::kDeltaCols != 0 || d->valuedim > 256)
         return SSD_ERR_UNSUPPORTED;
     if (d->ngroups * d->keydim >= ((int64_t)1 << 24) || d->nheads * d->valuedim >= ((int64_t)1 << 24)) return SSD_ERR_UNSUPPORTED;
-    const int64_t walks = d->nseq * d->nheads * (d->valuedim / ssd::kDeltaCols) + 8;
+    const int64_t walks = d->nseq * d->nheads * (d->valuedim / 16) + 8;
     const int64_t chunks = step ? 0 : ssd::delta_slots(d->total, d->nseq) * d->ngroups;
-    if (!launchable(walks, 256) || !launchable(chunks, 256)) return SSD_ERR_UNSUPPORTED;
+    if (!launchable(walks, 256) || !launchable(chunks, 512)) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
@@ -37,6 +37,14 @@ int strides(const ssd_delta_dims* d, int64_t& q, int64_t& k, int64_t& v) {
     return rc;
 }
 
+// Columns of a walk's workgroup.  With 32 each load of K, Q, Z and the scores serves twice the columns, with 16 the steps
+// of a chunk are shorter: 16 where its workgroups still have one of the 256 CUs each.  Forward and training step of one
+// sequence of 2048 tokens, us, 16 against 32 columns:
+//     bf16, 64 by 64     128 workgroups of 16 73/292 against 95/363, 256: 83/404 against 102/449, 384: 127/607 against 121/534
+//     bf16, 128 by 128   128: 76/329 against 101/422, 256: 88/459 against 113/512, 384: 116/651 against 121/592
+//     fp32, 128 by 128   128: 123/562 against 197/704, 256: 147/735 against 221/857, 384: 225/1262 against 237/972
+int walk_columns(const ssd_delta_dims* d) { return d->nseq * d->nheads * (d->valuedim / 16) <= 256 ? 16 : 32; }
+
 // Lays the workspace out from `base` (null: only its size is wanted), and returns its bytes.
 size_t lay_out(const ssd_delta_dims* d, bool backward, char* base, ssd::DeltaParams& p) {
     size_t at = 0;
@@ -47,16 +55,16 @@ size_t lay_out(const ssd_delta_dims* d, bool backward, char* base, ssd::DeltaPar
     };
     const size_t elem = d->dtype == SSD_BF16 ? 2 : 4, terms = d->dtype == SSD_BF16 ? 3 : 1;
     const size_t slots = (size_t)ssd::delta_slots(d->total, d->nseq), H = (size_t)d->nheads, G = (size_t)d->ngroups;
-    const size_t N = (size_t)d->keydim, P = (size_t)d->valuedim, C = ssd::kDeltaChunk, blocks = P / ssd::kDeltaCols;
+    const size_t N = (size_t)d->keydim, P = (size_t)d->valuedim, C = ssd::kDeltaChunk, blocks = P / (size_t)walk_columns(d);
     if (d->total == 0 || d->nseq == 0) return 0;
     p.z = take(slots * H * terms * C * C * elem);
-    p.scores = take(slots * H * (backward ? terms : 1) * C * C * elem);
-    p.kt = take(slots * G * N * C * elem);
+    p.scores = take(slots * H * (backward || terms == 1 ? terms : 2) * C * C * elem);
+    p.kr = take(slots * G * N * C * elem);
+    p.qr = take(slots * G * N * C * elem);
     p.gates = reinterpret_cast<float*>(take(slots * H * ssd::kDeltaGates * C * 4));
     if (!backward) return at;
     p.zt = take(slots * H * terms * C * C * elem);
     p.scores_t = take(slots * H * terms * C * C * elem);
-    p.qt = take(slots * G * N * C * elem);
     p.states = reinterpret_cast<float*>(take((slots + (size_t)d->nseq) * H * N * P * 4));
     p.wrong = reinterpret_cast<float*>(take((size_t)d->total * H * P * 4));
     p.dstates = take(slots * H * N * P * elem);
@@ -93,6 +101,7 @@ int fill(const ssd_delta_dims* d, const int64_t* cu, const void* q, const void* 
     p.G = (int)d->ngroups;
     p.N = (int)d->keydim;
     p.P = (int)d->valuedim;
+    p.cols = walk_columns(d);
     p.scale = d->scale;
     return SSD_OK;
 }

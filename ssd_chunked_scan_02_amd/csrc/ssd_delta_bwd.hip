@@ -10,6 +10,8 @@
 //            + e^(gC - g_i) dS' u_i - e^g_i S de_i.
 // Four launches: delta_prep_kernel and delta_walk_kernel again (which keep the states before the chunks, e and dy . y),
 // delta_back_kernel down the chunks from the last one, delta_grad_kernel for dq, dk and the sums, all chunks at once.
+#include <type_traits>
+
 #include "ssd_delta_prep.h"
 #include "ssd_delta_walk.h"
 
@@ -17,21 +19,24 @@ namespace ssd {
 namespace delta {
 namespace {
 
-// The gradient of the state, from chunk to chunk towards the first: as delta_walk_kernel, 32 columns a workgroup, the
+// The gradient of the state, from chunk to chunk towards the first: as delta_walk_kernel, 16 or 32 columns a workgroup, the
 // rows split over its waves, every product of fp32 values on operands of all terms.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, N * sizeof(T) >= 256 ? 1 : 2) delta_back_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
+template <typename T, int N, int CT>
+__global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 : 2) delta_back_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
-    constexpr int KN = N / M::kK, KC = kC / M::kK, TERMS = M::kTerms, NT = StateRows<N>::NT;
+    constexpr int KN = N / M::kK, KC = kC / M::kK, TERMS = M::kTerms, NT = StateRows<N, CT>::NT, kCols = 16 * CT;
     constexpr int LS = N + M::kPad, LC = kC + M::kPad, SA = kCols * LS, CA = kCols * LC;
-    // dS' [column][n]; dY [column][token]; of all terms: scale e^g dY, for this chunk and the next, B dU, -e^g dE
+    // dS' [column][n]; dY [column][token]; of all terms: scale e^g dY, for this chunk and the next, B dU, -e^g dE; K and Q
+    // [token][n]
     __shared__ __attribute__((aligned(16))) T sl[TERMS * SA];
     __shared__ __attribute__((aligned(16))) T yl[CA];
     extern __shared__ __attribute__((aligned(16))) char more[];
     T* const wl = reinterpret_cast<T*>(more);
     T* const rl = wl + 2 * TERMS * CA;
     T* const dl = rl + TERMS * CA;
+    T* const kl = dl + TERMS * CA;
+    T* const ql = kl + kC * LS;
 
     const int64_t unit = xcd_work_index(blockIdx.x, per_xcd, units);
     if (unit < 0) return;
@@ -41,67 +46,98 @@ __global__ void __launch_bounds__(kThreads, N * sizeof(T) >= 256 ? 1 : 2) delta_
     const int64_t slot0 = span.lo / kC + s, chunks = (span.len + kC - 1) / kC;
     const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), m = lane % 16, g = lane / 16;
     const int row0 = 16 * w + 4 * g, ks0 = 16 * w / M::kK;  // (steps before ks0 are left of the diagonal: zero)
-    const StateRows<N> rows(w, lane);
+    const StateRows<N, CT> rows(w, lane);
     const int64_t NP = (int64_t)N * p.P, HP = (int64_t)p.H * p.P, vcol = (int64_t)h * p.P + cb * kCols;
 
     f32x4 st[NT][CT];
     rows.load(st, p.dfinal ? p.dfinal + (s * p.H + h) * NP + cb * kCols : nullptr, p.P);
     rows.template share<TERMS>(st, sl, LS, SA);
 
-    Frag kf[KN], zf[KC][TERMS], pf[KC][TERMS], tf[NT][KC], uf[NT][KC];
+    const T *const at_s = sl + m * LS + g * M::kE, *const at_y = yl + m * LC + g * M::kE, *const at_w = wl + m * LC + g * M::kE,
+            *const at_r = rl + m * LC + g * M::kE, *const at_d = dl + m * LC + g * M::kE;
+    Frag kf[KN], qf[KN], zf[KC][TERMS], pf[KC][TERMS];
     f32x4 in, out, be, ahead, after[NT][CT];  // ahead: e^g of the chunk whose dY is loaded
     float all;
     T vv[4][CT], yv[4][CT];
     float ee[4][CT];
-    const auto have_of = [&](int64_t c) { return span.len - c * kC < kC ? span.len - c * kC : (int64_t)kC; };
-    const auto load_rows = [&](int64_t c) {
-        const Rows<T> kr(static_cast<const T*>(p.k) + (span.lo + c * kC) * p.k_stride + grp * N, have_of(c), p.k_stride, N);
+    constexpr uint32_t kStep = kWave * 16;  // bytes of an operand of all lanes
+    const int64_t end = chunks - 1, kept = chunks > 0 ? end : 0;  // (the chunks are taken from the last one on)
+    const auto to_last = [&](Chunks x) {
+        x.base += kept * x.step;
+        return x;
+    };
+    Chunks vc = to_last(Chunks(static_cast<const T*>(p.v) + span.lo * p.v_stride + vcol, span.len, p.v_stride, kCols));
+    Chunks yc = to_last(Chunks(static_cast<const T*>(p.dy) + span.lo * HP + vcol, span.len, HP, kCols));
+    Chunks oc = to_last(Chunks(static_cast<const T*>(p.dv) + span.lo * HP + vcol, span.len, HP, kCols));
+    Chunks ec = to_last(Chunks(p.wrong + span.lo * HP + vcol, span.len, HP, kCols));
+    constexpr int64_t kMat = TERMS * kC * kC * sizeof(T), kCol = N * kC * sizeof(T), kGate = kDeltaGates * kC;
+    const int64_t slot = slot0 + kept;
+    const char* zc = static_cast<const char*>(p.zt) + (slot * p.H + h) * kMat + w * KC * kStep;
+    const char* pc = static_cast<const char*>(p.scores_t) + (slot * p.H + h) * kMat + w * KC * kStep;
+    const int64_t row_at = (slot * p.G + grp) * kCol + w * KN * kStep;
+    const char *kc = static_cast<const char*>(p.kr) + row_at, *qc = static_cast<const char*>(p.qr) + row_at;
+    const float *gc = p.gates + (slot * p.H + h) * kGate, *hc = gc;  // hc: of the chunk whose dY is loaded
+    const float* sc = p.states + ((slot + 1 + s) * p.H + h) * NP + cb * kCols;
+    T* dc = static_cast<T*>(p.dstates) + (slot * p.H + h) * NP + cb * kCols;
+    const uint32_t own = lane * 16, four = row0 * 4;
+    uint32_t vat[4], yat[4];
 #pragma unroll
-        for (int i = 0; i < KN; ++i) kf[i] = kr.frag(16 * w + m, i * M::kK + g * M::kE);
-        const T* sc = static_cast<const T*>(p.scores_t) + ((slot0 + c) * p.H + h) * (int64_t)(TERMS * kC * kC) + (w * KC * kWave + lane) * M::kE;
+    for (int e = 0; e < 4; ++e) {
+        vat[e] = (uint32_t)(((row0 + e) * p.v_stride + CT * m) * sizeof(T));
+        yat[e] = (uint32_t)(((row0 + e) * HP + CT * m) * sizeof(T));
+    }
+    // loads of the chunk `back` chunks (1, or 0 before the first one) from the one loaded before, which is the last or not
+    const auto load_rows = [&](int64_t back) {
+        kc -= back * (p.G * kCol);
+        pc -= back * (p.H * kMat);
+        qc -= back * (p.G * kCol);
+        const Block kr(kc), qr(qc), s(pc);
+#pragma unroll
+        for (int i = 0; i < KN; ++i) kf[i] = kr.frag<T>(own, i * kStep);
 #pragma unroll
         for (int i = 0; i < KC; ++i)
 #pragma unroll
-            for (int u = 0; u < TERMS; ++u) pf[i][u] = frag(sc + u * (kC * kC) + max(i, ks0) * (kWave * M::kE));
+            for (int u = 0; u < TERMS; ++u) pf[i][u] = s.frag<T>(i < ks0 ? own + ks0 * kStep : own + i * kStep, u * (kC * kC * sizeof(T)));
+#pragma unroll
+        for (int i = 0; i < KN; ++i) qf[i] = qr.frag<T>(own, i * kStep);
     };
-    const auto load_z = [&](int64_t c) {
-        const T* z = static_cast<const T*>(p.zt) + ((slot0 + c) * p.H + h) * (int64_t)(TERMS * kC * kC) + (w * KC * kWave + lane) * M::kE;
+    const auto load_z = [&](int64_t back) {
+        zc -= back * (p.H * kMat);
+        const Block z(zc);
 #pragma unroll
         for (int i = 0; i < KC; ++i)
 #pragma unroll
-            for (int u = 0; u < TERMS; ++u) zf[i][u] = frag(z + u * (kC * kC) + max(i, ks0) * (kWave * M::kE));
+            for (int u = 0; u < TERMS; ++u) zf[i][u] = z.frag<T>(i < ks0 ? own + ks0 * kStep : own + i * kStep, u * (kC * kC * sizeof(T)));
     };
-    const auto load_values = [&](int64_t c) {
-        const float* gates = p.gates + ((slot0 + c) * p.H + h) * (kDeltaGates * kC);
-        in = as_f32x4(ld16(gates + kGateIn * kC + row0));
-        out = as_f32x4(ld16(gates + kGateOut * kC + row0));
-        be = as_f32x4(ld16(gates + kGateBeta * kC + row0));
-        all = gates[kGateIn * kC + kC - 1];
-        const int64_t t0 = span.lo + c * kC;
-        const Rows<T> vr(static_cast<const T*>(p.v) + t0 * p.v_stride + vcol, have_of(c), p.v_stride, kCols);
-        const Rows<float> er(p.wrong + t0 * HP + vcol, have_of(c), HP, kCols);
+    const auto load_values = [&](int64_t back, bool last) {
+        vc.base -= back * vc.step;
+        ec.base -= back * ec.step;
+        const Block vr = vc.block(last), er = ec.block(last);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            vr.load2(row0 + e, 2 * m, vv[e]);
-            er.load2(row0 + e, 2 * m, ee[e]);
+            vr.load<CT>(vat[e], vv[e]);
+            er.load<CT>(yat[e] * (4 / sizeof(T)), ee[e]);
         }
     };
-    const auto load_rest = [&](int64_t c) {
-        const int64_t o = ((slot0 + c) * p.G + grp) * (int64_t)(N * kC) + (rows.tile0 * KC * kWave + lane) * M::kE;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < KC; ++i) {
-                tf[t][i] = frag(static_cast<const T*>(p.kt) + o + (t * KC + i) * (kWave * M::kE));
-                uf[t][i] = frag(static_cast<const T*>(p.qt) + o + (t * KC + i) * (kWave * M::kE));
-            }
+    const auto load_gates = [&](int64_t back) {
+        gc -= back * (p.H * kGate);
+        const Block gr(gc);
+        in = as_f32x4(gr.load16(four, kGateIn * kC * 4));
+        out = as_f32x4(gr.load16(four, kGateOut * kC * 4));
+        be = as_f32x4(gr.load16(four, kGateBeta * kC * 4));
+        all = gc[kGateIn * kC + kC - 1];
     };
-    const auto load_after = [&](int64_t c) { rows.load(after, p.states + ((slot0 + c + 1 + s) * p.H + h) * NP + cb * kCols, p.P); };
-    const auto load_dy = [&](int64_t c) {
-        const Rows<T> yr(static_cast<const T*>(p.dy) + (span.lo + c * kC) * HP + vcol, have_of(c), HP, kCols);
+    const auto load_after = [&](int64_t back) {
+        sc -= back * (p.H * NP);
+        rows.load(after, sc, p.P);
+    };
+    const auto load_dy = [&](int64_t back, bool last) {
+        yc.base -= back * yc.step;
+        hc -= back * (p.H * kGate);
+        const Block yr = yc.block(last);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) yr.load2(row0 + e, 2 * m, yv[e]);
-        ahead = as_f32x4(ld16(p.gates + ((slot0 + c) * p.H + h) * (kDeltaGates * kC) + kGateIn * kC + row0));
+        for (int e = 0; e < 4; ++e) yr.load<CT>(yat[e], yv[e]);
+        ahead = as_f32x4(Block(hc).load16(four, kGateIn * kC * 4));
     };
     const auto share_dy = [&](T* to) {
 #pragma unroll
@@ -112,18 +148,52 @@ __global__ void __launch_bounds__(kThreads, N * sizeof(T) >= 256 ? 1 : 2) delta_
         }
     };
     if (chunks > 0) {
-        const int64_t c = chunks - 1;
-        load_dy(c);
-        load_rows(c);
-        load_z(c);
-        load_values(c);
-        load_rest(c);
-        load_after(c);
-        share_dy(wl + (c & 1) * (TERMS * CA));
-        load_dy(c > 0 ? c - 1 : 0);
+        load_dy(0, true);
+        load_rows(0);
+        load_z(0);
+        load_values(0, true);
+        load_gates(0);
+        load_after(0);
+        share_dy(wl + (end & 1) * (TERMS * CA));
+        load_dy(chunks > 1, chunks == 1);
     }
     for (int64_t c = chunks - 1; c >= 0; --c) {
-        const int64_t next = c > 0 ? c - 1 : 0, at = (slot0 + c) * p.H + h;
+        const int64_t back = c > 0, at = (slot0 + c) * p.H + h;
+        const bool last = c == end && c == 0;  // of the chunk to load: the present one again, before the first
+        rows.store(st, dc, p.P);
+        dc -= p.H * NP;
+        lds_barrier();  // dS' and dY are there
+        f32x4 a[CT] = {}, d[CT] = {}, x[CT];
+        {
+            Operands<T, CT, 1> y[KC];
+            Operands<T, CT, TERMS> b[2];
+            b[0].read(at_s, 0, 16 * LS, SA);
+#pragma unroll
+            for (int t = 0; t < KC; ++t)
+                if (t >= ks0) y[t].read(at_y, t, 16 * LC, 0);
+#pragma unroll
+            for (int t = 0; t < KN; ++t) {
+                if (t + 1 < KN) b[(t + 1) % 2].read(at_s, t + 1, 16 * LS, SA);
+                __builtin_amdgcn_sched_barrier(0);
+                b[t % 2].template add<1>(a, &kf[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < KC; ++t)
+                if (t >= ks0) y[t].template add<TERMS>(d, pf[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+            x[i] = p.scale * d[i] + out * a[i];
+            put4<TERMS>(rl + (16 * i + m) * LC + M::place_of(w, g), CA, be * x[i]);
+        }
+        // (K's and Q's columns are the state's other operands: by way of LDS)
+#pragma unroll
+        for (int t = 0; t < KN; ++t) {
+            st16(kl + (16 * w + m) * LS + t * M::kK + g * M::kE, __builtin_bit_cast(uint4, kf[t]));
+            st16(ql + (16 * w + m) * LS + t * M::kK + g * M::kE, __builtin_bit_cast(uint4, qf[t]));
+        }
+        load_rows(back);
+        lds_barrier();  // B dU is there, dS' and dY are free
         float dot = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -131,38 +201,23 @@ __global__ void __launch_bounds__(kThreads, N * sizeof(T) >= 256 ? 1 : 2) delta_
             for (int i = 0; i < CT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dot += st[t][i][e] * after[t][i][e];
-        if (StateRows<N>::kAll || rows.own) {
-            const Rows<T> sr(static_cast<T*>(p.dstates) + at * NP + cb * kCols, N, p.P, kCols);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sr.store2(16 * (rows.tile0 + t) + 4 * g + e, 2 * m, st[t][0][e], st[t][1][e]);
-        } else {
-            dot = 0.f;
-        }
-        lds_barrier();  // dS' and dY are there
-        f32x4 x[CT];
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
-            f32x4 a{}, b{};
-#pragma unroll
-            for (int t = 0; t < KN; ++t) a = mma_terms<T, 1, TERMS>(&kf[t], sl + (16 * i + m) * LS + t * M::kK + g * M::kE, SA, a);
-#pragma unroll
-            for (int t = 0; t < KC; ++t)
-                if (t >= ks0) b = mma_terms<T, TERMS, 1>(pf[t], yl + (16 * i + m) * LC + t * M::kK + g * M::kE, 0, b);
-            x[i] = p.scale * b + out * a;
-            put4<TERMS>(rl + (16 * i + m) * LC + M::place_of(w, g), CA, be * x[i]);
-        }
-        load_rows(next);
-        lds_barrier();  // B dU is there, dS' and dY are free
+        if (!StateRows<N, CT>::kAll && !rows.own) dot = 0.f;
         f32x4 dv{}, db{};
-        const Rows<T> dr(static_cast<T*>(p.dv) + (span.lo + c * kC) * HP + vcol, have_of(c), HP, kCols);
+        const Block dr = oc.block(c == end);
+        oc.base -= oc.step;
         f32x4 de[CT];
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
+        {
+            Operands<T, CT, TERMS> b[KC];
 #pragma unroll
             for (int t = 0; t < KC; ++t)
-                if (t >= ks0) x[i] = mma_terms<T, TERMS, TERMS>(zf[t], rl + (16 * i + m) * LC + t * M::kK + g * M::kE, CA, x[i]);
+                if (t >= ks0) b[t].read(at_r, t, 16 * LC, CA);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < KC; ++t)
+                if (t >= ks0) b[t].template add<TERMS>(x, zf[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
             de[i] = be * x[i];
             put4<TERMS>(dl + (16 * i + m) * LC + M::place_of(w, g), CA, -in * de[i]);
 #pragma unroll
@@ -171,15 +226,19 @@ __global__ void __launch_bounds__(kThreads, N * sizeof(T) >= 256 ? 1 : 2) delta_
                 db[e] += x[i][e] * ee[e][i];
             }
         }
-        if (c > 0) share_dy(wl + (next & 1) * (TERMS * CA));
+        if (c > 0) share_dy(wl + ((c - 1) & 1) * (TERMS * CA));
         const float now = all;
-        load_z(next);
-        load_values(next);
-        load_after(next);
-        load_dy(next > 0 ? next - 1 : 0);
+        load_z(back);
+        load_values(back, last);
+        load_gates(back);
+        load_after(back);
+        load_dy(c > 1, end == 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            dr.store2(row0 + e, 2 * m, de[0][e], de[1][e]);
+            float x[CT];
+#pragma unroll
+            for (int i = 0; i < CT; ++i) x[i] = de[i][e];
+            dr.store<CT, T>(yat[e], x);
             dv[e] = sum16(dv[e]);
             db[e] = sum16(db[e]);
         }
@@ -195,72 +254,234 @@ __global__ void __launch_bounds__(kThreads, N * sizeof(T) >= 256 ? 1 : 2) delta_
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < CT; ++i) {
-                st[t][i] *= now;
+            for (int i = 0; i < CT; ++i) st[t][i] *= now;
 #pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    const int o = (16 * i + m) * LC + k * M::kK + g * M::kE;
-                    st[t][i] = mma_terms<T, 1, TERMS>(&tf[t][k], dl + o, CA, st[t][i]);
-                    st[t][i] = mma_terms<T, 1, TERMS>(&uf[t][k], wl + (c & 1) * (TERMS * CA) + o, CA, st[t][i]);
-                }
+        for (int k = 0; k < KC; ++k) {
+            Operands<T, CT, TERMS> b, y;
+            b.read(at_d, k, 16 * LC, CA);
+            y.read(at_w + (c & 1) * (TERMS * CA), k, 16 * LC, CA);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const Frag kt = columns_of(kl, LS, 16 * (rows.tile0 + t), k, m, g), qt = columns_of(ql, LS, 16 * (rows.tile0 + t), k, m, g);
+                b.template add<1>(st[t], &kt);
+                y.template add<1>(st[t], &qt);
             }
+        }
         rows.template share<TERMS>(st, sl, LS, SA);
-        load_rest(next);
     }
     if (p.dinit) rows.store(st, p.dinit + (s * p.H + h) * NP + cb * kCols, p.P);
 }
 
-template <typename T, int N>
+template <typename T, int N, int CT>
 int launch_back(const DeltaParams& p, hipStream_t stream) {
     using M = Mat<T>;
-    const int64_t units = p.nseq * p.H * (p.P / kCols), per = (units + 7) / 8;
-    constexpr int lds = 4 * M::kTerms * kCols * (kC + M::kPad) * (int)sizeof(T);
-    if (hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_back_kernel<T, N>), hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+    const int64_t units = p.nseq * p.H * (p.P / p.cols), per = (units + 7) / 8;
+    constexpr int lds = (4 * M::kTerms * 16 * CT * (kC + M::kPad) + 2 * kC * (N + M::kPad)) * (int)sizeof(T);
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_back_kernel<T, N, CT>), hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
         return -1;
-    hipLaunchKernelGGL((delta_back_kernel<T, N>), dim3((unsigned)(8 * per)), dim3(kThreads), lds, stream, p, units, per);
+    hipLaunchKernelGGL((delta_back_kernel<T, N, CT>), dim3((unsigned)(8 * per)), dim3(kThreads), lds, stream, p, units, per);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 // dq and dk of one chunk and key head, summed over its value heads in registers (no atomics), and their dlog a and dbeta.
-// A wave has a quarter of the rows n of dq^T and dk^T, for all 64 tokens as columns; the score tiles it computes
-// are those of its own 16 tokens.  One bf16 term each: the outputs are of the inputs' type.
+// Eight waves.  A wave has 16 rows n of dq^T and dk^T, of all 64 tokens as columns (of fewer where there are fewer
+// rows), and of the score tiles those of 16 tokens, either the ones with dY or the ones with dE.  dq and dk are of the inputs' type: in
+// bf16 their operands have one term, but U, which is in most of their products, has two (errors of 2.9e-3 with one and 2.4e-3 with
+// two, of which 1.7e-3 is the outputs' own rounding; a second term of the state leaves them there).
 template <typename T, int N, int PK>
-__global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_grad_kernel(DeltaParams p) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
-    constexpr int KC = kC / M::kK, KP = PK / M::kK, NT = (N / 16 + 3) / 4;
-    constexpr int LP = PK + M::kPad, LC = kC + M::kPad;
-    // dY, dE and U of a block of value dimensions [token][p]; then the three score matrices [token][contraction]
-    __shared__ __attribute__((aligned(16))) T mem[3 * kC * (LP > LC ? LP : LC)];
+    constexpr int KC = kC / M::kK, KP = PK / M::kK, NTILES = N / 16, CW = NTILES / 2;  // CW: column tiles of a wave (4, 2, 1)
+    constexpr int LP = PK + M::kPad, LC = kC + M::kPad, LS = N + M::kPad;
+    constexpr int PER = kC * (PK / 4) / (2 * kThreads), FRAGS = kC * N / M::kE / kWave, ROWS = (FRAGS + 7) / 8;
+    // dY, dE and U (TU terms) of a block of value dimensions [token][p], and in the same place the three score matrices
+    // [token][contraction]; K and Q [token][n]
+    constexpr int TU = sizeof(T) == 2 ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) T mem[(2 + TU) * kC * LP > 3 * kC * LC ? (2 + TU) * kC * LP : 3 * kC * LC];
+    extern __shared__ __attribute__((aligned(16))) char more[];
     __shared__ float ghi[kC], glo[kC];
     T *const yl = mem, *const el = mem + kC * LP, *const ul = mem + 2 * kC * LP;
     T *const bq = mem, *const bk = mem + kC * LC, *const bqk = mem + 2 * kC * LC;
+    T *const kl = reinterpret_cast<T*>(more), *const ql = kl + kC * LS;
 
     const int64_t slot = blockIdx.x / p.G;
     const int grp = blockIdx.x % p.G, group = p.H / p.G;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), m = lane % 16, g = lane / 16;
+    const int64_t rows_at = (slot * p.G + grp) * (int64_t)(N * kC);
     const int64_t s = seq_of_slot(p, slot);
     const Span span = span_of(p, s);
     const int64_t chunk = slot - (span.lo / kC + s);
     if (chunk < 0 || chunk * kC >= span.len) return;
-    const int64_t tok0 = span.lo + chunk * kC;
+    const int64_t tok0 = span.lo + chunk * kC, HP = (int64_t)p.H * p.P;
     const int have = (int)(span.len - chunk * kC < kC ? span.len - chunk * kC : kC);
-    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave, m = lane % 16, g = lane / 16;
-    const int tile0 = w * NT, blocks = p.P / kCols;
+    const int w = wave % 4, set = wave / 4;                        // scores: tokens 16 w .., of dY (0) or dE (1)
+    const int n0 = 16 * (wave % NTILES), c0 = wave / NTILES * CW;  // products: rows n0 .., column tiles c0 ..
+    const int blocks = p.P / p.cols;
+    {
+        const Block kb(static_cast<const T*>(p.kr) + rows_at, FRAGS * kWave * 16), qb(static_cast<const T*>(p.qr) + rows_at, FRAGS * kWave * 16);
+        uint4 x[2][ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            x[0][i] = kb.load16(threadIdx.x * 16, i * 2 * kThreads * 16);
+            x[1][i] = qb.load16(threadIdx.x * 16, i * 2 * kThreads * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int f = wave + i * 8;
+            if (FRAGS % 8 != 0 && f >= FRAGS) continue;
+            const int at = (16 * (f / (N / M::kK)) + m) * LS + f % (N / M::kK) * M::kK + g * M::kE;
+            st16(kl + at, x[0][i]);
+            st16(ql + at, x[1][i]);
+        }
+    }
+    uint32_t put[PER], token[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int x = threadIdx.x + i * 2 * kThreads, t = x / (PK / 4), c = 4 * (x % (PK / 4));
+        put[i] = t * LP + c;
+        token[i] = (uint32_t)(t * HP + c);
+    }
 
-    f32x4 dq[NT][4], dk[NT][4];
+    f32x4 dq[CW], dk[CW];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dq[t][i] = dk[t][i] = f32x4{};
+    for (int i = 0; i < CW; ++i) dq[i] = dk[i] = f32x4{};
 
     for (int r = 0; r < group; ++r) {
         const int h = grp * group + r;
         const int64_t at = slot * p.H + h;
-        const float* gates = p.gates + at * (kDeltaGates * kC);
+        const Block gates(p.gates + at * (kDeltaGates * kC));
+        if (threadIdx.x < kC) {
+            ghi[threadIdx.x] = gates.loadf(threadIdx.x * 4, kGateHigh * kC * 4);
+            glo[threadIdx.x] = gates.loadf(threadIdx.x * 4, kGateLow * kC * 4);
+        }
+        // scores, rows: contraction index j or l; columns: tokens i = 16 w ..  Tiles before w: x_i.u_j, after w: x_l.u_i,
+        // tile w: both, the latter in diag; x = dy or de
+        f32x4 near[4], diag{};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) near[i] = f32x4{};
+        for (int p0 = 0; p0 < p.P; p0 += PK) {
+            // everything that the block needs of memory, on its way at once
+            const uint32_t bytes = (uint32_t)((have - 1) * HP + PK);
+            const int64_t o = tok0 * HP + h * p.P + p0;
+            const Block yb(static_cast<const T*>(p.dy) + o, bytes * sizeof(T)), eb(static_cast<const T*>(p.dv) + o, bytes * sizeof(T)), ub(p.wrong + o, bytes * 4);
+            typedef typename std::conditional<sizeof(T) == 4, uint4, uint2>::type four;  // four elements
+            four x4[2][PER];
+            uint4 u4[PER];
+            float beta[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    x4[0][i] = yb.load16(token[i] * 4, 0);
+                    x4[1][i] = eb.load16(token[i] * 4, 0);
+                } else {
+                    x4[0][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(yb.r, (int)(token[i] * 2), 0, 0));
+                    x4[1][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(eb.r, (int)(token[i] * 2), 0, 0));
+                }
+                u4[i] = ub.load16(token[i] * 4, 0);
+                beta[i] = gates.loadf(threadIdx.x / (PK / 4) * 4, (kGateBeta * kC + i * 2 * kThreads / (PK / 4)) * 4);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                *reinterpret_cast<four*>(yl + put[i]) = x4[0][i];
+                *reinterpret_cast<four*>(el + put[i]) = x4[1][i];
+                put4<TU>(ul + put[i], kC * LP, beta[i] * as_f32x4(u4[i]));
+            }
+            // (the states' rows: on their way under the scores, in the registers of what has gone to LDS)
+            const Block sb(p.states + ((slot + s) * p.H + h) * (int64_t)N * p.P + p0), db(static_cast<const T*>(p.dstates) + at * (int64_t)N * p.P + p0);
+            const uint32_t sat = (uint32_t)((n0 + m) * p.P + g * M::kE);
+            f32x4 x0[KP][M::kE / 4];
+            Frag f1[KP];
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                f1[k] = db.frag<T>(sat * sizeof(T), k * M::kK * sizeof(T));
+#pragma unroll
+                for (int e = 0; e < M::kE / 4; ++e) x0[k][e] = as_f32x4(sb.load16(sat * 4, (k * M::kK + 4 * e) * 4));
+            }
+            __syncthreads();
+            const auto row = [&](const T* x, int tile, int k) { return frag(x + (16 * tile + m) * LP + k * M::kK + g * M::kE); };
+            const T* xl = set == 0 ? yl : el;
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const Frag xi = row(xl, w, k);
+                Frag ui[TU];
+#pragma unroll
+                for (int u = 0; u < TU; ++u) ui[u] = row(ul + u * kC * LP, w, k);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    // (the tile's own rows: U's where they come before, dY's or dE's where after)
+#pragma unroll
+                    for (int u = 0; u < TU; ++u)
+                        near[t] = M::mma(row(t <= w ? ul + u * kC * LP : xl, t, k), t <= w ? xi : ui[u], near[t]);
+                    if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int u = 0; u < TU; ++u) diag = M::mma(xi, ui[u], diag);
+                __builtin_amdgcn_sched_barrier(0);  // (here and below: the operands of one step at a time, in 128 registers)
+            }
+            // products with the states before and after the chunk
+            Frag f0[KP];
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
+                for (int e = 0; e < M::kE; ++e) f0[k][e] = (T)x0[k][e / 4][e % 4];
+#pragma unroll
+            for (int i = 0; i < CW; ++i) {
+                f32x4 a{}, b{}, c{};
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    a = M::mma(f0[k], row(yl, c0 + i, k), a);
+                    b = M::mma(f0[k], row(el, c0 + i, k), b);
+#pragma unroll
+                    for (int u = 0; u < TU; ++u) c = M::mma(f1[k], row(ul + u * kC * LP, c0 + i, k), c);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                const float in = gates.loadf((16 * c0 + m) * 4, (kGateIn * kC + 16 * i) * 4), out = gates.loadf((16 * c0 + m) * 4, (kGateOut * kC + 16 * i) * 4);
+                dq[i] += (p.scale * in) * a;
+                dk[i] += out * c - in * b;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
         __syncthreads();
-        if (w == 0) {
-            ghi[lane] = gates[kGateHigh * kC + lane];
-            glo[lane] = gates[kGateLow * kC + lane];
+        {
+            const int i = 16 * w + m;
+            const float hi = ghi[i], li = glo[i], by = set == 0 ? p.scale : -1.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f32x4 before{}, after{};  // of contraction indices up to i, and from i on
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * t + 4 * g + e;
+                    const float apart = (hi - ghi[j]) + (li - glo[j]);  // of i > j; for j > i the decay is of its opposite
+                    const float far = j <= i ? apart : -apart, d = by * (sizeof(T) == 4 ? expf(far) : __expf(far));
+                    if (j < i || (set == 0 && j == i)) before[e] = d * near[t][e];
+                    if (j > i || (set == 0 && j == i)) after[e] = d * (t == w ? diag[e] : near[t][e]);
+                }
+                const int o = i * LC + M::place_of(t, g);
+                if (set == 0) {
+                    put4<1>(bq + o, 0, before);
+                    put4<1>(bqk + o, 0, after);
+                } else {
+                    put4<1>(bk + o, 0, before + after);
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const Frag kf = columns_of(kl, LS, n0, k, m, g), qf = columns_of(ql, LS, n0, k, m, g);
+#pragma unroll
+            for (int i = 0; i < CW; ++i) {
+                const int o = (16 * (c0 + i) + m) * LC + k * M::kK + g * M::kE;
+                dq[i] = M::mma(kf, frag(bq + o), dq[i]);
+                dk[i] = M::mma(kf, frag(bk + o), dk[i]);
+                dk[i] = M::mma(qf, frag(bqk + o), dk[i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (wave == r % 8) {
             // the sums, token by token; of the decays from a token to the chunk's end
             double db = 0.0, dg = 0.0;
             for (int b = 0; b < blocks; ++b) {
@@ -268,169 +489,38 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(DeltaParams p) 
                 db += p.dot_b[o];
                 dg += (double)p.dot_y[o] - p.dot_v[o];
             }
+            double all = lane < blocks * kWaves ? p.dot_s[at * blocks * kWaves + lane] : 0.0;
 #pragma unroll
             for (int off = 1; off < kWave; off <<= 1) {
                 const double o = __shfl_down(dg, off, kWave);
                 if (lane + off < kWave) dg += o;
+                all += __shfl_xor(all, off, kWave);
             }
-            for (int b = 0; b < blocks * kWaves; ++b) dg += p.dot_s[at * blocks * kWaves + b];
             if (lane < have) {
                 const int64_t o = (tok0 + lane) * p.H + h;
                 p.dbeta[o] = (float)db;
                 // (a decay of zero passes nothing on; the sums would leave their rounding)
-                p.dlog_a[o] = expf(p.log_a[o]) == 0.f ? 0.f : (float)dg;
-            }
-        }
-        float in[4], out[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            in[i] = gates[kGateIn * kC + 16 * i + m];
-            out[i] = gates[kGateOut * kC + 16 * i + m];
-        }
-        // rows: contraction index j or l; columns: the wave's own tokens i
-        f32x4 near1[4], near2[4], own1{}, own2{};  // tiles before w: dy_i.u_j, de_i.u_j; after w: dy_l.u_i, de_l.u_i
-        f32x4 diag1{}, diag2{};                    // tile w: own for j, diag for l
-#pragma unroll
-        for (int i = 0; i < 4; ++i) near1[i] = near2[i] = f32x4{};
-        for (int p0 = 0; p0 < p.P; p0 += PK) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kC * (PK / 4); i += kThreads) {
-                const int t = i / (PK / 4), c = 4 * (i % (PK / 4));
-                f32x4 y{}, e{}, u{};
-                if (t < have) {
-                    const int64_t o = ((tok0 + t) * p.H + h) * p.P + p0 + c;
-                    u = gates[kGateBeta * kC + t] * as_f32x4(ld16(p.wrong + o));
-                    if constexpr (sizeof(T) == 4) {
-                        y = as_f32x4(ld16(static_cast<const float*>(p.dy) + o));
-                        e = as_f32x4(ld16(static_cast<const float*>(p.dv) + o));
-                    } else {
-                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                        const bf16x4 a = *reinterpret_cast<const bf16x4*>(static_cast<const T*>(p.dy) + o);
-                        const bf16x4 b = *reinterpret_cast<const bf16x4*>(static_cast<const T*>(p.dv) + o);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            y[k] = (float)a[k];
-                            e[k] = (float)b[k];
-                        }
-                    }
-                }
-                put4<1>(yl + t * LP + c, 0, y);
-                put4<1>(el + t * LP + c, 0, e);
-                put4<1>(ul + t * LP + c, 0, u);
-            }
-            __syncthreads();
-            const auto row = [&](const T* x, int tile, int k) { return frag(x + (16 * tile + m) * LP + k * M::kK + g * M::kE); };
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const Frag yi = row(yl, w, k), ei = row(el, w, k), ui = row(ul, w, k);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (t < w) {
-                        const Frag uj = row(ul, t, k);
-                        near1[t] = M::mma(uj, yi, near1[t]);
-                        near2[t] = M::mma(uj, ei, near2[t]);
-                    } else if (t > w) {
-                        near1[t] = M::mma(row(yl, t, k), ui, near1[t]);
-                        near2[t] = M::mma(row(el, t, k), ui, near2[t]);
-                    }
-                }
-                own1 = M::mma(ui, yi, own1);
-                own2 = M::mma(ui, ei, own2);
-                diag1 = M::mma(yi, ui, diag1);
-                diag2 = M::mma(ei, ui, diag2);
-            }
-            // products with the states before and after the chunk
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (tile0 + t >= N / 16) continue;
-                const int64_t n = 16 * (tile0 + t) + m;
-                const float* s0 = p.states + (((slot + s) * p.H + h) * N + n) * p.P + p0 + g * M::kE;
-                const T* s1 = static_cast<const T*>(p.dstates) + (at * N + n) * p.P + p0 + g * M::kE;
-                Frag f0[KP], f1[KP];
-#pragma unroll
-                for (int k = 0; k < KP; ++k) {
-                    f1[k] = frag(s1 + k * M::kK);
-#pragma unroll
-                    for (int e = 0; e < M::kE; e += 4) {
-                        const f32x4 x = as_f32x4(ld16(s0 + k * M::kK + e));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) f0[k][e + j] = (T)x[j];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f32x4 a{}, b{}, c{};
-#pragma unroll
-                    for (int k = 0; k < KP; ++k) {
-                        a = M::mma(f0[k], row(yl, i, k), a);
-                        b = M::mma(f0[k], row(el, i, k), b);
-                        c = M::mma(f1[k], row(ul, i, k), c);
-                    }
-                    dq[t][i] += (p.scale * in[i]) * a;
-                    dk[t][i] += out[i] * c - in[i] * b;
-                }
-            }
-        }
-        __syncthreads();
-        {
-            const int i = 16 * w + m;
-            const float hi = ghi[i], li = glo[i];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f32x4 a{}, b{}, c{};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * t + 4 * g + e;
-                    const float apart = (hi - ghi[j]) + (li - glo[j]);  // of i > j; for j > i the decay is of its opposite
-                    const float d = expf(j <= i ? apart : -apart);
-                    if (t < w) {
-                        a[e] = p.scale * d * near1[t][e];
-                        b[e] = -d * near2[t][e];
-                    } else if (t > w) {
-                        c[e] = p.scale * d * near1[t][e];
-                        b[e] = -d * near2[t][e];
-                    } else {
-                        a[e] = j <= i ? p.scale * d * own1[e] : 0.f;
-                        c[e] = j >= i ? p.scale * d * diag1[e] : 0.f;
-                        b[e] = j < i ? -d * own2[e] : j > i ? -d * diag2[e] : 0.f;
-                    }
-                }
-                const int o = i * LC + M::place_of(t, g);
-                put4<1>(bq + o, 0, a);
-                put4<1>(bk + o, 0, b);
-                put4<1>(bqk + o, 0, c);
-            }
-        }
-        __syncthreads();
-        const T* kt = static_cast<const T*>(p.kt) + (slot * p.G + grp) * (int64_t)(N * kC) + lane * M::kE;
-        const T* qt = static_cast<const T*>(p.qt) + (slot * p.G + grp) * (int64_t)(N * kC) + lane * M::kE;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (tile0 + t >= N / 16) continue;
-#pragma unroll
-            for (int k = 0; k < KC; ++k) {
-                const Frag kf = frag(kt + ((tile0 + t) * KC + k) * (kWave * M::kE)), qf = frag(qt + ((tile0 + t) * KC + k) * (kWave * M::kE));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int o = (16 * i + m) * LC + k * M::kK + g * M::kE;
-                    dq[t][i] = M::mma(kf, frag(bq + o), dq[t][i]);
-                    dk[t][i] = M::mma(kf, frag(bk + o), dk[t][i]);
-                    dk[t][i] = M::mma(qf, frag(bqk + o), dk[t][i]);
-                }
+                p.dlog_a[o] = expf(p.log_a[o]) == 0.f ? 0.f : (float)(dg + all);
             }
         }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        if (tile0 + t >= N / 16) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (16 * i + m >= have) continue;
-            const int64_t o = ((tok0 + 16 * i + m) * p.G + grp) * N + 16 * (tile0 + t) + 4 * g;
-            store4(static_cast<T*>(p.dq) + o, dq[t][i][0], dq[t][i][1], dq[t][i][2], dq[t][i][3]);
-            store4(static_cast<T*>(p.dk) + o, dk[t][i][0], dk[t][i][1], dk[t][i][2], dk[t][i][3]);
-        }
+    for (int i = 0; i < CW; ++i) {
+        const int t = 16 * (c0 + i) + m;
+        if (t >= have) continue;
+        const int64_t o = ((tok0 + t) * p.G + grp) * N + n0 + 4 * g;
+        store4(static_cast<T*>(p.dq) + o, dq[i][0], dq[i][1], dq[i][2], dq[i][3]);
+        store4(static_cast<T*>(p.dk) + o, dk[i][0], dk[i][1], dk[i][2], dk[i][3]);
     }
+}
+
+template <typename T, int N, int PK>
+int launch_grad(const DeltaParams& p, hipStream_t stream) {
+    constexpr int lds = 2 * kC * (N + Mat<T>::kPad) * (int)sizeof(T);
+    const auto kernel = &delta_grad_kernel<T, N, PK>;
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess) return -1;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.slots * p.G)), dim3(2 * kThreads), lds, stream, p);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 template <typename T, int N>
@@ -440,11 +530,9 @@ int launch_backward(const DeltaParams& p, hipStream_t stream) {
         rc = launch_prep<T, N, true>(p, stream);
         if (rc == 0) rc = launch_walk<T, N, true>(p, stream);
     }
-    if (rc == 0) rc = launch_back<T, N>(p, stream);
+    if (rc == 0) rc = p.cols == 16 ? launch_back<T, N, 1>(p, stream) : launch_back<T, N, 2>(p, stream);
     if (rc != 0 || p.total == 0) return rc;
-    if (p.P % 64 == 0) hipLaunchKernelGGL((delta_grad_kernel<T, N, 64>), dim3((unsigned)(p.slots * p.G)), dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((delta_grad_kernel<T, N, 32>), dim3((unsigned)(p.slots * p.G)), dim3(kThreads), 0, stream, p);
-    return hipGetLastError() == hipSuccess ? 0 : -1;
+    return p.P % 64 == 0 ? launch_grad<T, N, 64>(p, stream) : launch_grad<T, N, 32>(p, stream);
 }
 
 }  // namespace

@@ -9,7 +9,7 @@
 namespace ssd {
 
 constexpr int kDeltaChunk = 64;  // tokens of a chunk
-constexpr int kDeltaCols = 32;   // columns of the state (value dimensions) of a walk's workgroup
+constexpr int kDeltaCols = 32;   // value dimensions come in multiples of these (a walk's workgroup takes 16 or 32 columns)
 
 // Chunk c of the sequence that begins at token `lo` of the packed axis has slot lo / 64 + s + c: sequences of any
 // lengths then have slots of their own, total / 64 + nseq of them at most.
@@ -39,19 +39,20 @@ struct DeltaParams {
     void* scores;           // [slots, H][terms][64 x 64]: decayed q . k
     void* zt;               // their transposes (backward)
     void* scores_t;
-    void* kt;               // [slots, G][N x 64]
-    void* qt;
+    void* kr;               // [slots, G][64 x N]: rows of K and Q by tile, zeros behind a sequence's end
+    void* qr;
     float* gates;           // [slots, H][kDeltaGates][64]
     float* states;          // [slots + nseq, H, N, P]: the state before each chunk, and after the last
     float* wrong;           // [total, H, P]: e
     void* dstates;          // [slots, H, N, P]: gradient of the state after each chunk
-    float* dot_y;           // [slots, H, P / 32][64]: dy . y of a workgroup's columns
+    float* dot_y;           // [slots, H, P / cols][64]: dy . y of a workgroup's columns
     float* dot_v;           // dv . v
     float* dot_b;           // x . e
-    float* dot_s;           // [slots, H, P / 32]: <dstate, state> after each chunk
+    float* dot_s;           // [slots, H, P / cols][4]: <dstate, state> after each chunk
     int64_t nseq, total, each, slots;
     int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
     int H, G, N, P;
+    int cols;               // columns of the state of a walk's workgroup: 16 or 32
     float scale;
 };
 

@@ -16,18 +16,23 @@ namespace delta {
 
 constexpr int kLdz = kC + 4;  // LDS row stride of a 64 x 64 fp32 matrix
 
-// Operand fragments of a [64][64] matrix of LDS, or of its transpose, to memory: rows by tile, then steps, then lanes.
-template <typename T, bool TRANSPOSED, int TERMS, typename F>
-__device__ __forceinline__ void emit(T* out, const F& at) {
+// Operand fragments of a lower triangular [64][64] matrix of LDS, or of its transpose, to memory: rows by tile, then steps,
+// then lanes.  Steps that are zero throughout have their places and are not written (nor read).
+template <typename T, bool TRANSPOSED, int TERMS>
+__device__ __forceinline__ void emit(T* out, const float* at) {
     using M = Mat<T>;
-    constexpr int KC = kC / M::kK;
+    constexpr int KC = kC / M::kK, TILES = M::kK / 16;
     for (int f = threadIdx.x; f < 4 * KC * kWave; f += kThreads) {
-        const int lane = f % kWave, ks = f / kWave % KC, rt = f / (kWave * KC), row = 16 * rt + lane % 16;
+        const int lane = f % kWave, ks = f / kWave % KC, rt = f / (kWave * KC), m = lane % 16, g = lane / 16;
         float x[M::kE];
+        if (TRANSPOSED ? TILES * ks + TILES - 1 < rt : TILES * ks > rt) continue;
 #pragma unroll
-        for (int e = 0; e < M::kE; ++e) {
-            const int t = M::token_of(ks, lane / 16, e);
-            x[e] = TRANSPOSED ? at(t, row) : at(row, t);
+        for (int i = 0; i < TILES; ++i) {  // a step is of one or two tiles, four tokens of each in a lane
+            const int ct = TILES * ks + i;
+            const bool left = TRANSPOSED ? ct >= rt : ct <= rt;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[4 * i + e] = !left ? 0.f : TRANSPOSED ? at[(16 * ct + 4 * g + e) * kLdz + 16 * rt + m] : at[(16 * rt + m) * kLdz + 16 * ct + 4 * g + e];
         }
         put_frag<TERMS>(out + (int64_t)f * M::kE, kC * kC, x);
     }
@@ -37,28 +42,15 @@ __device__ __forceinline__ void emit(T* out, const F& at) {
 template <typename T, int N>
 __device__ __forceinline__ void stage_rows(T* to, const T* from, int64_t stride, int have) {
     using M = Mat<T>;
-    const Rows<T> rows(from, have, stride, N);
+    const Block rows = Chunks(from, have, stride, N).block(true);
     constexpr int CH = N / M::kE, PER = kC * CH / kThreads;
     typename M::Frag x[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) x[i] = rows.frag((threadIdx.x + i * kThreads) / CH, (threadIdx.x + i * kThreads) % CH * M::kE);
+    for (int i = 0; i < PER; ++i)
+        x[i] = rows.template frag<T>((uint32_t)(((threadIdx.x + i * kThreads) / CH * stride + (threadIdx.x + i * kThreads) % CH * M::kE) * sizeof(T)), 0);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         st16(to + (threadIdx.x + i * kThreads) / CH * (N + M::kPad) + (threadIdx.x + i * kThreads) % CH * M::kE, __builtin_bit_cast(uint4, x[i]));
-}
-
-// The columns of staged rows as operand fragments: index n, contracting over the chunk's tokens.
-template <typename T, int N>
-__device__ __forceinline__ void emit_columns(T* out, const T* rows) {
-    using M = Mat<T>;
-    constexpr int KC = kC / M::kK;
-    for (int f = threadIdx.x; f < (N / 16) * KC * kWave; f += kThreads) {
-        const int lane = f % kWave, ks = f / kWave % KC, n = 16 * (f / (kWave * KC)) + lane % 16;
-        typename M::Frag x;
-#pragma unroll
-        for (int e = 0; e < M::kE; ++e) x[e] = rows[M::token_of(ks, lane / 16, e) * (N + M::kPad) + n];
-        st16(out + (int64_t)f * M::kE, __builtin_bit_cast(uint4, x));
-    }
 }
 
 template <typename T, int N> constexpr int prep_lds_bytes() {
@@ -67,12 +59,12 @@ template <typename T, int N> constexpr int prep_lds_bytes() {
 }
 
 template <typename T, int N, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(DeltaParams p) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
     constexpr int KN = N / M::kK, TERMS = M::kTerms;
     __shared__ __attribute__((aligned(16))) char mem[prep_lds_bytes<T, N>()];
-    __shared__ float ghi[kC], glo[kC], beta[kC];
+    __shared__ float ghi[kWaves][kC], glo[kWaves][kC], betas[kWaves][kC];  // of four heads at a time
 
     const int64_t slot = blockIdx.x / p.G;
     const int grp = blockIdx.x % p.G, group = p.H / p.G;
@@ -82,7 +74,37 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaParams p) {
     if (chunk < 0 || chunk * kC >= span.len) return;
     const int64_t tok0 = span.lo + chunk * kC;
     const int have = (int)(span.len - chunk * kC < kC ? span.len - chunk * kC : kC);
-    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave, m = lane % 16, g = lane / 16;
+    const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), m = lane % 16, g = lane / 16;
+
+    // wave w's head of the next four: its gates, summed along the chunk
+    float la = 0.f, be = 0.f;
+    const auto load_gates = [&](int r) {
+        const bool ok = r + w < group && lane < have;
+        const int64_t tok = (tok0 + (ok ? lane : 0)) * p.H + grp * group + (ok ? r + w : 0);
+        la = ok ? p.log_a[tok] : 0.f;
+        be = ok ? p.beta[tok] : 0.f;
+    };
+    const auto put_gates = [&](int r) {
+        if (r + w >= group) return;
+        la = la < -160.f ? -160.f : la;
+        double sum = la;
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+            const double o = __shfl_up(sum, off, kWave);
+            if (lane >= off) sum += o;
+        }
+        const float hi = (float)sum, lo = (float)(sum - (double)hi);
+        ghi[w][lane] = hi;
+        glo[w][lane] = lo;
+        betas[w][lane] = be;
+        float* gates = p.gates + (slot * p.H + grp * group + r + w) * (kDeltaGates * kC) + lane;
+        gates[kGateIn * kC] = expf(hi);
+        gates[kGateOut * kC] = expf((float)(__shfl(sum, kWave - 1, kWave) - sum));
+        gates[kGateBeta * kC] = be;
+        gates[kGateHigh * kC] = hi;
+        gates[kGateLow * kC] = lo;
+    };
+    load_gates(0);
 
     // k_i.k_j and q_i.k_j: wave w has rows 16 w .. of the lower tiles
     f32x4 kk[4], qk[4];
@@ -91,11 +113,23 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaParams p) {
         const T* kp = static_cast<const T*>(p.k) + tok0 * p.k_stride + grp * N;
         const T* qp = static_cast<const T*>(p.q) + tok0 * p.q_stride + grp * N;
         Frag qf[KN];
-        const Rows<T> qrows(qp, have, p.q_stride, N);
+        const Block qrows = Chunks(qp, have, p.q_stride, N).block(true);
+        const uint32_t qat = (uint32_t)(((16 * w + m) * p.q_stride + g * M::kE) * sizeof(T));
 #pragma unroll
-        for (int t = 0; t < KN; ++t) qf[t] = qrows.frag(16 * w + m, t * M::kK + g * M::kE);
+        for (int t = 0; t < KN; ++t) qf[t] = qrows.frag<T>(qat, t * M::kK * sizeof(T));
         stage_rows<T, N>(rows, kp, p.k_stride, have);
+        put_gates(0);
         __syncthreads();
+        // the rows themselves, in the order of the walks' loads (as they lie in their tensors, a head's rows are often
+        // some multiple of 4 KB apart, which are all of one channel of the L2)
+        Frag kf[KN];
+        const int64_t own = (slot * p.G + grp) * (int64_t)(N * kC) + (w * KN * kWave + lane) * M::kE;
+#pragma unroll
+        for (int t = 0; t < KN; ++t) {
+            kf[t] = frag(rows + (16 * w + m) * (N + M::kPad) + t * M::kK + g * M::kE);
+            st16(static_cast<T*>(p.kr) + own + t * (kWave * M::kE), __builtin_bit_cast(uint4, kf[t]));
+            st16(static_cast<T*>(p.qr) + own + t * (kWave * M::kE), __builtin_bit_cast(uint4, qf[t]));
+        }
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct) {
             kk[ct] = qk[ct] = f32x4{};
@@ -103,68 +137,40 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaParams p) {
 #pragma unroll
             for (int t = 0; t < KN; ++t) {
                 const Frag kb = frag(rows + (16 * ct + m) * (N + M::kPad) + t * M::kK + g * M::kE);
-                kk[ct] = M::mma(frag(rows + (16 * w + m) * (N + M::kPad) + t * M::kK + g * M::kE), kb, kk[ct]);
+                kk[ct] = M::mma(kf[t], kb, kk[ct]);
                 qk[ct] = M::mma(qf[t], kb, qk[ct]);
             }
         }
-        emit_columns<T, N>(static_cast<T*>(p.kt) + (slot * p.G + grp) * (int64_t)(N * kC), rows);
         __syncthreads();
-        if constexpr (BACKWARD) {
-            stage_rows<T, N>(rows, qp, p.q_stride, have);
-            __syncthreads();
-            emit_columns<T, N>(static_cast<T*>(p.qt) + (slot * p.G + grp) * (int64_t)(N * kC), rows);
-            __syncthreads();
-        }
     }
 
     float* lm = reinterpret_cast<float*>(mem);  // L
     float* zm = lm + kC * kLdz;                 // the scores, then Z; tiles above the diagonal are not written
     for (int r = 0; r < group; ++r) {
-        const int h = grp * group + r;
-        const int64_t at = slot * p.H + h;
-        if (w == 0) {
-            const int64_t tok = (tok0 + lane) * p.H + h;
-            float la = lane < have ? p.log_a[tok] : 0.f;
-            la = la < -160.f ? -160.f : la;
-            const float b = lane < have ? p.beta[tok] : 0.f;
-            double sum = la;
-#pragma unroll
-            for (int off = 1; off < kWave; off <<= 1) {
-                const double o = __shfl_up(sum, off, kWave);
-                if (lane >= off) sum += o;
-            }
-            const float hi = (float)sum, lo = (float)(sum - (double)hi);
-            ghi[lane] = hi;
-            glo[lane] = lo;
-            beta[lane] = b;
-            float* gates = p.gates + at * (kDeltaGates * kC) + lane;
-            gates[kGateIn * kC] = expf(hi);
-            gates[kGateOut * kC] = expf((float)(__shfl(sum, kWave - 1, kWave) - sum));
-            gates[kGateBeta * kC] = b;
-            gates[kGateHigh * kC] = hi;
-            gates[kGateLow * kC] = lo;
+        const int64_t at = slot * p.H + grp * group + r;
+        if (r > 0 && r % kWaves == 0) {
+            put_gates(r);
+            __syncthreads();
         }
-        __syncthreads();
+        if (r % kWaves == kWaves - 1) load_gates(r + 1);
+        const float *const gh = ghi[r % kWaves], *const gl = glo[r % kWaves], *const beta = betas[r % kWaves];
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct) {
             if (ct > w) continue;
             const int j = 16 * ct + m;
-            const float hj = ghi[j], lj = glo[j];
+            const float hj = gh[j], lj = gl[j];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * w + 4 * g + e;
-                const float d = j <= i ? expf((ghi[i] - hj) + (glo[i] - lj)) : 0.f;
+                const float d = j <= i ? expf((gh[i] - hj) + (gl[i] - lj)) : 0.f;
                 lm[i * kLdz + j] = j < i ? d * kk[ct][e] : 0.f;
                 zm[i * kLdz + j] = j <= i ? d * qk[ct][e] : 0.f;
             }
         }
         __syncthreads();
-        const auto below = [&](int i, int j) { return j / 16 <= i / 16 ? zm[i * kLdz + j] : 0.f; };
-        // (the forward pass makes nothing but y of the scores: one term)
-        constexpr int ST = BACKWARD ? TERMS : 1;
-        emit<T, false, ST>(static_cast<T*>(p.scores) + at * (ST * kC * kC), below);
-        if constexpr (BACKWARD) emit<T, true, TERMS>(static_cast<T*>(p.scores_t) + at * (TERMS * kC * kC), below);
-        __syncthreads();
+        constexpr int ST = terms_of_y<T>(BACKWARD);
+        emit<T, false, ST>(static_cast<T*>(p.scores) + at * (ST * kC * kC), zm);
+        if constexpr (BACKWARD) emit<T, true, TERMS>(static_cast<T*>(p.scores_t) + at * (TERMS * kC * kC), zm);
 
         // Z of the diagonal tile w, row by row: z_i = -L_i - sum_{j<i} L_ij beta_j z_j
         f32x4 z, inv;  // inv: row m, columns 4 g .. of (I + L B)^-1's diagonal tile, an operand
@@ -178,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[e] -= lw[(4 * g + e) * kLdz + i] * zi;
             }
+            __syncthreads();  // (the scores are written)
 #pragma unroll
             for (int e = 0; e < 4; ++e) zm[(16 * w + 4 * g + e) * kLdz + 16 * w + m] = z[e];
         }
@@ -209,8 +216,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(DeltaParams p) {
             }
             __syncthreads();
         }
-        emit<T, false, TERMS>(static_cast<T*>(p.z) + at * (TERMS * kC * kC), below);
-        if constexpr (BACKWARD) emit<T, true, TERMS>(static_cast<T*>(p.zt) + at * (TERMS * kC * kC), below);
+        emit<T, false, TERMS>(static_cast<T*>(p.z) + at * (TERMS * kC * kC), zm);
+        if constexpr (BACKWARD) emit<T, true, TERMS>(static_cast<T*>(p.zt) + at * (TERMS * kC * kC), zm);
         __syncthreads();
     }
 }

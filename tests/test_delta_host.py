@@ -124,14 +124,15 @@ def test_step_refusals(lib):
 
 
 def test_workspace_bytes():
-    """bf16 operands of computed values are three terms: Z, and the scores that only y takes in one."""
+    """bf16 operands of computed values are three terms: Z, and the scores in two where only y takes them; rows of K and Q."""
     slots = 100 // 64 + 2
     chunk = 64 * 64 * 2
-    forward = slots * 4 * (3 + 1) * chunk + slots * 2 * 64 * 64 * 2 + slots * 4 * 5 * 64 * 4
+    rows = 2 * slots * 2 * 64 * 64 * 2
+    forward = slots * 4 * (3 + 2) * chunk + rows + slots * 4 * 5 * 64 * 4
     assert ssd.ssd_delta_forward_workspace_bytes(_dims()) == forward
-    state = 64 * 96
-    backward = (slots * 4 * 12 * chunk + 2 * slots * 2 * 64 * 64 * 2 + slots * 4 * 5 * 64 * 4 + (slots + 2) * 4 * state * 4
-                + 100 * 4 * 96 * 4 + slots * 4 * state * 2 + 3 * slots * 4 * 3 * 64 * 4 + slots * 4 * 3 * 16)
+    state, blocks = 64 * 96, 96 // 16
+    backward = (slots * 4 * 12 * chunk + rows + slots * 4 * 5 * 64 * 4 + (slots + 2) * 4 * state * 4
+                + 100 * 4 * 96 * 4 + slots * 4 * state * 2 + 3 * slots * 4 * blocks * 64 * 4 + slots * 4 * blocks * 16)
     assert ssd.ssd_delta_backward_workspace_bytes(_dims()) == backward
     for bad in (dict(keydim=48), dict(nseq=0), dict(total=0), dict(dtype=7)):
         assert ssd.ssd_delta_forward_workspace_bytes(_dims(**bad)) == 0
