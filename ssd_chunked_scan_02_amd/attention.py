@@ -115,6 +115,13 @@ def _token_stride(t, name, dim, dtype, device):
     return step
 
 
+def _stride(t, name, dim, dtype, device):
+    """As _token_stride; a dense tensor, a step's above all, is seen to be one without asking for its strides."""
+    if t.dim() == dim and t.dtype is dtype and t.device == device and device.type == "cuda" and t.is_contiguous():
+        return t.shape[-2] * t.shape[-1]
+    return _token_stride(t, name, dim, dtype, device)
+
+
 def _offsets(t, name, device, n=None):
     if t is None or (n is not None and t.dtype is torch.int64 and t.shape == (n,) and t.device == device and t.is_contiguous()):
         return

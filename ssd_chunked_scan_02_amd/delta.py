@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _DTYPE_CODE, _in_stream, _on_stream, load_library
-from .attention import _addr, _call, _dense, _offsets, _token_stride, _workspace
+from .attention import _addr, _call, _dense, _offsets, _stride, _workspace
 
 
 class DeltaDims(ctypes.Structure):
@@ -42,7 +42,7 @@ def _dims(q, k, v, log_a, beta, cu_seqlens, scale, dim):
     dev = q.device
     if q.dtype not in _DTYPE_CODE:
         raise TypeError("q must be float32 or bfloat16, got %s" % q.dtype)
-    strides = [_token_stride(t, n, dim, q.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
+    strides = _stride(q, "q", dim, q.dtype, dev), _stride(k, "k", dim, q.dtype, dev), _stride(v, "v", dim, q.dtype, dev)
     if k.shape != q.shape or v.shape[:-2] != q.shape[:-2]:
         raise ValueError("q, k and v must have the same tokens, and q and k be alike: q %s, k %s, v %s"
                          % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _DTYPE_CODE, _in_stream, _on_stream, load_library
-from .attention import AttnCache, _addr, _bias_args, _call, _dense, _offsets, _token_stride, _workspace
+from .attention import AttnCache, _addr, _bias_args, _call, _dense, _offsets, _stride, _workspace
 
 SSD_KV8_INT8, SSD_KV8_E4M3 = 0, 1
 _FORMAT = {torch.int8: SSD_KV8_INT8, torch.float8_e4m3fn: SSD_KV8_E4M3}
@@ -70,7 +70,7 @@ def ssd_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
     ``cu_seqlens``: int64 offsets of each sequence's new tokens (None: one token per sequence); ``seq_lens`` counts the
     sequences with them.  Returns the rotated q, or None without q."""
     dev = k.device
-    strides = [0 if t is None else _token_stride(t, n, 3, k.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
+    strides = [0 if t is None else _stride(t, n, 3, k.dtype, dev) for n, t in (("q", q), ("k", k), ("v", v))]
     tokens, Hk, D = k.shape
     H = Hk if q is None else q.shape[1]
     dims, pages = _pages(k.dtype, dev, H, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, strides)
@@ -110,7 +110,7 @@ def ssd_kv8_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
 
     Bias and cap as in ssd_attn_forward.  Returns y [nseq,H,D]."""
     dev = q.device
-    stride = _token_stride(q, "q", 3, q.dtype, dev)
+    stride = _stride(q, "q", 3, q.dtype, dev)
     nseq, H, D = q.shape
     dims, pages = _pages(q.dtype, dev, H, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, (stride, 0, 0), scale, softcap,
                          _bias_args(slopes, table, H, dev), max_distance, bidirectional)

@@ -11,7 +11,7 @@ import math
 import torch
 
 from . import _DTYPE_CODE, _in_stream, _on_stream
-from .attention import _addr, _call, _dense, _offsets, _token_stride
+from .attention import _addr, _call, _dense, _offsets, _stride
 
 
 class RotaryDims(ctypes.Structure):
@@ -39,7 +39,7 @@ def ssd_rotate(q, inv_freq, cu_seqlens=None, start=None, k=None, interleaved: bo
     dev, dim = q.device, 4 if cu_seqlens is None else 3
     if q.dtype not in _DTYPE_CODE:
         raise TypeError("q must be float32 or bfloat16, got %s" % q.dtype)
-    strides = [0 if t is None else _token_stride(t, n, dim, q.dtype, dev) for n, t in (("q", q), ("k", k))]
+    strides = [0 if t is None else _stride(t, n, dim, q.dtype, dev) for n, t in (("q", q), ("k", k))]
     if k is not None and (k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
         raise ValueError("q %s and k %s must have the same tokens and head dim" % (tuple(q.shape), tuple(k.shape)))
     if k is None and k_out is not None:
