@@ -308,8 +308,18 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
 
     const int64_t slot = blockIdx.x / p.G;
     const int grp = blockIdx.x % p.G, group = p.H / p.G;
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), m = lane % 16, g = lane / 16;
+    int tid = threadIdx.x, lane = tid % kWave, m = lane % 16, g = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int64_t rows_at = (slot * p.G + grp) * (int64_t)(N * kC);
+    uint4 rows[2][ROWS];  // (on their way while the slot's sequence is looked for)
+    {
+        const Block kb(static_cast<const T*>(p.kr) + rows_at, FRAGS * kWave * 16), qb(static_cast<const T*>(p.qr) + rows_at, FRAGS * kWave * 16);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            rows[0][i] = kb.load16(threadIdx.x * 16, i * 2 * kThreads * 16);
+            rows[1][i] = qb.load16(threadIdx.x * 16, i * 2 * kThreads * 16);
+        }
+    }
     const int64_t s = seq_of_slot(p, slot);
     const Span span = span_of(p, s);
     const int64_t chunk = slot - (span.lo / kC + s);
@@ -319,42 +329,34 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
     const int w = wave % 4, set = wave / 4;                        // scores: tokens 16 w .., of dY (0) or dE (1)
     const int n0 = 16 * (wave % NTILES), c0 = wave / NTILES * CW;  // products: rows n0 .., column tiles c0 ..
     const int blocks = p.P / p.cols;
-    {
-        const Block kb(static_cast<const T*>(p.kr) + rows_at, FRAGS * kWave * 16), qb(static_cast<const T*>(p.qr) + rows_at, FRAGS * kWave * 16);
-        uint4 x[2][ROWS];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            x[0][i] = kb.load16(threadIdx.x * 16, i * 2 * kThreads * 16);
-            x[1][i] = qb.load16(threadIdx.x * 16, i * 2 * kThreads * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int f = wave + i * 8;
-            if (FRAGS % 8 != 0 && f >= FRAGS) continue;
-            const int at = (16 * (f / (N / M::kK)) + m) * LS + f % (N / M::kK) * M::kK + g * M::kE;
-            st16(kl + at, x[0][i]);
-            st16(ql + at, x[1][i]);
-        }
+    for (int i = 0; i < ROWS; ++i) {
+        const int f = wave + i * 8;
+        if (FRAGS % 8 != 0 && f >= FRAGS) continue;
+        const int at = (16 * (f / (N / M::kK)) + m) * LS + f % (N / M::kK) * M::kK + g * M::kE;
+        st16(kl + at, rows[0][i]);
+        st16(ql + at, rows[1][i]);
     }
-    uint32_t put[PER], token[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int x = threadIdx.x + i * 2 * kThreads, t = x / (PK / 4), c = 4 * (x % (PK / 4));
-        put[i] = t * LP + c;
-        token[i] = (uint32_t)(t * HP + c);
-    }
-
     f32x4 dq[CW], dk[CW];
 #pragma unroll
     for (int i = 0; i < CW; ++i) dq[i] = dk[i] = f32x4{};
 
+    // (what follows computes its lane's addresses anew from here: kept through the loops, they would take registers that
+    // are not there)
+    const auto fresh = [&] {
+        asm volatile("" : "+v"(tid));
+        lane = tid % kWave;
+        m = lane % 16;
+        g = lane / 16;
+    };
     for (int r = 0; r < group; ++r) {
         const int h = grp * group + r;
         const int64_t at = slot * p.H + h;
+        fresh();
         const Block gates(p.gates + at * (kDeltaGates * kC));
-        if (threadIdx.x < kC) {
-            ghi[threadIdx.x] = gates.loadf(threadIdx.x * 4, kGateHigh * kC * 4);
-            glo[threadIdx.x] = gates.loadf(threadIdx.x * 4, kGateLow * kC * 4);
+        if (tid < kC) {
+            ghi[tid] = gates.loadf(tid * 4, kGateHigh * kC * 4);
+            glo[tid] = gates.loadf(tid * 4, kGateLow * kC * 4);
         }
         // scores, rows: contraction index j or l; columns: tokens i = 16 w ..  Tiles before w: x_i.u_j, after w: x_l.u_i,
         // tile w: both, the latter in diag; x = dy or de
@@ -362,6 +364,14 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
 #pragma unroll
         for (int i = 0; i < 4; ++i) near[i] = f32x4{};
         for (int p0 = 0; p0 < p.P; p0 += PK) {
+            fresh();
+            uint32_t put[PER], token[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int x = tid + i * 2 * kThreads, t = x / (PK / 4), c = 4 * (x % (PK / 4));
+                put[i] = t * LP + c;
+                token[i] = (uint32_t)(t * HP + c);
+            }
             // everything that the block needs of memory, on its way at once
             const uint32_t bytes = (uint32_t)((have - 1) * HP + PK);
             const int64_t o = tok0 * HP + h * p.P + p0;
@@ -380,7 +390,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
                     x4[1][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(eb.r, (int)(token[i] * 2), 0, 0));
                 }
                 u4[i] = ub.load16(token[i] * 4, 0);
-                beta[i] = gates.loadf(threadIdx.x / (PK / 4) * 4, (kGateBeta * kC + i * 2 * kThreads / (PK / 4)) * 4);
+                beta[i] = gates.loadf(tid / (PK / 4) * 4, (kGateBeta * kC + i * 2 * kThreads / (PK / 4)) * 4);
             }
             __syncthreads();
 #pragma unroll
@@ -445,6 +455,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
             }
         }
         __syncthreads();
+        fresh();
         {
             const int i = 16 * w + m;
             const float hi = ghi[i], li = glo[i], by = set == 0 ? p.scale : -1.f;
