@@ -21,22 +21,24 @@ namespace {
 
 // The gradient of the state, from chunk to chunk towards the first: as delta_walk_kernel, 16 or 32 columns a workgroup, the
 // rows split over its waves, every product of fp32 values on operands of all terms.
+template <typename T, int N, int CT> constexpr bool back_lean() { return CT == 2 && N * sizeof(T) <= 256; }
+
 template <typename T, int N, int CT>
-__global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 : 2) delta_back_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
+__global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && !back_lean<T, N, CT>() ? 1 : 2)) delta_back_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
     constexpr int KN = N / M::kK, KC = kC / M::kK, TERMS = M::kTerms, NT = StateRows<N, CT>::NT, kCols = 16 * CT;
     constexpr int LS = N + M::kPad, LC = kC + M::kPad, SA = kCols * LS, CA = kCols * LC;
-    // dS' [column][n]; dY [column][token]; of all terms: scale e^g dY, for this chunk and the next, B dU, -e^g dE; K and Q
-    // [token][n]
-    __shared__ __attribute__((aligned(16))) T sl[TERMS * SA];
-    __shared__ __attribute__((aligned(16))) T yl[CA];
-    extern __shared__ __attribute__((aligned(16))) char more[];
-    T* const wl = reinterpret_cast<T*>(more);
-    T* const rl = wl + 2 * TERMS * CA;
+    constexpr bool LEAN = back_lean<T, N, CT>();
+    // dS' [column][n], and in its place, between its reading and its next writing, K and Q [token][n]; dY [column][token]; of
+    // all terms: scale e^g dY, B dU, -e^g dE
+    extern __shared__ __attribute__((aligned(16))) char back_lds[];
+    T* const sl = reinterpret_cast<T*>(back_lds);
+    T *const kl = sl, *const ql = kl + kC * LS;
+    T* const yl = sl + (TERMS * SA > 2 * kC * LS ? TERMS * SA : 2 * kC * LS);
+    T* const wl = yl + CA;
+    T* const rl = wl + TERMS * CA;
     T* const dl = rl + TERMS * CA;
-    T* const kl = dl + TERMS * CA;
-    T* const ql = kl + kC * LS;
 
     const int64_t unit = xcd_work_index(blockIdx.x, per_xcd, units);
     if (unit < 0) return;
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
     const T *const at_s = sl + m * LS + g * M::kE, *const at_y = yl + m * LC + g * M::kE, *const at_w = wl + m * LC + g * M::kE,
             *const at_r = rl + m * LC + g * M::kE, *const at_d = dl + m * LC + g * M::kE;
     Frag kf[KN], qf[KN], zf[KC][TERMS], pf[KC][TERMS];
-    f32x4 in, out, be, ahead, after[NT][CT];  // ahead: e^g of the chunk whose dY is loaded
+    f32x4 in, out, be, after[NT][CT];
     float all;
     T vv[4][CT], yv[4][CT];
     float ee[4][CT];
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
     const char* pc = static_cast<const char*>(p.scores_t) + (slot * p.H + h) * kMat + w * KC * kStep;
     const int64_t row_at = (slot * p.G + grp) * kCol + w * KN * kStep;
     const char *kc = static_cast<const char*>(p.kr) + row_at, *qc = static_cast<const char*>(p.qr) + row_at;
-    const float *gc = p.gates + (slot * p.H + h) * kGate, *hc = gc;  // hc: of the chunk whose dY is loaded
+    const float* gc = p.gates + (slot * p.H + h) * kGate;
     const float* sc = p.states + ((slot + 1 + s) * p.H + h) * NP + cb * kCols;
     T* dc = static_cast<T*>(p.dstates) + (slot * p.H + h) * NP + cb * kCols;
     const uint32_t own = lane * 16, four = row0 * 4;
@@ -90,14 +92,17 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
     const auto load_rows = [&](int64_t back) {
         kc -= back * (p.G * kCol);
         pc -= back * (p.H * kMat);
-        qc -= back * (p.G * kCol);
-        const Block kr(kc), qr(qc), s(pc);
+        const Block kr(kc), s(pc);
 #pragma unroll
         for (int i = 0; i < KN; ++i) kf[i] = kr.frag<T>(own, i * kStep);
 #pragma unroll
         for (int i = 0; i < KC; ++i)
 #pragma unroll
             for (int u = 0; u < TERMS; ++u) pf[i][u] = s.frag<T>(i < ks0 ? own + ks0 * kStep : own + i * kStep, u * (kC * kC * sizeof(T)));
+    };
+    const auto load_q = [&](int64_t back) {
+        qc -= back * (p.G * kCol);
+        const Block qr(qc);
 #pragma unroll
         for (int i = 0; i < KN; ++i) qf[i] = qr.frag<T>(own, i * kStep);
     };
@@ -133,28 +138,28 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
     };
     const auto load_dy = [&](int64_t back, bool last) {
         yc.base -= back * yc.step;
-        hc -= back * (p.H * kGate);
         const Block yr = yc.block(last);
 #pragma unroll
         for (int e = 0; e < 4; ++e) yr.load<CT>(yat[e], yv[e]);
-        ahead = as_f32x4(Block(hc).load16(four, kGateIn * kC * 4));
     };
-    const auto share_dy = [&](T* to) {
+    const auto share_dy = [&] {
 #pragma unroll
         for (int i = 0; i < CT; ++i) {
             const f32x4 x = {to_f32(yv[0][i]), to_f32(yv[1][i]), to_f32(yv[2][i]), to_f32(yv[3][i])};
             put4<1>(yl + (16 * i + m) * LC + M::place_of(w, g), 0, x);
-            put4<TERMS>(to + (16 * i + m) * LC + M::place_of(w, g), CA, p.scale * ahead * x);
         }
     };
     if (chunks > 0) {
         load_dy(0, true);
         load_rows(0);
-        load_z(0);
-        load_values(0, true);
+        if constexpr (!LEAN) {
+            load_q(0);
+            load_z(0);
+            load_values(0, true);
+            load_after(0);
+        }
         load_gates(0);
-        load_after(0);
-        share_dy(wl + (end & 1) * (TERMS * CA));
+        share_dy();
         load_dy(chunks > 1, chunks == 1);
     }
     for (int64_t c = chunks - 1; c >= 0; --c) {
@@ -181,27 +186,28 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
             for (int t = 0; t < KC; ++t)
                 if (t >= ks0) y[t].template add<TERMS>(d, pf[t]);
         }
+        if constexpr (LEAN) {
+            load_z(c < end);
+            load_q(c < end);
+            load_values(c < end, c == end);
+            load_after(c < end);
+        }
 #pragma unroll
         for (int i = 0; i < CT; ++i) {
             x[i] = p.scale * d[i] + out * a[i];
             put4<TERMS>(rl + (16 * i + m) * LC + M::place_of(w, g), CA, be * x[i]);
         }
+        lds_barrier();  // B dU is there, dS' and dY are free
         // (K's and Q's columns are the state's other operands: by way of LDS)
 #pragma unroll
         for (int t = 0; t < KN; ++t) {
             st16(kl + (16 * w + m) * LS + t * M::kK + g * M::kE, __builtin_bit_cast(uint4, kf[t]));
             st16(ql + (16 * w + m) * LS + t * M::kK + g * M::kE, __builtin_bit_cast(uint4, qf[t]));
         }
-        load_rows(back);
-        lds_barrier();  // B dU is there, dS' and dY are free
-        float dot = 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < CT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dot += st[t][i][e] * after[t][i][e];
-        if (!StateRows<N, CT>::kAll && !rows.own) dot = 0.f;
+        if constexpr (!LEAN) {
+            load_rows(back);
+            load_q(back);
+        }
         f32x4 dv{}, db{};
         const Block dr = oc.block(c == end);
         oc.base -= oc.step;
@@ -216,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
             for (int t = 0; t < KC; ++t)
                 if (t >= ks0) b[t].template add<TERMS>(x, zf[t]);
         }
+        if constexpr (LEAN) load_rows(back);
 #pragma unroll
         for (int i = 0; i < CT; ++i) {
             de[i] = be * x[i];
@@ -226,12 +233,28 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
                 db[e] += x[i][e] * ee[e][i];
             }
         }
-        if (c > 0) share_dy(wl + ((c - 1) & 1) * (TERMS * CA));
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {  // (dY of this lane's own tokens, which it put there)
+            const T* mine = yl + (16 * i + m) * LC + M::place_of(w, g);
+            const f32x4 x = {to_f32(mine[0]), to_f32(mine[1]), to_f32(mine[2]), to_f32(mine[3])};
+            put4<TERMS>(wl + (16 * i + m) * LC + M::place_of(w, g), CA, p.scale * in * x);
+        }
+        if (c > 0) share_dy();
         const float now = all;
-        load_z(back);
-        load_values(back, last);
+        float dot = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dot += st[t][i][e] * after[t][i][e];
+        if (!StateRows<N, CT>::kAll && !rows.own) dot = 0.f;
+        if constexpr (!LEAN) {
+            load_z(back);
+            load_values(back, last);
+            load_after(back);
+        }
         load_gates(back);
-        load_after(back);
         load_dy(c > 1, end == 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -259,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
         for (int k = 0; k < KC; ++k) {
             Operands<T, CT, TERMS> b, y;
             b.read(at_d, k, 16 * LC, CA);
-            y.read(at_w + (c & 1) * (TERMS * CA), k, 16 * LC, CA);
+            y.read(at_w, k, 16 * LC, CA);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -268,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) >= 128 ? 1 
                 y.template add<1>(st[t], &qt);
             }
         }
+        lds_barrier();  // K and Q are free
         rows.template share<TERMS>(st, sl, LS, SA);
     }
     if (p.dinit) rows.store(st, p.dinit + (s * p.H + h) * NP + cb * kCols, p.P);
@@ -277,7 +301,8 @@ template <typename T, int N, int CT>
 int launch_back(const DeltaParams& p, hipStream_t stream) {
     using M = Mat<T>;
     const int64_t units = p.nseq * p.H * (p.P / p.cols), per = (units + 7) / 8;
-    constexpr int lds = (4 * M::kTerms * 16 * CT * (kC + M::kPad) + 2 * kC * (N + M::kPad)) * (int)sizeof(T);
+    constexpr int LS = N + M::kPad, cols = 16 * CT, states = M::kTerms * cols * LS, rows = 2 * kC * LS;
+    constexpr int lds = ((states > rows ? states : rows) + (3 * M::kTerms + 1) * cols * (kC + M::kPad)) * (int)sizeof(T);
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_back_kernel<T, N, CT>), hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
         return -1;
     hipLaunchKernelGGL((delta_back_kernel<T, N, CT>), dim3((unsigned)(8 * per)), dim3(kThreads), lds, stream, p, units, per);

@@ -65,8 +65,12 @@ template <int N, int CT> struct StateRows {
     }
 };
 
+// Whether U has the place of S between its reading and its next writing, for one barrier more: where two workgroups would not
+// fit a CU's LDS otherwise.
+template <typename T, int N, int CT, bool SAVE> constexpr bool walk_shares() { return SAVE && CT == 2 && N == 128 && sizeof(T) == 2; }
+
 template <typename T, int N, int CT, bool SAVE>
-__global__ void __launch_bounds__(kThreads, CT == 2 && (N * sizeof(T) == 512 || (SAVE && N == 128)) ? 1 : 2) delta_walk_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
+__global__ void __launch_bounds__(kThreads, CT == 2 && N * sizeof(T) == 512 ? 1 : 2) delta_walk_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
     constexpr int KN = N / M::kK, KC = kC / M::kK, TERMS = M::kTerms;
@@ -74,12 +78,13 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && (N * sizeof(T) == 512 || 
     constexpr int NT = StateRows<N, CT>::NT, kCols = 16 * CT;
     constexpr int LS = N + M::kPad, LC = kC + M::kPad;
     constexpr int SA = kCols * LS, CA = kCols * LC;  // elements from one term to the next
+    constexpr bool SHARED = walk_shares<T, N, CT, SAVE>();
     extern __shared__ __attribute__((aligned(16))) char walk_lds[];
     T* const sl = reinterpret_cast<T*>(walk_lds);  // S   [column][n]
     T* const rl = sl + TERMS * SA;                 // B R [column][token]
     T* const dl = rl + TERMS * CA;                 // e^(gC - g) U
-    T* const ul = dl + TERMS * CA;                 // U
-    T* const kl = ul + TY * CA;                    // K   [token][n]
+    T* const ul = SHARED ? sl : dl + TERMS * CA;   // U
+    T* const kl = dl + (TERMS + (SHARED ? 0 : TY)) * CA;  // K   [token][n]
 
     const int64_t unit = xcd_work_index(blockIdx.x, per_xcd, units);
     if (unit < 0) return;
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && (N * sizeof(T) == 512 || 
         load_gates(0);
         load_z(0);
         load_values(0, chunks == 1);
-        load_rest(0, chunks == 1);
+        if constexpr (!SHARED) load_rest(0, chunks == 1);
     }
     float* keep = SAVE ? p.states + ((slot0 + s) * p.H + h) * NP + cb * kCols : nullptr;
     for (int64_t c = 0; c < chunks; ++c) {
@@ -235,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && (N * sizeof(T) == 512 || 
             put4<TY>(ul + (16 * i + m) * LC + M::place_of(w, g), CA, u[i]);
             y[i] *= in;
         }
-        load_z(on);
+        // (two workgroups have registers for one of Z and P at a time)
+        if constexpr (SHARED) load_rest(c > 0, !on);
+        else load_z(on);
         lds_barrier();  // U is there, B R is free
         {
             Operands<T, CT, TERMS> b[KC];
@@ -260,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && (N * sizeof(T) == 512 || 
 #pragma unroll
         for (int t = 0; t < KC; ++t) b[t].read(at_u, t, 16 * LC, CA);
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (SHARED) lds_barrier();  // U is free
         rows.template share<TERMS>(st, sl, LS, SA);
 #pragma unroll
         for (int t = 0; t < KC; ++t)
@@ -293,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, CT == 2 && (N * sizeof(T) == 512 || 
             }
             yc.base += yc.step;
         }
-        load_rest(on, last);
+        if constexpr (SHARED) load_z(on);
+        else load_rest(on, last);
     }
     if constexpr (SAVE) rows.store(st, keep, p.P);
     else if (p.final_state) rows.store(st, p.final_state + (s * p.H + h) * NP + cb * kCols, p.P);
@@ -304,7 +313,7 @@ int launch_walk(const DeltaParams& p, hipStream_t stream) {
     using M = Mat<T>;
     const int64_t units = p.nseq * p.H * (p.P / (16 * CT)), per = (units + 7) / 8;
     constexpr int TY = terms_of_y<T>(SAVE), LS = N + M::kPad, LC = kC + M::kPad;
-    constexpr int lds = (16 * CT * (M::kTerms * LS + (2 * M::kTerms + TY) * LC) + kC * LS) * (int)sizeof(T);
+    constexpr int lds = (16 * CT * (M::kTerms * LS + (2 * M::kTerms + (walk_shares<T, N, CT, SAVE>() ? 0 : TY)) * LC) + kC * LS) * (int)sizeof(T);
     const auto kernel = &delta_walk_kernel<T, N, CT, SAVE>;
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess) return -1;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(8 * per)), dim3(kThreads), lds, stream, p, units, per);
