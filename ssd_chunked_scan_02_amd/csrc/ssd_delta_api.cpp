@@ -40,9 +40,11 @@ int strides(const ssd_delta_dims* d, int64_t& q, int64_t& k, int64_t& v) {
 // Columns of a walk's workgroup.  With 32 each load of K, Q, Z and the scores serves twice the columns, with 16 the steps
 // of a chunk are shorter: 16 where its workgroups still have one of the 256 CUs each.  Forward and training step of one
 // sequence of 2048 tokens, us, 16 against 32 columns:
-//     bf16, 64 by 64     128 workgroups of 16 73/292 against 95/363, 256: 83/404 against 102/449, 384: 127/607 against 121/534
-//     bf16, 128 by 128   128: 76/329 against 101/422, 256: 88/459 against 113/512, 384: 116/651 against 121/592
-//     fp32, 128 by 128   128: 123/562 against 197/704, 256: 147/735 against 221/857, 384: 225/1262 against 237/972
+//     bf16, 64 by 64     128 workgroups of 16 73/287 against 94/359, 256: 87/402 against 103/444, 384: 126/603 against 121/525
+//     bf16, 128 by 128   128: 75/307 against 103/403, 256: 89/427 against 115/485, 384: 116/630 against 122/560
+//     fp32, 64 by 64     128: 92/384 against 133/507, 256: 118/526 against 158/639, 384: 185/808 against 177/757
+//     fp32, 128 by 128   128: 124/563 against 197/721, 256: 145/732 against 218/872, 384: 225/1251 against 235/985
+// and of four sequences with 768 and 1024 workgroups of 16, bf16, 128 by 64: 307/1435 against 282/1229, 389/1818 against 339/1480.
 int walk_columns(const ssd_delta_dims* d) { return d->nseq * d->nheads * (d->valuedim / 16) <= 256 ? 16 : 32; }
 
 // Lays the workspace out from `base` (null: only its size is wanted), and returns its bytes.
@@ -72,6 +74,7 @@ size_t lay_out(const ssd_delta_dims* d, bool backward, char* base, ssd::DeltaPar
     p.dot_v = reinterpret_cast<float*>(take(slots * H * blocks * C * 4));
     p.dot_b = reinterpret_cast<float*>(take(slots * H * blocks * C * 4));
     p.dot_s = reinterpret_cast<float*>(take(slots * H * blocks * 4 * 4));
+    p.dot_0 = reinterpret_cast<float*>(take((size_t)d->nseq * H * blocks * 4 * 4));
     return at;
 }
 

@@ -49,6 +49,7 @@ struct DeltaParams {
     float* dot_v;           // dv . v
     float* dot_b;           // x . e
     float* dot_s;           // [slots, H, P / cols][4]: <dstate, state> after each chunk
+    float* dot_0;           // [nseq, H, P / cols][4]: before the first, where there is an init
     int64_t nseq, total, each, slots;
     int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
     int H, G, N, P;
