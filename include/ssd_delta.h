@@ -20,7 +20,8 @@
  * else is dense.  Values: log_a <= 0 (below -160 it is taken as that, a decay of zero in fp32); an infinity or NaN in an
  * input may reach every output of its own sequence (of its own head; through a key or query, of its group), and none
  * of another.  Precision: states, gates, their gradients and all sums fp32; with bf16 inputs products of computed values
- * take them in two bf16 terms, off by 2^-18 at most, but for what only bf16 outputs are made of (one term).
+ * take them in three bf16 terms, which hold an fp32's 24 bits, and what only y is made of in two in the forward pass.
+ * dq and dk of bf16 inputs are sums of products whose operands are rounded to bf16 once (u = beta e: to two terms).
  * dlog_a is a difference of sums over its chunk: its rounding is relative to those, not to itself.
  * Outputs and the workspace must not overlap inputs or each other; a call where one of them is the very pointer of
  * an input or of another output is refused (SSD_ERR_INVALID), but for final_state, which may be init_state itself.

@@ -132,7 +132,7 @@ def test_workspace_bytes():
     assert ssd.ssd_delta_forward_workspace_bytes(_dims()) == forward
     state, blocks = 64 * 96, 96 // 16
     backward = (slots * 4 * 12 * chunk + rows + slots * 4 * 5 * 64 * 4 + (slots + 2) * 4 * state * 4
-                + 100 * 4 * 96 * 4 + slots * 4 * state * 2 + 3 * slots * 4 * blocks * 64 * 4 + slots * 4 * blocks * 16)
+                + 100 * 4 * 96 * 4 + slots * 4 * state * 2 + 3 * slots * 4 * blocks * 64 * 4 + (slots + 2) * 4 * blocks * 16)
     assert ssd.ssd_delta_backward_workspace_bytes(_dims()) == backward
     for bad in (dict(keydim=48), dict(nseq=0), dict(total=0), dict(dtype=7)):
         assert ssd.ssd_delta_forward_workspace_bytes(_dims(**bad)) == 0
