@@ -10,7 +10,8 @@ namespace {
 
 // One token: a workgroup takes 32 columns of one state, a thread four of them in every 32nd row.  Both products with
 // the old state are taken in the one pass that reads it: S_t^T q = a S^T q + (k.q) beta e.  Bound by the state's bytes, read
-// once and written once: 64 sequences, 32 heads of 128 by 128, 52 us, 5.1 TB/s; one sequence 13 us, the host's call.
+// once and written once: 64 sequences, 32 heads of 128 by 128, 52 us, 5.1 TB/s (41 us where its states are still in the last-level cache);
+// one sequence 13 us, the host's call.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepParams p) {
     constexpr int R = N / 32;

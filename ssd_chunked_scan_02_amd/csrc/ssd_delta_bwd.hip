@@ -24,12 +24,12 @@ namespace {
 
 // The gradient of the state, from chunk to chunk towards the first: as delta_walk_kernel, 16 or 32 columns a workgroup, the
 // rows split over its waves, every product of fp32 values on operands of all terms.
-// As there the chain of a chunk bounds it: 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 273 us, 4.3 us a chunk for each of
+// As there the chain of a chunk bounds it: 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 280 us, 4.4 us a chunk for each of
 // two workgroups.
 //
 // Whether a workgroup of 32 columns keeps to half of a CU, 256 registers a lane and 80 KB: it then loads Z, Q, the values
 // and the state in the chunk that takes them, under the products before, and not a chunk ahead.  The shape above, whose 384 workgroups
-// are one and a half times the CUs, 355 us with a CU each and 273 so; 256 workgroups of 128 by 128, four sequences of 2048 tokens,
+// are one and a half times the CUs, 355 us with a CU each and 280 so; 256 workgroups of 128 by 128, four sequences of 2048 tokens,
 // the whole step 671 and 643 us.  (fp32 operands of 128 keys do not fit a half.)
 template <typename T, int N, int CT> constexpr bool back_lean() { return CT == 2 && N * sizeof(T) <= 256; }
 
@@ -308,11 +308,15 @@ __global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && 
         lds_barrier();  // K and Q are free
         rows.template share<TERMS>(st, sl, LS, SA);
     }
-    if (p.dinit) rows.store(st, p.dinit + (s * p.H + h) * NP + cb * kCols, p.P);
+    // (its addresses computed here, not kept in registers through the chunks)
+    int end_lane = threadIdx.x % kWave;
+    asm volatile("" : "+v"(end_lane));
+    const StateRows<N, CT> ends(w, end_lane);
+    if (p.dinit) ends.store(st, p.dinit + (s * p.H + h) * NP + cb * kCols, p.P);
     if (p.init && chunks > 0) {
-        rows.load(after, p.init + (s * p.H + h) * NP + cb * kCols, p.P);
+        ends.load(after, p.init + (s * p.H + h) * NP + cb * kCols, p.P);
         const float dot = state_dot();
-        if (lane == 0) p.dot_0[((s * p.H + h) * blocks + cb) * kWaves + w] = dot;
+        if (end_lane == 0) p.dot_0[((s * p.H + h) * blocks + cb) * kWaves + w] = dot;
     }
 }
 
@@ -334,7 +338,7 @@ int launch_back(const DeltaParams& p, hipStream_t stream) {
 // bf16 their operands have one term, but U, which is in most of their products, has two (errors of 2.9e-3 with one and 2.4e-3 with
 // two, of which 1.7e-3 is the outputs' own rounding; a second term of the state leaves them there).
 //
-// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 275 us for 413 MB read and 201 MB written (2.2 TB/s; 310 us with its addresses
+// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 280 us for 413 MB read and 206 MB written (2.2 TB/s; 310 us with its addresses
 // spilled): a workgroup's three phases wait for each other, and 128 registers a lane, for two workgroups a CU, leave no room to
 // load the next head's rows under them.
 template <typename T, int N, int PK>
@@ -568,13 +572,21 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
             }
         }
     }
+    // by way of LDS, in the place of K and Q: rows of N elements leave whole
+    fresh();
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < CW; ++i) {
-        const int t = 16 * (c0 + i) + m;
-        if (t >= have) continue;
-        const int64_t o = ((tok0 + t) * p.G + grp) * N + n0 + 4 * g;
-        store4(static_cast<T*>(p.dq) + o, dq[i][0], dq[i][1], dq[i][2], dq[i][3]);
-        store4(static_cast<T*>(p.dk) + o, dk[i][0], dk[i][1], dk[i][2], dk[i][3]);
+        const int at = (16 * (c0 + i) + m) * LS + n0 + 4 * g;
+        store4(ql + at, dq[i][0], dq[i][1], dq[i][2], dq[i][3]);
+        store4(kl + at, dk[i][0], dk[i][1], dk[i][2], dk[i][3]);
+    }
+    __syncthreads();
+    for (int f = tid; f < have * (N / M::kE); f += 2 * kThreads) {
+        const int t = f / (N / M::kE), c = f % (N / M::kE) * M::kE;
+        const int64_t o = ((tok0 + t) * p.G + grp) * N + c;
+        st16(static_cast<T*>(p.dq) + o, ld16(ql + t * LS + c));
+        st16(static_cast<T*>(p.dk) + o, ld16(kl + t * LS + c));
     }
 }
 
