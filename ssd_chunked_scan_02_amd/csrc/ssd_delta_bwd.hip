@@ -338,8 +338,8 @@ int launch_back(const DeltaParams& p, hipStream_t stream) {
 // bf16 their operands have one term, but U, which is in most of their products, has two (errors of 2.9e-3 with one and 2.4e-3 with
 // two, of which 1.7e-3 is the outputs' own rounding; a second term of the state leaves them there).
 //
-// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 280 us for 413 MB read and 206 MB written (2.2 TB/s; 310 us with its addresses
-// spilled): a workgroup's three phases wait for each other, and 128 registers a lane, for two workgroups a CU, leave no room to
+// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 245 us for 371 MB read and 227 MB written (2.4 TB/s; 310 us with its addresses
+// spilled and dq and dk stored 32 bytes at a time): a workgroup's three phases wait for each other, and 128 registers a lane, for two workgroups a CU, leave no room to
 // load the next head's rows under them.
 template <typename T, int N, int PK>
 __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_grad_kernel(DeltaParams p) {
