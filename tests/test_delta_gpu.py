@@ -38,6 +38,29 @@ def test_against_the_recurrence(lens, H, G, N, P, state, dtype):
     check(run(cuda(d)), want, d, dtype, "delta %s %s" % (lens, dtype))
 
 
+MANY = [  # lens, H, G, N, P: enough heads and sequences for walks of 32 columns
+    ([130, 1, 0, 77, 64, 3, 200], 12, 4, 128, 64), ([257, 40, 64], 16, 16, 128, 96), ([65, 0, 190], 20, 5, 64, 96), ([129, 128], 40, 8, 32, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("lens,H,G,N,P", MANY, ids=range(len(MANY)))
+def test_many_heads(lens, H, G, N, P, state, dtype):
+    """As above, in a workspace of NaN, twice with the same bits."""
+    d = make(31 + N, lens, H, G, N, P, dtype, state=state)
+    g = cuda(d)
+    assert len(lens) * H * P // 16 > 256
+    got = run(g)
+    check(got, reference(d), d, dtype, "many heads %s %s" % (dtype, (lens, H, G, N, P, state)))
+    args = [g[x] for x in ARGS]
+    size = ssd.ssd_delta_backward_workspace_bytes(ssd.delta._dims(*args, g["cu"], None, 3))
+    again = ssd.ssd_delta_backward(*args, g["dy"], cu_seqlens=g["cu"], init_state=g["init"], dfinal=g["dfinal"], want_dinit=True,
+                                   workspace=torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert all(torch.equal(again[n], got[n]) for n in again)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_batched_layout(dtype):
     """[B, T, ...] without offsets is the packed batch of equal sequences, bit for bit; a scale of the caller's."""
