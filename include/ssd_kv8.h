@@ -48,7 +48,8 @@ int ssd_kv8_append(const ssd_attn_cache* dims, const ssd_kv8_pages* pages, int64
 
 /*
  * ssd_attn_decode over 8-bit pages: the operator of ssd_attn.h on the values that the pages stand for.  Arguments as
- * there; the workspace from its own query.
+ * there; the workspace from its own query.  Scores, softmax and sums are fp32; the weights of a bf16 call hold 16 bits or more in its
+ * products (2^-16 of each), so that y is off by its own rounding.
  */
 size_t ssd_kv8_decode_workspace_bytes(const ssd_attn_cache* dims);
 

@@ -5,9 +5,11 @@
 // (sequence, key head, split) in turn with a running maximum and sum of its own, for up to 16 query heads of the group (the
 // columns of 16x16 MFMA tiles).  Either form of x8 is exact in bf16, so the products go through bf16 MFMAs on x8 itself: the
 // key's scale is a factor of its score, the value's scale one of its weight.  fp32 queries and weights are taken in
-// three bf16 terms, which together hold their 24 bits; bf16 weights are rounded to one (up to 2^-8 of each, as y's own rounding).
-// 64 sequences of up to 8192 keys, 64/8 heads of 128, bf16 queries: 150 us and 4.7 for the join, 606 MB (4.0 TB/s; the same keys
-// in bf16 250 us); 17 sequences of up to 4001 keys, 24 heads of 64, capped, biased by distance: 60 and 4 us.  Two waves a SIMD: four spill (much
+// three bf16 terms, which together hold their 24 bits; the weights of a bf16 call in two (2^-16 of each), so that y is off by its own
+// rounding: a weight has the value's scale in it and the divisor has not, so one term's roundings (up to 2^-8) would not drop out of
+// a sum that one key dominates (errors of 2.4e-3 of y with one term, 1.66e-3 with two).
+// 64 sequences of up to 8192 keys, 64/8 heads of 128, bf16 queries: 152 us and 5 for the join, 606 MB (4.0 TB/s; the same keys
+// in bf16 250 us); 17 sequences of up to 4001 keys, 24 heads of 64, capped, biased by distance: 63 and 5 us.  Two waves a SIMD: four spill (much
 // slower), and neither lanes in another order over a key's bytes nor non-temporal loads change it.
 #include "ssd_attn_join.h"
 #include "ssd_kv8_launch.h"
@@ -64,7 +66,8 @@ template <int TERMS> __device__ __forceinline__ void split(const float (&x)[8], 
 
 template <typename T, int D, int FORM, bool CAP, int BIAS, int NW>
 __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) kv8_decode_kernel(DecodeParams p, Kv8Pages pages, int64_t units) {
-    constexpr int TERMS = terms_of<T>(), NT = D / 32, DT = D / 16;
+    constexpr int TERMS = terms_of<T>(), WTERMS = TERMS > 2 ? TERMS : 2;  // of the queries, of the weights
+    constexpr int NT = D / 32, DT = D / 16;
     constexpr int KB = D >= 64 ? 16 : 8;      // bytes of a key's load: lane group g has KB g .. of each 4 KB
     constexpr int NK = D / (4 * KB);          // loads of a key
     constexpr int CH = D / 16;                // 16-byte chunks of a value
@@ -227,8 +230,8 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) kv8_decode_k
                 l += e;
                 w[4 * n + r] = e * vs[n][r];
             }
-        bf16x8 pf[TERMS];
-        split<TERMS>(w, pf);
+        bf16x8 pf[WTERMS];
+        split<WTERMS>(w, pf);
         const __bf16* at = vt + (4 * g + col / 4) * VS + 4 * (col % 4);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(NW * kWave, NW == kWaves ? 2 : 1) kv8_decode_k
             const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(at + 16 * VS + 16 * d));
             const v8i16 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-            for (int u = TERMS - 1; u >= 0; --u) o[d] = mfma_bf16(__builtin_bit_cast(bf16x8, v), pf[u], o[d]);
+            for (int u = WTERMS - 1; u >= 0; --u) o[d] = mfma_bf16(__builtin_bit_cast(bf16x8, v), pf[u], o[d]);
         }
     }
 
