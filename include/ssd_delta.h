@@ -20,8 +20,8 @@
  * else is dense.  Values: log_a <= 0 (below -160 it is taken as that, a decay of zero in fp32); an infinity or NaN in an
  * input may reach every output of its own sequence (of its own head; through a key or query, of its group), and none
  * of another.  Precision: states, gates, their gradients and all sums fp32; with bf16 inputs products of computed values
- * take them in three bf16 terms, which hold an fp32's 24 bits, and what only y is made of in two in the forward pass.
- * dq and dk of bf16 inputs are sums of products whose operands are rounded to bf16 once (u = beta e: to two terms).
+ * take them in three bf16 terms, which hold an fp32's 24 bits, and what only bf16 outputs are made of (y in the forward pass, dq and
+ * dk) in two: 2^-16 of each operand, so that those outputs are off by their own rounding.
  * dlog_a is a difference of sums over its chunk: its rounding is relative to those, not to itself.
  * Outputs and the workspace must not overlap inputs or each other; a call where one of them is the very pointer of
  * an input or of another output is refused (SSD_ERR_INVALID), but for final_state, which may be init_state itself.
@@ -75,8 +75,9 @@ int ssd_delta_forward(const ssd_delta_dims* dims, const int64_t* cu_seqlens, con
  *   dq, dk       [total, G, N] (summed over the value heads of each group);  dv [total, H, P].
  *   dlog_a, dbeta  [total, H] fp32.
  *   dinit        [nseq, H, N, P] fp32, or NULL to skip it.
- *   workspace    at least ssd_delta_backward_workspace_bytes(dims) bytes; chiefly a state of fp32 and one of `dtype` for
- *                every 64 tokens of a head.
+ *   workspace    at least ssd_delta_backward_workspace_bytes(dims) bytes; chiefly, for every 64 tokens of a head, a state of
+ *                fp32 and one of `dtype` (48 KB at 128 by 64, bf16) and four triangular 64 x 64 operands of all terms (96 KB in bf16, 64 in
+ *                fp32).
  * Four launches.
  */
 size_t ssd_delta_backward_workspace_bytes(const ssd_delta_dims* dims);

@@ -61,6 +61,7 @@ size_t lay_out(const ssd_delta_dims* d, bool backward, char* base, ssd::DeltaPar
     if (d->total == 0 || d->nseq == 0) return 0;
     p.z = take(slots * H * terms * C * C * elem);
     p.scores = take(slots * H * (backward || terms == 1 ? terms : 2) * C * C * elem);
+    const size_t walked = at;  // what the walk down the chunks alone reads
     p.kr = take(slots * G * N * C * elem);
     p.qr = take(slots * G * N * C * elem);
     p.gates = reinterpret_cast<float*>(take(slots * H * ssd::kDeltaGates * C * 4));
@@ -70,6 +71,14 @@ size_t lay_out(const ssd_delta_dims* d, bool backward, char* base, ssd::DeltaPar
     p.states = reinterpret_cast<float*>(take((slots + (size_t)d->nseq) * H * N * P * 4));
     p.wrong = reinterpret_cast<float*>(take((size_t)d->total * H * P * 4));
     p.dstates = take(slots * H * N * P * elem);
+    if (terms > 1) {
+        // in the place of Z and the scores, which the backward walk does not read, where there is room (N P + 64 P of 24576
+        // elements for a chunk and head: all but keys of 128 with values of 160 and more)
+        const size_t states = align16(slots * H * N * P * elem), values = align16((size_t)d->total * H * P * elem);
+        const bool room = states + values <= walked;
+        p.dstates_rest = room ? base : take(states);
+        p.dv_rest = room ? (base ? base + states : nullptr) : take(values);
+    }
     p.dot_y = reinterpret_cast<float*>(take(slots * H * blocks * C * 4));
     p.dot_v = reinterpret_cast<float*>(take(slots * H * blocks * C * 4));
     p.dot_b = reinterpret_cast<float*>(take(slots * H * blocks * C * 4));

@@ -24,8 +24,7 @@ namespace {
 
 // The gradient of the state, from chunk to chunk towards the first: as delta_walk_kernel, 16 or 32 columns a workgroup, the
 // rows split over its waves, every product of fp32 values on operands of all terms.
-// As there the chain of a chunk bounds it: 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 280 us, 4.4 us a chunk for each of
-// two workgroups.
+// 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 309 us (278 without the second terms of dS' and dV that it stores for dq and dk).
 //
 // Whether a workgroup of 32 columns keeps to half of a CU, 256 registers a lane and 80 KB: it then loads Z, Q, the values
 // and the state in the chunk that takes them, under the products before, and not a chunk ahead.  The shape above, whose 384 workgroups
@@ -81,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && 
     Chunks vc = to_last(Chunks(static_cast<const T*>(p.v) + span.lo * p.v_stride + vcol, span.len, p.v_stride, kCols));
     Chunks yc = to_last(Chunks(static_cast<const T*>(p.dy) + span.lo * HP + vcol, span.len, HP, kCols));
     Chunks oc = to_last(Chunks(static_cast<const T*>(p.dv) + span.lo * HP + vcol, span.len, HP, kCols));
+    Chunks lc = to_last(Chunks(static_cast<const T*>(p.dv_rest) + span.lo * HP + vcol, span.len, HP, kCols));  // (bf16)
     Chunks ec = to_last(Chunks(p.wrong + span.lo * HP + vcol, span.len, HP, kCols));
     constexpr int64_t kMat = TERMS * kC * kC * sizeof(T), kCol = N * kC * sizeof(T), kGate = kDeltaGates * kC;
     const int64_t slot = slot0 + kept;
@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && 
     const float* gc = p.gates + (slot * p.H + h) * kGate;
     const float* sc = p.states + ((slot + 1 + s) * p.H + h) * NP + cb * kCols;
     T* dc = static_cast<T*>(p.dstates) + (slot * p.H + h) * NP + cb * kCols;
+    const int64_t rest_of = static_cast<T*>(p.dstates_rest) - static_cast<T*>(p.dstates);  // (bf16)
     const uint32_t own = lane * 16, four = row0 * 4;
     uint32_t vat[4], yat[4];
 #pragma unroll
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && 
         const int64_t back = c > 0, at = (slot0 + c) * p.H + h;
         const bool last = c == end && c == 0;  // of the chunk to load: the present one again, before the first
         rows.store(st, dc, p.P);
+        if constexpr (TERMS > 1) rows.store_rest(st, dc + rest_of, p.P);
         dc -= p.H * NP;
         lds_barrier();  // dS' and dY are there
         f32x4 a[CT] = {}, d[CT] = {}, x[CT];
@@ -235,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && 
         f32x4 dv{}, db{};
         const Block dr = oc.block(c == end);
         oc.base -= oc.step;
+        const Block lr = lc.block(c == end);
+        lc.base -= lc.step;
         f32x4 de[CT];
         {
             Operands<T, CT, TERMS> b[KC];
@@ -279,6 +283,11 @@ __global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && 
 #pragma unroll
             for (int i = 0; i < CT; ++i) x[i] = de[i][e];
             dr.store<CT, T>(yat[e], x);
+            if constexpr (TERMS > 1) {
+#pragma unroll
+                for (int i = 0; i < CT; ++i) x[i] -= (float)(T)x[i];
+                lr.store<CT, T>(yat[e], x);
+            }
             dv[e] = sum16(dv[e]);
             db[e] = sum16(db[e]);
         }
@@ -335,12 +344,12 @@ int launch_back(const DeltaParams& p, hipStream_t stream) {
 // dq and dk of one chunk and key head, summed over its value heads in registers (no atomics), and their dlog a and dbeta.
 // Eight waves.  A wave has 16 rows n of dq^T and dk^T, of all 64 tokens as columns (of fewer where there are fewer
 // rows), and of the score tiles those of 16 tokens, either the ones with dY or the ones with dE.  dq and dk are of the inputs' type: in
-// bf16 their operands have one term, but U, which is in most of their products, has two (errors of 2.9e-3 with one and 2.4e-3 with
-// two, of which 1.7e-3 is the outputs' own rounding; a second term of the state leaves them there).
+// bf16 every computed operand (U, dE, the states, the decayed scores) has two terms, 2^-16 of it, which leaves dq and dk their own
+// rounding (errors of 1.66e-3; 2.4e-3 with one term of all but U).
 //
-// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 245 us for 371 MB read and 227 MB written (2.4 TB/s; 310 us with its addresses
-// spilled and dq and dk stored 32 bytes at a time): a workgroup's three phases wait for each other, and 128 registers a lane, for two workgroups a CU, leave no room to
-// load the next head's rows under them.
+// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 311 us (245 with one term: the other terms are 150 MB more to read, and twice the
+// products).  128 registers a lane, for two workgroups a CU, leave no room for loads ahead: the states' rows asked for before the
+// scores, under which they would come, have 12 registers spilled and take 329 us (64 by 64: 173 us for 165; fp32: no difference).
 template <typename T, int N, int PK>
 __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_grad_kernel(DeltaParams p) {
     using M = Mat<T>;
@@ -348,14 +357,17 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
     constexpr int KC = kC / M::kK, KP = PK / M::kK, NTILES = N / 16, CW = NTILES / 2;  // CW: column tiles of a wave (4, 2, 1)
     constexpr int LP = PK + M::kPad, LC = kC + M::kPad, LS = N + M::kPad;
     constexpr int PER = kC * (PK / 4) / (2 * kThreads), FRAGS = kC * N / M::kE / kWave, ROWS = (FRAGS + 7) / 8;
-    // dY, dE and U (TU terms) of a block of value dimensions [token][p], and in the same place the three score matrices
-    // [token][contraction]; K and Q [token][n]
+    // dY, dE and U (the latter of TU terms) of a block of value dimensions [token][p], and in the same place the three score matrices
+    // [token][contraction] of TU terms; K and Q [token][n].  Keys of 128 leave room for five of six terms beside a second workgroup
+    // on the CU: the last one goes in when the first ones have been read
     constexpr int TU = sizeof(T) == 2 ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) T mem[(2 + TU) * kC * LP > 3 * kC * LC ? (2 + TU) * kC * LP : 3 * kC * LC];
+    constexpr bool LATE = TU == 2 && N == 128;
+    constexpr int kOperands = (1 + 2 * TU) * kC * LP, kScores = (3 * TU - LATE) * kC * LC;
+    __shared__ __attribute__((aligned(16))) T mem[kOperands > kScores ? kOperands : kScores];
     extern __shared__ __attribute__((aligned(16))) char more[];
     __shared__ float ghi[kC], glo[kC];
-    T *const yl = mem, *const el = mem + kC * LP, *const ul = mem + 2 * kC * LP;
-    T *const bq = mem, *const bk = mem + kC * LC, *const bqk = mem + 2 * kC * LC;
+    T *const yl = mem, *const el = mem + kC * LP, *const ul = mem + (1 + TU) * kC * LP;
+    T *const bq = mem, *const bk = mem + TU * kC * LC, *const bqk = mem + 2 * TU * kC * LC;
     T *const kl = reinterpret_cast<T*>(more), *const ql = kl + kC * LS;
 
     const int64_t slot = blockIdx.x / p.G;
@@ -429,7 +441,8 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
             const int64_t o = tok0 * HP + h * p.P + p0;
             const Block yb(static_cast<const T*>(p.dy) + o, bytes * sizeof(T)), eb(static_cast<const T*>(p.dv) + o, bytes * sizeof(T)), ub(p.wrong + o, bytes * 4);
             typedef typename std::conditional<sizeof(T) == 4, uint4, uint2>::type four;  // four elements
-            four x4[2][PER];
+            four x4[1 + TU][PER];
+            const Block rb(static_cast<const T*>(TU == 2 ? p.dv_rest : p.dv) + o, bytes * sizeof(T));
             uint4 u4[PER];
             float beta[PER];
 #pragma unroll
@@ -440,6 +453,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
                 } else {
                     x4[0][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(yb.r, (int)(token[i] * 2), 0, 0));
                     x4[1][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(eb.r, (int)(token[i] * 2), 0, 0));
+                    x4[2][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rb.r, (int)(token[i] * 2), 0, 0));
                 }
                 u4[i] = ub.load16(token[i] * 4, 0);
                 beta[i] = gates.loadf(tid / (PK / 4) * 4, (kGateBeta * kC + i * 2 * kThreads / (PK / 4)) * 4);
@@ -448,66 +462,115 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 *reinterpret_cast<four*>(yl + put[i]) = x4[0][i];
-                *reinterpret_cast<four*>(el + put[i]) = x4[1][i];
+#pragma unroll
+                for (int u = 0; u < TU; ++u) *reinterpret_cast<four*>(el + u * kC * LP + put[i]) = x4[1 + u][i];
                 put4<TU>(ul + put[i], kC * LP, beta[i] * as_f32x4(u4[i]));
             }
-            // (the states' rows: on their way under the scores, in the registers of what has gone to LDS)
-            const Block sb(p.states + ((slot + s) * p.H + h) * (int64_t)N * p.P + p0), db(static_cast<const T*>(p.dstates) + at * (int64_t)N * p.P + p0);
+            const Block sb(p.states + ((slot + s) * p.H + h) * (int64_t)N * p.P + p0);
             const uint32_t sat = (uint32_t)((n0 + m) * p.P + g * M::kE);
-            f32x4 x0[KP][M::kE / 4];
-            Frag f1[KP];
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                f1[k] = db.frag<T>(sat * sizeof(T), k * M::kK * sizeof(T));
-#pragma unroll
-                for (int e = 0; e < M::kE / 4; ++e) x0[k][e] = as_f32x4(sb.load16(sat * 4, (k * M::kK + 4 * e) * 4));
-            }
             __syncthreads();
-            const auto row = [&](const T* x, int tile, int k) { return frag(x + (16 * tile + m) * LP + k * M::kK + g * M::kE); };
-            const T* xl = set == 0 ? yl : el;
+            // term u of a tile's rows
+            const auto row = [&](const T* x, int u, int tile, int k) { return frag(x + u * kC * LP + (16 * tile + m) * LP + k * M::kK + g * M::kE); };
+            const auto scores = [&](const T* xl, auto terms) {
+                constexpr int TX = decltype(terms)::value;
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const Frag xi = row(xl, w, k);
-                Frag ui[TU];
+                for (int k = 0; k < KP; ++k) {
+                    Frag xi[TX], ui[TU];
 #pragma unroll
-                for (int u = 0; u < TU; ++u) ui[u] = row(ul + u * kC * LP, w, k);
+                    for (int u = 0; u < TX; ++u) xi[u] = row(xl, u, w, k);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    // (the tile's own rows: U's where they come before, dY's or dE's where after)
+                    for (int u = 0; u < TU; ++u) ui[u] = row(ul, u, w, k);
 #pragma unroll
-                    for (int u = 0; u < TU; ++u)
-                        near[t] = M::mma(row(t <= w ? ul + u * kC * LP : xl, t, k), t <= w ? xi : ui[u], near[t]);
-                    if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+                    for (int t = 0; t < 4; ++t) {
+                        // (the tile's own rows: U's where they come before, dY's or dE's where after)
+                        const bool up = t <= w;
+                        const T* own = up ? ul : xl;
+                        const Frag x = row(own, 0, t, k);
+                        if constexpr (TU == 2) {
+                            const Frag rest = row(up || TX == 2 ? own + kC * LP : own, 0, t, k);
+                            near[t] = M::mma(rest, up ? xi[0] : ui[TX == 2 ? 0 : 1], near[t]);
+                            if constexpr (TX == 2) near[t] = M::mma(x, up ? xi[1] : ui[1], near[t]);
+                        }
+                        near[t] = M::mma(x, up ? xi[0] : ui[0], near[t]);
+                        if (TU == 2 || t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+                    }
+#pragma unroll
+                    for (int v = TX - 1; v >= 0; --v)
+#pragma unroll
+                        for (int u = TU - 1; u >= 0; --u)
+                            if (u + v < TU) diag = M::mma(xi[v], ui[u], diag);
+                    __builtin_amdgcn_sched_barrier(0);  // (here and below: the operands of one step at a time, in 128 registers)
                 }
-#pragma unroll
-                for (int u = 0; u < TU; ++u) diag = M::mma(xi, ui[u], diag);
-                __builtin_amdgcn_sched_barrier(0);  // (here and below: the operands of one step at a time, in 128 registers)
-            }
+            };
+            if (set == 0) scores(yl, std::integral_constant<int, 1>{});
+            else scores(el, std::integral_constant<int, TU>{});
             // products with the states before and after the chunk
-            Frag f0[KP];
+            f32x4 x0[KP][M::kE / 4];
+            Frag f0[KP][TU], f1[KP][TU];
 #pragma unroll
             for (int k = 0; k < KP; ++k)
 #pragma unroll
-                for (int e = 0; e < M::kE; ++e) f0[k][e] = (T)x0[k][e / 4][e % 4];
+                for (int e = 0; e < M::kE / 4; ++e) x0[k][e] = as_f32x4(sb.load16(sat * 4, (k * M::kK + 4 * e) * 4));
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
+                for (int e = 0; e < M::kE; ++e) {
+                    float rest = x0[k][e / 4][e % 4];
+#pragma unroll
+                    for (int u = 0; u < TU; ++u) {
+                        f0[k][u][e] = (T)rest;
+                        rest -= (float)f0[k][u][e];
+                    }
+                }
 #pragma unroll
             for (int i = 0; i < CW; ++i) {
-                f32x4 a{}, b{}, c{};
+                f32x4 a{}, b{};
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
-                    a = M::mma(f0[k], row(yl, c0 + i, k), a);
-                    b = M::mma(f0[k], row(el, c0 + i, k), b);
+                    const Frag y = row(yl, 0, c0 + i, k);
 #pragma unroll
-                    for (int u = 0; u < TU; ++u) c = M::mma(f1[k], row(ul + u * kC * LP, c0 + i, k), c);
+                    for (int u = TU - 1; u >= 0; --u) a = M::mma(f0[k][u], y, a);
+#pragma unroll
+                    for (int v = TU - 1; v >= 0; --v) {
+                        const Frag x = row(el, v, c0 + i, k);
+#pragma unroll
+                        for (int u = TU - 1; u >= 0; --u)
+                            if (u + v < TU) b = M::mma(f0[k][u], x, b);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                const float in = gates.loadf((16 * c0 + m) * 4, (kGateIn * kC + 16 * i) * 4), out = gates.loadf((16 * c0 + m) * 4, (kGateOut * kC + 16 * i) * 4);
+                const float in = gates.loadf((16 * c0 + m) * 4, (kGateIn * kC + 16 * i) * 4);
                 dq[i] += (p.scale * in) * a;
-                dk[i] += out * c - in * b;
+                dk[i] -= in * b;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int u = 0; u < TU; ++u) {
+                const Block db(static_cast<const T*>(u == 0 ? p.dstates : p.dstates_rest) + at * (int64_t)N * p.P + p0);
+#pragma unroll
+                for (int k = 0; k < KP; ++k) f1[k][u] = db.frag<T>(sat * sizeof(T), k * M::kK * sizeof(T));
+            }
+#pragma unroll
+            for (int i = 0; i < CW; ++i) {
+                f32x4 c{};
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+#pragma unroll
+                    for (int v = TU - 1; v >= 0; --v) {
+                        const Frag x = row(ul, v, c0 + i, k);
+#pragma unroll
+                        for (int u = TU - 1; u >= 0; --u)
+                            if (u + v < TU) c = M::mma(f1[k][u], x, c);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                dk[i] += gates.loadf((16 * c0 + m) * 4, (kGateOut * kC + 16 * i) * 4) * c;
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         __syncthreads();
         fresh();
+        uint2 late[LATE ? 4 : 1];  // the second terms of bqk
         {
             const int i = 16 * w + m;
             const float hi = ghi[i], li = glo[i], by = set == 0 ? p.scale : -1.f;
@@ -524,10 +587,17 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
                 }
                 const int o = i * LC + M::place_of(t, g);
                 if (set == 0) {
-                    put4<1>(bq + o, 0, before);
-                    put4<1>(bqk + o, 0, after);
+                    put4<TU>(bq + o, kC * LC, before);
+                    put4<LATE ? 1 : TU>(bqk + o, kC * LC, after);
+                    if constexpr (LATE) {
+                        float x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = after[e] - (float)(T)after[e];
+                        late[t].x = take2(x[0], x[1]);
+                        late[t].y = take2(x[2], x[3]);
+                    }
                 } else {
-                    put4<1>(bk + o, 0, before + after);
+                    put4<TU>(bk + o, kC * LC, before + after);
                 }
             }
         }
@@ -538,10 +608,30 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
 #pragma unroll
             for (int i = 0; i < CW; ++i) {
                 const int o = (16 * (c0 + i) + m) * LC + k * M::kK + g * M::kE;
-                dq[i] = M::mma(kf, frag(bq + o), dq[i]);
-                dk[i] = M::mma(kf, frag(bk + o), dk[i]);
-                dk[i] = M::mma(qf, frag(bqk + o), dk[i]);
+#pragma unroll
+                for (int u = TU - 1; u >= 0; --u) {
+                    dq[i] = M::mma(kf, frag(bq + u * kC * LC + o), dq[i]);
+                    dk[i] = M::mma(kf, frag(bk + u * kC * LC + o), dk[i]);
+                    if (u == 0 || !LATE) dk[i] = M::mma(qf, frag(bqk + u * kC * LC + o), dk[i]);
+                }
                 __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if constexpr (LATE) {
+            __syncthreads();
+            if (set == 0) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) st8(mem + (16 * w + m) * LC + M::place_of(t, g), late[t]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+                const Frag qf = columns_of(ql, LS, n0, k, m, g);
+#pragma unroll
+                for (int i = 0; i < CW; ++i) {
+                    dk[i] = M::mma(qf, frag(mem + (16 * (c0 + i) + m) * LC + k * M::kK + g * M::kE), dk[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         if (wave == r % 8) {

@@ -1,12 +1,12 @@
 // Device helpers shared by the kernels of the gated delta rule: 16x16 MFMA tiles of either element type, operands split
-// into two bf16 terms, and the chunks of the packed axis.  gfx950 only.
+// into bf16 terms, and the chunks of the packed axis.  gfx950 only.
 //
 // Precision.  bf16 inputs are exact operands of the matrix unit.  What is computed (states, decayed scores, the
 // triangular inverse) is fp32, and a bf16 operand is made of it in three terms, each the rounded rest of those before it,
 // which together hold an fp32's 24 bits; the product of two such operands takes the six MFMAs whose terms' places add up
 // to two at most.  So the states and the fp32 gradients of bf16 inputs are as good as those of fp32 inputs, which go
-// through fp32 MFMAs (at a sixteenth of the bf16 rate).  Where only a bf16 output is made of a product, its operands have
-// two terms, or one where that output's own rounding stays the larger error.
+// through fp32 MFMAs (at a sixteenth of the bf16 rate).  Where only a bf16 output (y, dq, dk) is made of a product, its operands have
+// two terms, 2^-16 of each, which leaves that output its own rounding.
 #pragma once
 
 #include "ssd_common.h"

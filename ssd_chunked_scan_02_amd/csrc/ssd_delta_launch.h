@@ -45,6 +45,8 @@ struct DeltaParams {
     float* states;          // [slots + nseq, H, N, P]: the state before each chunk, and after the last
     float* wrong;           // [total, H, P]: e
     void* dstates;          // [slots, H, N, P]: gradient of the state after each chunk
+    void* dstates_rest;     // bf16: what its rounding leaves, and (below) that of dv, rounded: the second terms of operands
+    void* dv_rest;          // [total, H, P]
     float* dot_y;           // [slots, H, P / cols][64]: dy . y of a workgroup's columns
     float* dot_v;           // dv . v
     float* dot_b;           // x . e

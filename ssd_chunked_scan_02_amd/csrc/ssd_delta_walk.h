@@ -61,6 +61,17 @@ template <int N, int CT> struct StateRows {
                 b.store<CT, T>(at(t, e, P) / (4 / sizeof(T)), x);
             }
     }
+    // what their rounding to bf16 leaves, rounded to bf16
+    __device__ __forceinline__ void store_rest(const f32x4 (&st)[NT][CT], __bf16* to, int P) const {
+        f32x4 rest[NT][CT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rest[t][i][e] = st[t][i][e] - (float)(__bf16)st[t][i][e];
+        store(rest, to, P);
+    }
     // as operands [column][n] in LDS
     template <int TERMS, typename T> __device__ __forceinline__ void share(const f32x4 (&st)[NT][CT], T* sl, int row, int apart) const {
         if (!kAll && !own) return;
