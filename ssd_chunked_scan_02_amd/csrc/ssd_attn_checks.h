@@ -1,4 +1,4 @@
-// Argument checks and launch shapes that the entry points of the attention layer and of its 8-bit cache share (host only).
+// Argument checks that the entry points of the attention layer and of its 8-bit cache share, and how a decode step is split (host only).
 #pragma once
 
 #include <cmath>
@@ -109,16 +109,19 @@ struct DecodeShape {
     int splits, wide;
 };
 constexpr int64_t kWideKeys = 1024, kWideKeysFullLds = 256;
-inline DecodeShape decode_shape(const ssd_attn_cache* d) {
-    const int64_t group = d->nheads / d->nkvheads, units = d->nseq * d->nkvheads * ((group + 15) / 16);
-    const int64_t keys = d->max_pages * d->page_size;
-    const bool full_lds = d->headdim * (d->dtype == SSD_BF16 ? 2 : 4) >= 512;
-    if (keys <= (full_lds && units < 256 ? kWideKeysFullLds : kWideKeys) && units >= 128 && units < 512) return {1, 1};
+inline DecodeShape split_shape(int64_t units, int64_t keys) {
     int64_t n = units > 0 ? (1024 + units - 1) / units : 1;
     const int64_t most = (keys + 127) / 128;
     if (n > most) n = most;
     if (n > 64) n = 64;
     return {n < 1 ? 1 : (int)n, 0};
+}
+inline int64_t decode_units(const ssd_attn_cache* d) { return d->nseq * d->nkvheads * ((d->nheads / d->nkvheads + 15) / 16); }
+inline DecodeShape decode_shape(const ssd_attn_cache* d) {
+    const int64_t units = decode_units(d), keys = d->max_pages * d->page_size;
+    const bool full_lds = d->headdim * (d->dtype == SSD_BF16 ? 2 : 4) >= 512;
+    if (keys <= (full_lds && units < 256 ? kWideKeysFullLds : kWideKeys) && units >= 128 && units < 512) return {1, 1};
+    return split_shape(units, keys);
 }
 
 }  // namespace checks

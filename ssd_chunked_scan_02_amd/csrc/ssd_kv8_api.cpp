@@ -25,12 +25,28 @@ int take_pages(const ssd_attn_cache* d, const ssd_kv8_pages* g, bool needed, ssd
     return SSD_OK;
 }
 
+// As decode_shape, on this kernel's own times.  Its tiles of values are bf16 for either type of the queries (8.7 KB a wave at 128
+// wide), and a cache of 128 keys or fewer, which is not split either way, has too few blocks for eight waves.  Split (with its join)
+// against eight waves, us, 32/8 heads, int8, of 256 and 1000 keys, by workgroups (key heads of all sequences):
+//                    64                   96                   128                  256                   496                   640
+//     bf16  64 wide  7.3/6.3 11.1/12.1    7.4/6.4 12.4/12.1    7.5/6.3 13.4/12.1    8.9/6.5 16.5/13.5     11.1/8.6 25.2/19.9    12.7/12.1 27.4/27.2
+//          128 wide  9.0/8.4 13.4/16.4    9.0/8.5 16.3/17.7    9.0/8.5 19.6/17.7    11.5/8.7 24.5/19.5    17.4/16.6 36.9/34.7   20.3/23.9 40.3/48.6
+//     fp32  64 wide  7.8/6.8 11.7/13.1    7.8/6.9 13.3/13.2    7.8/6.9 15.4/13.2    9.5/7.0 19.4/15.0     12.8/12.1 28.8/27.4   15.1/17.6 31.8/38.6
+//          128 wide  9.7/9.4 14.6/18.5    9.7/9.5 19.8/19.8    9.8/9.5 22.7/19.8    12.5/9.6 29.1/21.6    20.7/19.1 44.5/39.3   24.8/27.4 49.7/55.0
+// 2000 keys: 18.1/21.3 and 25.9/29.4 (bf16, 128 workgroups, 64 and 128 wide); 128 keys: 8.6/11.8 (bf16, 128 wide, 496).  e4m3: the
+// same sides, up to 10% less.
+DecodeShape kv8_shape(const ssd_attn_cache* d) {
+    const int64_t units = decode_units(d), keys = d->max_pages * d->page_size;
+    if (keys > 128 && keys <= kWideKeys && units >= 128 && units < 512) return {1, 1};
+    return split_shape(units, keys);
+}
+
 struct Kv8Workspace {
     size_t o, ml, total;
 };
 Kv8Workspace decode_workspace(const ssd_attn_cache* d) {
     Kv8Workspace w{};
-    const size_t n = (size_t)decode_shape(d).splits, units = (size_t)d->nseq * (size_t)d->nheads;
+    const size_t n = (size_t)kv8_shape(d).splits, units = (size_t)d->nseq * (size_t)d->nheads;
     if (n > 1) {
         w.o = units * n * (size_t)d->headdim * 4;
         w.ml = align16(units * n * 2 * 4);
@@ -101,7 +117,7 @@ int ssd_kv8_decode(const ssd_attn_cache* d, const ssd_kv8_pages* pages, const vo
     if ((rc = take_pages(d, pages, d->nseq > 0, g)) != SSD_OK) return rc;
     if (d->nseq > 0 && (any_null({q, y, seq_lens}) || (d->max_pages > 0 && !block_table))) return SSD_ERR_INVALID;
     if (!all_aligned({q, slopes, table, y, workspace}, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 8)) return SSD_ERR_ALIGN;
-    const DecodeShape shape = decode_shape(d);
+    const DecodeShape shape = kv8_shape(d);
     p.splits = shape.splits;
     p.wide = shape.wide;
     if (d->nseq * d->nheads * p.splits >= ((int64_t)1 << 31)) return SSD_ERR_UNSUPPORTED;

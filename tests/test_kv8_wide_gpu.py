@@ -29,3 +29,15 @@ def test_eight_waves(dtype, form, D, bias, cap, how):
     assert workspace(dtype, form, len(lens), H, Hk, D, page, -(-max(lens) // page) + 1) == 0
     assert workspace(dtype, form, 8, H, Hk, D, page, -(-max(lens) // page) + 1) > 0
     decode_case(dtype, form, D, H, Hk, page, lens, bias=bias, cap=cap, seed=6, **how)
+
+
+@pytest.mark.parametrize("form", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D,lens", [(128, [1024 - 31 * i for i in range(32)]), (64, [129] * 17 + [1000] * 15), (128, [128] * 16 + [3] * 16)])
+def test_eight_waves_of_longer_caches(dtype, form, D, lens):
+    """128 to 511 workgroups are not split up to 1024 keys, of either type and at every width; of 128 keys or fewer they are not for
+    want of keys."""
+    H, Hk, page = 8, 4, 32
+    assert workspace(dtype, form, len(lens), H, Hk, D, page, 1024 // page) == 0
+    assert workspace(dtype, form, len(lens), H, Hk, D, page, 1056 // page) > 0
+    decode_case(dtype, form, D, H, Hk, page, lens, bias="slopes", seed=8)
