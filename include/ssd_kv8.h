@@ -5,8 +5,8 @@
  *
  * Held, for each token and key head, of its key and its value x [D]:
  *
- *     scale = max |x| (1 / L)      fp32, as 1 / L is; L = 127 (SSD_KV8_INT8) or 448 (SSD_KV8_E4M3)
- *     x8    = x / scale            rounded to the nearest value of the type, ties to even; zeros where scale is 0
+ *     scale = max |x| (1 / L)      fp32, as 1 / L is; L = 127 (SSD_KV8_INT8) or 448 (SSD_KV8_E4M3); rounded up where it is subnormal
+ *     x8    = x / scale            rounded to the nearest value of the type, ties to even; zeros where all are
  *
  * so that it stands for scale x8, off by at most scale / 2 (int8), or 2^-4 of the value and scale 2^-10 (e4m3).  A head with an
  * infinity or NaN has a NaN for its scale and reads as NaN.

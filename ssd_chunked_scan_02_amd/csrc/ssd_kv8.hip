@@ -381,7 +381,11 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(AppendParams p, Kv
         for (int off = 1; off < CH; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
         constexpr float kTop = FORM == kE4m3 ? 448.f : 127.f;
         const bool finite = top < 0x7f800000u;
-        const float scale = finite ? __builtin_bit_cast(float, top) * (1.f / kTop) : NAN, by = scale > 0.f ? scale : 1.f;
+        const float largest = __builtin_bit_cast(float, top);
+        float scale = finite ? largest * (1.f / kTop) : NAN;
+        // (a subnormal scale has few bits: it is rounded up, or the largest value would not fit)
+        if (scale < 0x1p-126f && scale * kTop < largest) scale = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, scale) + 1);
+        const float by = scale > 0.f ? scale : 1.f;
         uint32_t out[E / 4];
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
