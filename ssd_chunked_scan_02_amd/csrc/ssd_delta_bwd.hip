@@ -27,13 +27,22 @@ namespace {
 // 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 309 us (278 without the second terms of dS' and dV that it stores for dq and dk).
 //
 // Whether a workgroup of 32 columns keeps to half of a CU, 256 registers a lane and 80 KB: it then loads Z, Q, the values
-// and the state in the chunk that takes them, under the products before, and not a chunk ahead.  The shape above, whose 384 workgroups
-// are one and a half times the CUs, 355 us with a CU each and 280 so; 256 workgroups of 128 by 128, four sequences of 2048 tokens,
-// the whole step 671 and 643 us.  (fp32 operands of 128 keys do not fit a half.)
+// and the state in the chunk that takes them, under the products before, and not a chunk ahead.  With a CU each and so, us, 64 values a head:
+//     workgroups (sequences)     256 (4 x 2048)    384 (8 x 2048)    1024 (16 x 1024)
+//     bf16, keys of 32           189 151           264 216           285 237
+//                   64           165 160           296 245           329 271
+//                  128           189 186           364 305           (256: 128 values)
+//     fp32, keys of 32           174 167           249 232           284 265
+//                   64           189 176           348 266           381 308
+// (fp32 operands of 128 keys do not fit a half.)
 template <typename T, int N, int CT> constexpr bool back_lean() { return CT == 2 && N * sizeof(T) <= 256; }
+// Whether a workgroup may take all of a CU's registers: for fp32 keys of 128, which need more than half and have the CU for themselves
+// anyway, with 16 columns as 256 workgroups at most, with 32 by their LDS (four sequences of 2048 tokens, 16 heads of 128 by 64: 177 us; within
+// half, 16 registers spilled, 228).
+template <typename T, int N> constexpr bool back_alone() { return N * sizeof(T) > 256; }
 
 template <typename T, int N, int CT>
-__global__ void __launch_bounds__(kThreads, (CT == 2 && N * sizeof(T) >= 128 && !back_lean<T, N, CT>() ? 1 : 2)) delta_back_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
+__global__ void __launch_bounds__(kThreads, (back_alone<T, N>() ? 1 : 2)) delta_back_kernel(DeltaParams p, int64_t units, int64_t per_xcd) {
     using M = Mat<T>;
     using Frag = typename M::Frag;
     constexpr int KN = N / M::kK, KC = kC / M::kK, TERMS = M::kTerms, NT = StateRows<N, CT>::NT, kCols = 16 * CT;
@@ -654,11 +663,13 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
                 before += __shfl_xor(before, off, kWave);
             }
             const double missing = before - all - __shfl(dg, 0, kWave);
+            int rows = have;
+            asm volatile("" : "+v"(rows));  // (widened here, not kept in registers through the heads)
             if (lane < have) {
                 const int64_t o = (tok0 + lane) * p.H + h;
                 p.dbeta[o] = (float)db;
                 // (a decay of zero passes nothing on; the sums would leave their rounding)
-                p.dlog_a[o] = expf(p.log_a[o]) == 0.f ? 0.f : (float)(dg + all + missing * (1.0 - (double)lane / have));
+                p.dlog_a[o] = expf(p.log_a[o]) == 0.f ? 0.f : (float)(dg + all + missing * (1.0 - (double)lane / rows));
             }
         }
     }

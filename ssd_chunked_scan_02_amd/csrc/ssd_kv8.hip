@@ -9,7 +9,10 @@
 // rounding: a weight has the value's scale in it and the divisor has not, so one term's roundings (up to 2^-8) would not drop out of
 // a sum that one key dominates (errors of 2.4e-3 of y with one term, 1.66e-3 with two).
 // 64 sequences of up to 8192 keys, 64/8 heads of 128, bf16 queries: 152 us and 5 for the join, 606 MB (4.0 TB/s; the same keys
-// in bf16 250 us); 17 sequences of up to 4001 keys, 24 heads of 64, capped, biased by distance: 63 and 5 us.  Two waves a SIMD: four spill (much
+// in bf16 250 us); 17 sequences of up to 4001 keys, 24 heads of 64, capped, biased by distance: 63 and 5 us.
+// Of both types and forms, us, 64 sequences to 8192 keys, 64/8 heads of 32, 64, 128 (172, 326, 632 MB), and 17 sequences, 24 heads of 64, capped:
+//     bf16  int8  82 111 171  62    e4m3  72 106 161  47         fp32  int8  92 132 217  75    e4m3  83 126 199  60
+// fp32 queries' three terms are 48 registers at 128 wide; with int8's widening all but two of those kernels spill 19 to 27 of 256.  Two waves a SIMD: four spill (much
 // slower), and neither lanes in another order over a key's bytes nor non-temporal loads change it.
 #include "ssd_attn_join.h"
 #include "ssd_kv8_launch.h"
