@@ -6,7 +6,8 @@
  *
  *     (a, b) -> m (a cos t - b sin t, b cos t + a sin t),   t = p inv_freq[r]
  *
- * with m the magnitude of a context scaled beyond the one trained on (1 without).  Pairs are elements (r, r + rot_pairs), or with
+ * with m the magnitude of a context scaled beyond the one trained on (1 without; the appends to a cache have none: where all of a
+ * head is rotated take m^2 into the attention's scale, else rotate here and append without frequencies).  Pairs are elements (r, r + rot_pairs), or with
  * `interleaved` (2 r, 2 r + 1); elements from 2 rot_pairs on are copied.  With `inverse` the angle is -t: the gradient of
  * the rotation, taken of the gradients of its outputs.  Angles are reduced in fp64, so that far positions keep theirs.
  */

@@ -40,11 +40,11 @@ int strides(const ssd_delta_dims* d, int64_t& q, int64_t& k, int64_t& v) {
 // Columns of a walk's workgroup.  With 32 each load of K, Q, Z and the scores serves twice the columns, with 16 the steps
 // of a chunk are shorter: 16 where its workgroups still have one of the 256 CUs each.  Forward and training step of one
 // sequence of 2048 tokens, us, 16 against 32 columns:
-//     bf16, 64 by 64     128 workgroups of 16 73/287 against 94/359, 256: 87/402 against 103/444, 384: 126/603 against 121/525
-//     bf16, 128 by 128   128: 75/307 against 103/403, 256: 89/427 against 115/485, 384: 116/630 against 122/560
-//     fp32, 64 by 64     128: 92/384 against 133/507, 256: 118/526 against 158/639, 384: 185/808 against 177/757
-//     fp32, 128 by 128   128: 124/563 against 197/721, 256: 145/732 against 218/872, 384: 225/1251 against 235/985
-// and of four sequences with 768 and 1024 workgroups of 16, bf16, 128 by 64: 307/1435 against 282/1229, 389/1818 against 339/1480.
+//     bf16, 64 by 64     128 workgroups of 16 72/287 against 91/359, 256: 86/419 against 101/462, 384: 133/639 against 120/553
+//     bf16, 128 by 128   128: 78/316 against 102/426, 256: 94/446 against 111/522, 384: 125/669 against 118/597
+//     fp32, 64 by 64     128: 97/379 against 135/501, 256: 123/525 against 156/638, 384: 192/812 against 176/764
+//     fp32, 128 by 128   128: 127/495 against 199/723, 256: 151/654 against 217/872, 384: 234/1077 against 233/993
+// and of four sequences with 768 and 1024 workgroups of 16, bf16, 128 by 64: 314/1447 against 283/1294, 395/1871 against 337/1570.
 int walk_columns(const ssd_delta_dims* d) { return d->nseq * d->nheads * (d->valuedim / 16) <= 256 ? 16 : 32; }
 
 // Lays the workspace out from `base` (null: only its size is wanted), and returns its bytes.

@@ -24,7 +24,8 @@ namespace {
 
 // The gradient of the state, from chunk to chunk towards the first: as delta_walk_kernel, 16 or 32 columns a workgroup, the
 // rows split over its waves, every product of fp32 values on operands of all terms.
-// 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 309 us (278 without the second terms of dS' and dV that it stores for dq and dk).
+// Bound as there by a chunk's chain and by bytes: 8 x 2048 tokens, 24 heads of 128 by 64, bf16, 309 us, 856 MB read and 317 written (3.8 TB/s;
+// 278 us without the second terms of dS' and dV that it stores for dq and dk).
 //
 // Whether a workgroup of 32 columns keeps to half of a CU, 256 registers a lane and 80 KB: it then loads Z, Q, the values
 // and the state in the chunk that takes them, under the products before, and not a chunk ahead.  With a CU each and so, us, 64 values a head:
@@ -356,8 +357,8 @@ int launch_back(const DeltaParams& p, hipStream_t stream) {
 // bf16 every computed operand (U, dE, the states, the decayed scores) has two terms, 2^-16 of it, which leaves dq and dk their own
 // rounding (errors of 1.66e-3; 2.4e-3 with one term of all but U).
 //
-// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 311 us (245 with one term: the other terms are 150 MB more to read, and twice the
-// products).  128 registers a lane, for two workgroups a CU, leave no room for loads ahead: the states' rows asked for before the
+// 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 309 us, 893 MB read and 227 written (3.6 TB/s): bytes, most of them the fp32 states, e and
+// the two-term operands that the passes before made (245 us and 150 MB less to read with one term).  128 registers a lane, for two workgroups a CU, leave no room for loads ahead: the states' rows asked for before the
 // scores, under which they would come, have 12 registers spilled and take 329 us (64 by 64: 173 us for 165; fp32: no difference).
 template <typename T, int N, int PK>
 __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_grad_kernel(DeltaParams p) {

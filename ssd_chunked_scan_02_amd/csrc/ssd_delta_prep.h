@@ -8,9 +8,10 @@
 // g is kept in two fp32 parts, so that differences of far sums keep their bits; decays below e^-160 are taken as that,
 // which is zero in fp32 in every product.
 //
-// Bound by what it writes: Z in three terms and the scores in two are 40 KB a chunk and value head in bf16, 72 KB more with
-// the backward pass's (three terms of the scores, and both transposed); the rows of K and Q once more.  8 x 2048 tokens, 24 heads of
-// 128 by 64, bf16: 117 us for 398 MB, 152 us for 662 MB (4.4 TB/s); 16384 tokens, 32/16 heads of 128 by 128: 112 us.  All chunks
+// Bound by bytes, most of them written: Z in three terms and the scores in two are 30 KB a chunk and value head in bf16, and 72 KB in the
+// backward pass (three terms of the scores, and both transposed), in places of 40 and 96 with the steps that are zero throughout; the
+// rows of K and Q once more.  8 x 2048 tokens, 24 heads of 128 by 64, bf16: 113 us, 227 MB read and 398 written (5.5 TB/s); in the backward
+// pass 154 us, 227 and 662 MB (5.8 TB/s); 16384 tokens, 32/16 heads of 128 by 128: 113 us, 564 MB.  All chunks
 // at once here leaves the walks a chain without the substitution; a walk that made its own Z would do so in each of its
 // workgroups (4 to 16 of a head).
 #pragma once

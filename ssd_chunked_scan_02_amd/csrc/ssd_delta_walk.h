@@ -12,8 +12,9 @@
 // Bound by the chain of a chunk: three barriers, two products of each kind after another and the splitting into
 // terms in between, on one or two waves a SIMD, with the operands' way through the CU's L1 next (77 KB a chunk at 128 keys).  16384
 // tokens, 32/16 heads of 128 by 128, bf16: 256 chunks in 551 us, 2.15 us each (with its loads left out 1.45: the loads are
-// half hidden); 8 x 2048 tokens, 24 heads of 128 by 64, two workgroups on every other CU: 168 us, and 253 us with SAVE, which
-// writes 304 MB (300 us with one workgroup a CU).
+// half hidden); 8 x 2048 tokens, 24 heads of 128 by 64, two workgroups on every other CU: 167 us, 494 MB read and 54 written (3.3 TB/s), and
+// 255 us with SAVE, 568 and 311 MB (3.4 TB/s; 300 us with one workgroup a CU).  There the bytes, most of them operands of several terms
+// made for the walks, are two thirds of the time at the rate of a copy.
 //
 // SAVE (the backward pass's run of it): keeps the state before every chunk and after the last, e, and dy . y per token.
 #pragma once

@@ -12,8 +12,8 @@
 // in bf16 250 us); 17 sequences of up to 4001 keys, 24 heads of 64, capped, biased by distance: 63 and 5 us.
 // Of both types and forms, us, 64 sequences to 8192 keys, 64/8 heads of 32, 64, 128 (172, 326, 632 MB), and 17 sequences, 24 heads of 64, capped:
 //     bf16  int8  82 111 171  62    e4m3  72 106 161  47         fp32  int8  92 132 217  75    e4m3  83 126 199  60
-// fp32 queries' three terms are 48 registers at 128 wide; with int8's widening all but two of those kernels spill 19 to 27 of 256.  Two waves a SIMD: four spill (much
-// slower), and neither lanes in another order over a key's bytes nor non-temporal loads change it.
+// fp32 queries' three terms are 48 registers at 128 wide; with int8's widening all but two of those kernels spill 19 to 27 of 256.
+// Two waves a SIMD: four spill (much slower), and neither lanes in another order over a key's bytes nor non-temporal loads change it.
 #include "ssd_attn_join.h"
 #include "ssd_kv8_launch.h"
 #include "ssd_rotary_common.h"

@@ -72,7 +72,8 @@ def ssd_rotary_frequencies(dim: int, base: float = 10000.0, factor: float = 1.0,
     how="linear": every frequency over ``factor`` (positions interpolated).  "base": a larger base, so that the
     slowest pair's frequency is over ``factor`` and the fastest's unchanged.  "parts": by how often a pair turns in
     ``trained`` positions: ``fast`` times and more unchanged, ``slow`` times and less over ``factor``, in between a
-    straight mixture of the two; the magnitude is then 0.1 ln(factor) + 1."""
+    mixture of the two that is straight in the pair's turns; the magnitude is then 0.1 ln(factor) + 1.  (Models trained with a
+    mixture straight in the pair's index, or with borders rounded to whole pairs, have other angles: give `ssd_rotate` theirs.)"""
     if dim < 2 or dim % 2 != 0:
         raise ValueError("dim must be even and at least 2, got %d" % dim)
     if not (base > 1.0 and factor >= 1.0):
