@@ -358,8 +358,9 @@ int launch_back(const DeltaParams& p, hipStream_t stream) {
 // rounding (errors of 1.66e-3; 2.4e-3 with one term of all but U).
 //
 // 8 x 2048 tokens, 24 heads of 128 by 64, bf16: 309 us, 893 MB read and 227 written (3.6 TB/s): bytes, most of them the fp32 states, e and
-// the two-term operands that the passes before made (245 us and 150 MB less to read with one term).  128 registers a lane, for two workgroups a CU, leave no room for loads ahead: the states' rows asked for before the
-// scores, under which they would come, have 12 registers spilled and take 329 us (64 by 64: 173 us for 165; fp32: no difference).
+// the two-term operands that the passes before made (245 us and 150 MB less to read with one term).  128 registers a lane, for two workgroups a CU, leave
+// bf16 no room for loads ahead: the states' rows asked for before the scores, under which they come in fp32 (901 tokens, 6/2 heads of 64 by 32:
+// 34.5 us for 37), have 12 registers spilled and take 329 us (64 by 64: 173 us for 165).
 template <typename T, int N, int PK>
 __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_grad_kernel(DeltaParams p) {
     using M = Mat<T>;
@@ -478,6 +479,26 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
             }
             const Block sb(p.states + ((slot + s) * p.H + h) * (int64_t)N * p.P + p0);
             const uint32_t sat = (uint32_t)((n0 + m) * p.P + g * M::kE);
+            f32x4 x0[KP][M::kE / 4];
+            Frag f0[KP][TU], f1[KP][TU];
+            const auto load_before = [&] {
+#pragma unroll
+                for (int k = 0; k < KP; ++k)
+#pragma unroll
+                    for (int e = 0; e < M::kE / 4; ++e) x0[k][e] = as_f32x4(sb.load16(sat * 4, (k * M::kK + 4 * e) * 4));
+            };
+            const auto load_after = [&] {
+#pragma unroll
+                for (int u = 0; u < TU; ++u) {
+                    const Block db(static_cast<const T*>(u == 0 ? p.dstates : p.dstates_rest) + at * (int64_t)N * p.P + p0);
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) f1[k][u] = db.frag<T>(sat * sizeof(T), k * M::kK * sizeof(T));
+                }
+            };
+            if constexpr (TU == 1) {
+                load_before();
+                load_after();
+            }
             __syncthreads();
             // term u of a tile's rows
             const auto row = [&](const T* x, int u, int tile, int k) { return frag(x + u * kC * LP + (16 * tile + m) * LP + k * M::kK + g * M::kE); };
@@ -512,15 +533,11 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
                     __builtin_amdgcn_sched_barrier(0);  // (here and below: the operands of one step at a time, in 128 registers)
                 }
             };
-            if (set == 0) scores(yl, std::integral_constant<int, 1>{});
+            if constexpr (TU == 1) scores(set == 0 ? yl : el, std::integral_constant<int, 1>{});
+            else if (set == 0) scores(yl, std::integral_constant<int, 1>{});
             else scores(el, std::integral_constant<int, TU>{});
             // products with the states before and after the chunk
-            f32x4 x0[KP][M::kE / 4];
-            Frag f0[KP][TU], f1[KP][TU];
-#pragma unroll
-            for (int k = 0; k < KP; ++k)
-#pragma unroll
-                for (int e = 0; e < M::kE / 4; ++e) x0[k][e] = as_f32x4(sb.load16(sat * 4, (k * M::kK + 4 * e) * 4));
+            if constexpr (TU > 1) load_before();
 #pragma unroll
             for (int k = 0; k < KP; ++k)
 #pragma unroll
@@ -554,12 +571,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2) delta_gr
                 dk[i] -= in * b;
                 __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int u = 0; u < TU; ++u) {
-                const Block db(static_cast<const T*>(u == 0 ? p.dstates : p.dstates_rest) + at * (int64_t)N * p.P + p0);
-#pragma unroll
-                for (int k = 0; k < KP; ++k) f1[k][u] = db.frag<T>(sat * sizeof(T), k * M::kK * sizeof(T));
-            }
+            if constexpr (TU > 1) load_after();
 #pragma unroll
             for (int i = 0; i < CW; ++i) {
                 f32x4 c{};
